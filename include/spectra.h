@@ -13,7 +13,9 @@
  * fused into the kernels' register pipelines).  Around the matvec: the
  * packing steps, a compacted form of the bulk, rows of a packed table
  * gathered as embeddings, the Group-32 4-bit KV cache with decode attention
- * over it, and the self-contained container the layers are stored in.
+ * over it, its paged form for batches of sequences (append, attention,
+ * eviction), the token choice from the LM head's logits, and the
+ * self-contained container the layers are stored in.
  *
  * Conventions shared by every entry point:
  *   - All pointers named *_dev or documented as "device" are CUDA device
@@ -445,13 +447,16 @@ SPECTRA_API spectra_status spectra_embed_rows(const spectra_layer *table, const 
  * for the asynchronous weight copies are bounded: a wait that gives up
  * raises a per-device flag instead of hanging, and the outputs of that
  * launch are invalid.  The embedding gather raises its own flag for an id
- * outside the table (or an outlier index outside [0, k)), and the KV append
- * for a non-finite value or an FP16 scale overflow.  Returns, for what
+ * outside the table (or an outlier index outside [0, k)), the KV appends
+ * for a non-finite value or an FP16 scale overflow, the paged operators for a
+ * slot, page, length or row range out of bounds, and the sampler for a NaN
+ * logit or a row with nothing to choose.  Returns, for what
  * happened since the last call (and clears every flag):
  * SPECTRA_ERR_INTERNAL if a wait gave up, else SPECTRA_ERR_INVALID_ARG if the
- * gather saw a bad id, else SPECTRA_ERR_NONFINITE from the KV append, else
- * SPECTRA_ERR_RANGE from the KV append (a scale overflowing FP16) or from the
- * tensor-core matmul (an FP16 operand out of range), else SPECTRA_OK.
+ * gather saw a bad id, a paged operator a value out of bounds or the sampler
+ * an empty row, else SPECTRA_ERR_NONFINITE from a KV append or the sampler,
+ * else SPECTRA_ERR_RANGE from a KV append (a scale overflowing FP16) or from
+ * the tensor-core matmul (an FP16 operand out of range), else SPECTRA_OK.
  * Synchronous on `stream`.
  */
 SPECTRA_API spectra_status spectra_device_status(void *stream);
@@ -537,6 +542,203 @@ SPECTRA_API spectra_status spectra_attention_decode(const spectra_kv *k, const s
                                                     int32_t length, float scale, float *out,
                                                     void *workspace, size_t workspace_bytes,
                                                     void *stream);
+
+/*
+ * Paged Group-32 4-bit KV pool: one pair of K and V caches that many
+ * sequences share (abstract: microscaled Group-32 4-bit key-value caching).
+ * The pool is n_pages pages of page_size positions (a power of two, 16 to
+ * 1024) of every KV head; a sequence is a list of page ids and a length, both
+ * kept by the caller.  Codec as spectra_kv (spectra_pack's quantiser per token
+ * and head; head_dim D a multiple of 32, at most 256).  Layout, G = D/32,
+ * token slot ts = page*page_size + r (r the position in the page), slot =
+ * (page*n_heads + head)*page_size + r:
+ *   k_codes: u32 word slot*4G + w*G + g, nibble j = code of channel
+ *            32g + 8w + j;
+ *   v_codes: u16 word slot*8G + e*G + g, nibble j = code of channel
+ *            32g + 4e + j;
+ *   k_scales, v_scales: FP16 bits, element slot*G + g;
+ *   k_zeros, v_zeros: u32 word slot, nibble g;
+ *   mass:    float slot, the entry's accumulated attention weight (NULL in a
+ *            pool that keeps none).
+ * (A word holds neighbouring groups' codes next to each other, so that a
+ * thread of the attention kernel reads what it multiplies with one load.)
+ */
+typedef struct {
+    int32_t n_heads;     /* KV heads */
+    int32_t head_dim;    /* D */
+    int32_t page_size;   /* positions per page */
+    int32_t n_pages;
+    uint8_t *k_codes;    /* device, n_pages*page_size*n_heads*D/2 bytes */
+    uint16_t *k_scales;  /* device, n_pages*page_size*n_heads*D/32 */
+    uint32_t *k_zeros;   /* device, n_pages*page_size*n_heads */
+    uint8_t *v_codes;
+    uint16_t *v_scales;
+    uint32_t *v_zeros;
+    float *mass;         /* device, n_pages*page_size*n_heads, or NULL */
+} spectra_kv_pool;
+
+/* Byte sizes of a pool's buffers (codes, scales and zeros for K and for V
+ * each; host only, no CUDA call).  n_pages*page_size must be under 2^31. */
+SPECTRA_API spectra_status spectra_kv_pool_sizes(int32_t n_heads, int32_t head_dim, int32_t page_size,
+                                                 int32_t n_pages, size_t *codes_bytes,
+                                                 size_t *scales_bytes, size_t *zeros_bytes,
+                                                 size_t *mass_bytes);
+
+/*
+ * Quantise n_tok tokens' K and V vectors into the pool, one launch:
+ *   k, v      device, BF16 bits; token i's heads at k + i*k_stride, each
+ *             [n_heads][head_dim] contiguous (strides in elements, multiples
+ *             of 8, at least n_heads*head_dim: slices of a fused projection's
+ *             output serve as they are)
+ *   slots     device int32 [n_tok]: each token's slot page*page_size + r; a
+ *             negative one skips the token (padding).  The slots of one call
+ *             are distinct; two tokens given the same one leave a mixture of
+ *             both there
+ * Bit-identical to the oracle's quantiser.  The slot's mass starts at 0.  A
+ * group holding a NaN or infinity, or whose scale overflows FP16, is stored
+ * as zeros and reported by spectra_device_status (NONFINITE, RANGE), and so
+ * is a slot past the pool, which is skipped (INVALID_ARG).  n_tok == 0
+ * returns SPECTRA_OK without touching CUDA.  Asynchronous, allocates nothing,
+ * graph-capturable.  Errors: INVALID_ARG, SHAPE, ALIGN, UNSUPPORTED, CUDA.
+ */
+SPECTRA_API spectra_status spectra_kv_pool_append(const spectra_kv_pool *pool, const uint16_t *k,
+                                                  const uint16_t *v, int32_t n_tok, int64_t k_stride,
+                                                  int64_t v_stride, const int32_t *slots, void *stream);
+
+/*
+ * Read token slots back, dequantised (x_hat = (c - z) * s, exact in FP32,
+ * rounded once to nearest even for BF16):
+ *   slots         device int32 [n]; a negative one gives a zero row, one past
+ *                 the pool too, with INVALID_ARG from spectra_device_status
+ *   k_out, v_out  device [n][n_heads][head_dim] of out_dtype; one may be NULL
+ * n == 0 returns SPECTRA_OK without touching CUDA.  Asynchronous, allocates
+ * nothing.  Errors: INVALID_ARG, SHAPE, ALIGN, UNSUPPORTED, CUDA.
+ */
+SPECTRA_API spectra_status spectra_kv_pool_read(const spectra_kv_pool *pool, const int32_t *slots,
+                                                int32_t n, void *k_out, void *v_out,
+                                                spectra_dtype out_dtype, void *stream);
+
+/* The queries of one spectra_attention_paged call. */
+typedef struct {
+    const int32_t *pages;    /* device [n_seq][max_pages]: page ids in order of position */
+    const int32_t *lengths;  /* device [n_seq]: cached positions, the new tokens' included */
+    const int32_t *q_start;  /* device [n_seq + 1], nondecreasing: sequence b's new tokens are
+                                the rows q_start[b] .. q_start[b+1]-1; NULL: row b alone */
+    int32_t n_seq;
+    int32_t max_pages;       /* page ids per row of pages */
+    int32_t n_rows;          /* rows of q */
+    int32_t max_q;           /* at least every sequence's number of rows */
+    int32_t n_q_heads;       /* a multiple of the pool's n_heads, at most 64 times it */
+    int32_t window;          /* 0: none */
+    float scale;
+    float softcap;           /* 0: none */
+    const uint16_t *q;       /* device, BF16 bits [n_rows][n_q_heads][head_dim] */
+    const float *slopes;     /* device [n_q_heads], or NULL */
+    void *out;               /* device [n_rows][n_q_heads][head_dim] of out_dtype */
+    spectra_dtype out_dtype;
+    int32_t update_mass;     /* nonzero: add the weights to the pool's mass */
+    float *lse;              /* device [n_rows][n_q_heads], or NULL */
+} spectra_paged_query;
+
+/*
+ * Attention of a batch of sequences over the pool, for one or more of each
+ * sequence's newest tokens.  Row j (of m) of a sequence of length n stands at
+ * position pos = n - m + j and sees the positions t with 0 <= pos - t, and
+ * pos - t < window if there is one; query head i reads KV head h = i / (n_q_heads /
+ * n_heads):
+ *   s_t = f(scale * sum_d q[d] * k_hat[t][d]) - slopes[i] * (pos - t),
+ *   f(x) = softcap * tanh(x / softcap) (f(x) = x without a cap),
+ *   p = softmax(s), out[d] = sum_t p_t * v_hat[t][d], lse = log sum_t exp(s_t),
+ *   mass[t of head h] += sum over the rows and the group's query heads of p_t.
+ * A row that sees nothing (an empty sequence, or pos < 0) gets zeros and lse
+ * = -infinity.  Rows of q outside every sequence are neither read nor
+ * written.  Positions and distances count cached entries: after an eviction
+ * they count the entries that are left.
+ *   workspace  device, 16-byte aligned, >= the stated size; its contents need
+ *              not be kept, and calls that run in stream order may share it
+ * FP32 scores, softmax and sums; the products of the 4-bit codes with q and
+ * with the weights run on the tensor cores with FP32 accumulation.  Out of
+ * bounds values are reported by spectra_device_status as INVALID_ARG and
+ * touch nothing: a page id outside the pool hides its positions, a length
+ * outside [0, max_pages*page_size] counts as 0, and a sequence whose rows lie
+ * outside [0, n_rows) or number more than max_q has its rows left as they
+ * were.  Deterministic, asynchronous, allocates nothing, graph-capturable
+ * (lengths, pages and q_start are read on the device).  n_seq == 0 or n_rows
+ * == 0 returns SPECTRA_OK without touching CUDA.
+ * Errors: INVALID_ARG (update_mass without a mass buffer among them), SHAPE,
+ * ALIGN, BUFFER_TOO_SMALL, UNSUPPORTED, CUDA.
+ */
+/* Workspace bytes for a pool's geometry and the queries' n_rows and
+ * n_q_heads; 0 for invalid arguments.  Host only. */
+SPECTRA_API size_t spectra_attention_paged_workspace_size(const spectra_kv_pool *pool, int32_t n_rows,
+                                                          int32_t n_q_heads);
+SPECTRA_API spectra_status spectra_attention_paged(const spectra_kv_pool *pool,
+                                                   const spectra_paged_query *query, void *workspace,
+                                                   size_t workspace_bytes, void *stream);
+
+/*
+ * Eviction by accumulated attention weight.  Of each sequence and KV head,
+ * with n entries, keep = min(n, budget) stay: the newest min(recent, keep)
+ * ones, and of the others the ones with the largest mass (of equal masses the
+ * older; a NaN counts as the smallest).  The kept entries (K, V and mass)
+ * move, in their order, to positions 0 .. keep-1 of fresh pages; the old
+ * pages are left as they are, for the caller to free.
+ *   pages, lengths, max_pages, n_seq   as spectra_paged_query
+ *   dst_pages    device [n_seq][dst_max_pages] page ids, dst_max_pages *
+ *                page_size >= budget; no page named here may be another
+ *                sequence's, or named in the used part of pages
+ *   new_lengths  device int32 [n_seq], receives keep; must not overlap
+ *                lengths
+ *   workspace    device, 16-byte aligned, >= the stated size
+ * Each head keeps entries of its own choice, so a position of the evicted
+ * sequence stands for different tokens in different heads.  Pages outside the
+ * pool and lengths outside [0, max_pages*page_size] as
+ * spectra_attention_paged (an entry on a bad page, or bound for one, is not
+ * moved).  Deterministic, asynchronous, allocates nothing, graph-capturable.
+ * n_seq == 0 returns SPECTRA_OK without touching CUDA.  Errors: INVALID_ARG
+ * (a pool without mass among them), SHAPE (budget < 1, recent outside [0,
+ * budget], dst_max_pages too small), ALIGN, BUFFER_TOO_SMALL, UNSUPPORTED,
+ * CUDA.
+ */
+/* Workspace bytes; 0 for invalid arguments.  Host only. */
+SPECTRA_API size_t spectra_kv_evict_workspace_size(const spectra_kv_pool *pool, int32_t n_seq,
+                                                   int32_t max_pages);
+SPECTRA_API spectra_status spectra_kv_evict(const spectra_kv_pool *pool, const int32_t *pages,
+                                            int32_t max_pages, const int32_t *lengths, int32_t n_seq,
+                                            const int32_t *dst_pages, int32_t dst_max_pages,
+                                            int32_t budget, int32_t recent, int32_t *new_lengths,
+                                            void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Token choice from logits, one per row, from given uniform numbers.
+ *   logits       device, float; row r at logits + r*stride (stride >= vocab)
+ *   u            device float [rows], in [0, 1) (clamped into it; NaN reads as 0)
+ *   temperature  device float [rows], or NULL for 1; <= 0 (or NaN): the first
+ *                of the largest logits
+ *   top_k        device int32 [rows], or NULL; <= 0: off
+ *   top_p        device float [rows], or NULL; >= 1: off
+ *   min_p        device float [rows], or NULL; <= 0: off
+ *   ids          device int32 [rows]
+ *   logprob      device float [rows], or NULL: log of the chosen token's share
+ *                of what is left after the filters
+ * With w_i = exp((x_i - max x) / temperature): top-k keeps the k largest (of
+ * equal logits the lower index first); top-p keeps a token while the weight of
+ * those before it, in that order, is under top_p of the top-k set's weight;
+ * min-p keeps w_i >= min_p; the largest always stays.  The choice is the first
+ * token, in index order, whose running sum of kept weight exceeds u times the
+ * whole.  Weights are 64-bit fixed-point numbers in steps of 2^-44, summed
+ * exactly, from double exponentials.  A logit of -infinity is never chosen;
+ * nor is a NaN, which spectra_device_status reports (NONFINITE).  A row
+ * without any other logit gets id -1, logprob -infinity and INVALID_ARG there.
+ * vocab <= 524288.  rows == 0 returns SPECTRA_OK without touching CUDA.
+ * Deterministic, asynchronous, allocates nothing, graph-capturable.
+ * Errors: INVALID_ARG, SHAPE, ALIGN (4-byte pointers), UNSUPPORTED, CUDA.
+ */
+SPECTRA_API spectra_status spectra_sample(const float *logits, int32_t rows, int32_t vocab,
+                                          int64_t stride, const float *u, const float *temperature,
+                                          const int32_t *top_k, const float *top_p,
+                                          const float *min_p, int32_t *ids, float *logprob,
+                                          void *stream);
 
 /*
  * TRDC container (abstract: every weight, scale and offset is serialised

@@ -18,7 +18,7 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib
-from ._lib import KV, Layer, Sizes, TrdcLayer
+from ._lib import KV, Layer, PagedQuery, Sizes, TrdcLayer
 
 __all__ = ["SpectraError", "PackedLayer", "spectra_status_string", "spectra_version",
            "spectra_packed_sizes", "spectra_packed_sizes_compact", "spectra_pack_plan",
@@ -26,7 +26,8 @@ __all__ = ["SpectraError", "PackedLayer", "spectra_status_string", "spectra_vers
            "spectra_gemv", "spectra_gemm_small", "spectra_gemv_batched", "spectra_embed",
            "spectra_device_status",
            "pack_layer", "library", "spectra_crc32", "write_container", "Container", "KVCache",
-           "spectra_attention_decode"]
+           "spectra_attention_decode", "KVPool", "spectra_attention_paged", "spectra_kv_evict",
+           "spectra_sample"]
 
 class _Lazy:
     """Loads libspectra.so on first attribute access."""
@@ -517,3 +518,237 @@ def spectra_attention_decode(k: KVCache, v: KVCache, q: torch.Tensor, length: in
                                        workspace.numel(), _stream(stream)),
            "spectra_attention_decode")
     return out
+
+
+# ---------------------------------------------------------------- paged KV pool
+
+def _arg(t: torch.Tensor, name: str, dtype, shape, dev=None) -> int:
+    """The pointer of a contiguous device tensor of this type and shape."""
+    if t.dtype is not dtype or tuple(t.shape) != shape or not t.is_cuda or not t.is_contiguous() or \
+            (dev is not None and t.device != dev):
+        raise ValueError(f"{name}: a contiguous {dtype} tensor {list(shape)} on {dev or 'a CUDA device'} is "
+                         f"wanted, got {t.dtype} {list(t.shape)} with strides {t.stride()} on {t.device}")
+    return t.data_ptr()
+
+
+def _opt(t, name, dtype, shape, dev):
+    return None if t is None else _arg(t, name, dtype, shape, dev)
+
+
+def _on(dev: torch.device, stream, call):
+    """call(stream handle) with dev as the current device, and with `stream`
+    (when one is given) as the stream that allocations belong to."""
+    if stream is None and torch.cuda.current_device() == dev.index:
+        return call(torch.cuda.current_stream().cuda_stream)
+    with torch.cuda.device(dev):
+        if stream is None:
+            return call(torch.cuda.current_stream().cuda_stream)
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), device=dev)
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+
+
+class KVPool:
+    """A paged Group-32 4-bit pool of K and V that many sequences share:
+    n_pages pages of page_size positions of n_heads KV heads, in device buffers
+    allocated here with torch (``from_buffers`` takes existing ones).  With
+    ``mass`` it also holds every entry's accumulated attention weight."""
+
+    def __init__(self, n_heads: int, head_dim: int, page_size: int, n_pages: int, device="cuda", *,
+                 mass: bool = False):
+        sz = self.sizes(n_heads, head_dim, page_size, n_pages)
+        dev = torch.device(device)
+        new = lambda n, dtype, item: torch.zeros(n // item, dtype=dtype, device=dev)  # noqa: E731
+        self._set(n_heads, head_dim, page_size, n_pages,
+                  [new(sz["codes"], torch.uint8, 1), new(sz["scales"], torch.int16, 2),
+                   new(sz["zeros"], torch.int32, 4)] +
+                  [new(sz["codes"], torch.uint8, 1), new(sz["scales"], torch.int16, 2),
+                   new(sz["zeros"], torch.int32, 4)],
+                  new(sz["mass"], torch.float32, 4) if mass else None)
+
+    @staticmethod
+    def sizes(n_heads: int, head_dim: int, page_size: int, n_pages: int) -> dict:
+        """Bytes of each buffer (codes, scales and zeros once for K and once for V)."""
+        got = [ctypes.c_size_t() for _ in range(4)]
+        _check(_L.spectra_kv_pool_sizes(n_heads, head_dim, page_size, n_pages, *map(ctypes.byref, got)),
+               "spectra_kv_pool_sizes")
+        return dict(zip(("codes", "scales", "zeros", "mass"), (g.value for g in got)))
+
+    @classmethod
+    def from_buffers(cls, n_heads: int, head_dim: int, page_size: int, n_pages: int, k_codes, k_scales,
+                     k_zeros, v_codes, v_scales, v_zeros, mass=None) -> "KVPool":
+        """A pool over existing device buffers: codes uint8, scales int16 (FP16
+        bits), zeros int32, mass float32, flat, of the sizes that ``sizes`` gives."""
+        sz = cls.sizes(n_heads, head_dim, page_size, n_pages)
+        for t, name, dtype, item in ((k_codes, "codes", torch.uint8, 1), (k_scales, "scales", torch.int16, 2),
+                                     (k_zeros, "zeros", torch.int32, 4), (v_codes, "codes", torch.uint8, 1),
+                                     (v_scales, "scales", torch.int16, 2), (v_zeros, "zeros", torch.int32, 4)):
+            _arg(t, name, dtype, (sz[name] // item,), k_codes.device)
+        _opt(mass, "mass", torch.float32, (sz["mass"] // 4,), k_codes.device)
+        self = cls.__new__(cls)
+        self._set(n_heads, head_dim, page_size, n_pages,
+                  [k_codes, k_scales, k_zeros, v_codes, v_scales, v_zeros], mass)
+        return self
+
+    def _set(self, n_heads, head_dim, page_size, n_pages, buffers, mass):
+        self.n_heads, self.head_dim, self.page_size, self.n_pages = n_heads, head_dim, page_size, n_pages
+        (self.k_codes, self.k_scales, self.k_zeros, self.v_codes, self.v_scales, self.v_zeros) = buffers
+        self.mass = mass
+        self.device = self.k_codes.device
+        self._view = _lib.KVPool(n_heads, head_dim, page_size, n_pages, *map(_ptr, buffers), _ptr(mass))
+        self._ref = ctypes.byref(self._view)
+
+    def view(self) -> _lib.KVPool:
+        return self._view
+
+    @property
+    def nbytes(self) -> int:
+        """Bytes of the quantised K and V (without the mass)."""
+        return 2 * (self.k_codes.numel() + 2 * self.k_scales.numel() + 4 * self.k_zeros.numel())
+
+    def _tokens(self, x, name):
+        """(pointer, token stride) of BF16 [n_tok, n_heads, head_dim], heads contiguous."""
+        h, d = self.n_heads, self.head_dim
+        n = x.shape[0]
+        if x.dtype is not torch.bfloat16 or x.shape[1:] != (h, d) or x.device != self.device or \
+                (n > 0 and (x.stride(2) != 1 or (h > 1 and x.stride(1) != d))):
+            raise ValueError(f"{name}: BF16 [n_tok, {h}, {d}] on {self.device} with contiguous heads is wanted, "
+                             f"got {x.dtype} {list(x.shape)} with strides {x.stride()} on {x.device}")
+        return x.data_ptr(), x.stride(0) if n > 1 else h * d
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, *, stream=None) -> None:
+        """Quantise k and v (BF16 [n_tok, n_heads, head_dim], the tokens any
+        stride apart) into the token slots page * page_size + r (int32 [n_tok],
+        distinct; negative: skipped)."""
+        n = k.shape[0]
+        kp, ks = self._tokens(k, "k")
+        vp, vs = self._tokens(v, "v")
+        if v.shape[0] != n:
+            raise ValueError("k and v hold different numbers of tokens")
+        sp = _arg(slots, "slots", torch.int32, (n,), self.device)
+        _on(self.device, stream, lambda s: _check(
+            _L.spectra_kv_pool_append(self._ref, kp, vp, n, ks, vs, sp, s), "spectra_kv_pool_append"))
+
+    def read(self, slots: torch.Tensor, *, out_dtype=torch.bfloat16, stream=None):
+        """K and V of the token slots (int32 [n]; negative: zeros), dequantised:
+        two tensors [n, n_heads, head_dim]."""
+        n = slots.shape[0]
+        sp = _arg(slots, "slots", torch.int32, (n,), self.device)
+
+        def call(s):
+            k, v = torch.empty((2, n, self.n_heads, self.head_dim), dtype=out_dtype, device=self.device).unbind(0)
+            _check(_L.spectra_kv_pool_read(self._ref, sp, n, k.data_ptr(), v.data_ptr(), _DT[out_dtype], s),
+                   "spectra_kv_pool_read")
+            return k, v
+
+        return _on(self.device, stream, call)
+
+
+def spectra_attention_paged(pool: KVPool, pages: torch.Tensor, lengths: torch.Tensor, q: torch.Tensor,
+                            q_start: torch.Tensor | None = None, *, max_q: int | None = None,
+                            scale: float | None = None, softcap: float = 0.0,
+                            slopes: torch.Tensor | None = None, window: int = 0,
+                            out: torch.Tensor | None = None, out_dtype=torch.bfloat16,
+                            want_lse: bool = False, update_mass: bool = False,
+                            workspace: torch.Tensor | None = None, stream=None):
+    """Attention of sequences over a pool: pages int32 [n_seq, max_pages],
+    lengths int32 [n_seq] (the new tokens' positions included), q BF16 [n_rows,
+    n_q_heads, head_dim].  Sequence b's new tokens are the rows q_start[b] ..
+    q_start[b+1]-1 (int32 [n_seq + 1]; without it, row b), at most max_q of
+    them (n_rows by default).  softcap > 0 caps the scores, slopes (float
+    [n_q_heads]) subtract slope * distance from them, window > 0 hides positions
+    that far back and further.  Returns out [n_rows, n_q_heads, head_dim], with
+    want_lse also the rows' log sums (float [n_rows, n_q_heads]); update_mass
+    adds the weights to the pool's mass.  Rows outside every sequence are not
+    written."""
+    dev = pool.device
+    n_seq, max_pages = pages.shape
+    n_rows, hq, d = q.shape
+    if d != pool.head_dim:
+        raise ValueError(f"q has head_dim {d}, the pool {pool.head_dim}")
+    if max_q is None:
+        max_q = 1 if q_start is None else max(n_rows, 1)
+    x = PagedQuery(_arg(pages, "pages", torch.int32, (n_seq, max_pages), dev),
+                   _arg(lengths, "lengths", torch.int32, (n_seq,), dev),
+                   _opt(q_start, "q_start", torch.int32, (n_seq + 1,), dev), n_seq, max_pages, n_rows, max_q,
+                   hq, window, d ** -0.5 if scale is None else scale, softcap,
+                   _arg(q, "q", torch.bfloat16, (n_rows, hq, d), dev),
+                   _opt(slopes, "slopes", torch.float32, (hq,), dev), None, 0, int(update_mass), None)
+
+    def call(s):
+        o, lse, ws = out, None, workspace
+        if o is None:
+            o = torch.empty((n_rows, hq, d), dtype=out_dtype, device=dev)
+        x.out, x.out_dtype = _arg(o, "out", o.dtype, (n_rows, hq, d), dev), _DT[o.dtype]
+        if want_lse:
+            lse = torch.empty((n_rows, hq), dtype=torch.float32, device=dev)
+            x.lse = lse.data_ptr()
+        if ws is None:
+            need = _L.spectra_attention_paged_workspace_size(pool._ref, n_rows, hq)
+            ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        _check(_L.spectra_attention_paged(pool._ref, ctypes.byref(x), ws.data_ptr(),
+                                          ws.numel() * ws.element_size(), s), "spectra_attention_paged")
+        return (o, lse) if want_lse else o
+
+    return _on(dev, stream, call)
+
+
+def spectra_kv_evict(pool: KVPool, pages: torch.Tensor, lengths: torch.Tensor, dst_pages: torch.Tensor,
+                     budget: int, recent: int, new_lengths: torch.Tensor | None = None, *,
+                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Cut each sequence to its `budget` entries: per head the newest `recent`
+    and the ones with the largest accumulated weight, moved in order to the
+    fresh pages dst_pages (int32 [n_seq, >= ceil(budget / page_size)]).
+    Returns the new lengths (int32 [n_seq], which may not be `lengths`)."""
+    dev = pool.device
+    n_seq, max_pages = pages.shape
+    dst_max = dst_pages.shape[1]
+    args = (_arg(pages, "pages", torch.int32, (n_seq, max_pages), dev), max_pages,
+            _arg(lengths, "lengths", torch.int32, (n_seq,), dev), n_seq,
+            _arg(dst_pages, "dst_pages", torch.int32, (n_seq, dst_max), dev), dst_max, budget, recent)
+
+    def call(s):
+        n, ws = new_lengths, workspace
+        if n is None:
+            n = torch.empty(n_seq, dtype=torch.int32, device=dev)
+        if ws is None:
+            need = _L.spectra_kv_evict_workspace_size(pool._ref, n_seq, max_pages)
+            ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        _check(_L.spectra_kv_evict(pool._ref, *args, _arg(n, "new_lengths", torch.int32, (n_seq,), dev),
+                                   ws.data_ptr(), ws.numel() * ws.element_size(), s), "spectra_kv_evict")
+        return n
+
+    return _on(dev, stream, call)
+
+
+# ---------------------------------------------------------------- token choice
+
+def spectra_sample(logits: torch.Tensor, u: torch.Tensor, *, temperature: torch.Tensor | None = None,
+                   top_k: torch.Tensor | None = None, top_p: torch.Tensor | None = None,
+                   min_p: torch.Tensor | None = None, stream=None):
+    """Choose a token per row of logits (float [rows, vocab], rows any stride
+    apart, or [vocab]) with the uniform numbers u (float [rows]); temperature,
+    top_p, min_p (float) and top_k (int32) are [rows] or None.  Returns (ids
+    int32 [rows], log of the chosen tokens' probabilities float [rows])."""
+    if logits.dim() == 1:
+        logits = logits.unsqueeze(0)
+    rows, vocab = logits.shape
+    dev = logits.device
+    if logits.dtype is not torch.float32 or not logits.is_cuda or (rows > 0 and logits.stride(1) != 1):
+        raise ValueError(f"logits: float32 rows on a CUDA device are wanted, got {logits.dtype} "
+                         f"{list(logits.shape)} with strides {logits.stride()} on {dev}")
+    stride = logits.stride(0) if rows > 1 else vocab
+    f32 = torch.float32
+    args = (_arg(u, "u", f32, (rows,), dev), _opt(temperature, "temperature", f32, (rows,), dev),
+            _opt(top_k, "top_k", torch.int32, (rows,), dev), _opt(top_p, "top_p", f32, (rows,), dev),
+            _opt(min_p, "min_p", f32, (rows,), dev))
+
+    def call(s):
+        ids = torch.empty(rows, dtype=torch.int32, device=dev)
+        logp = torch.empty(rows, dtype=f32, device=dev)
+        _check(_L.spectra_sample(logits.data_ptr(), rows, vocab, stride, *args, ids.data_ptr(), logp.data_ptr(),
+                                 s), "spectra_sample")
+        return ids, logp
+
+    return _on(dev, stream, call)

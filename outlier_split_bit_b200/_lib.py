@@ -50,6 +50,25 @@ class KV(ctypes.Structure):
                 ("scales", ctypes.c_void_p), ("zeros", ctypes.c_void_p)]
 
 
+class KVPool(ctypes.Structure):
+    """spectra_kv_pool: a view of a paged 4-bit K and V pool (device buffers)."""
+    _fields_ = [("n_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("k_zeros", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p), ("v_zeros", ctypes.c_void_p),
+                ("mass", ctypes.c_void_p)]
+
+
+class PagedQuery(ctypes.Structure):
+    """spectra_paged_query: the queries of one spectra_attention_paged call."""
+    _fields_ = [("pages", ctypes.c_void_p), ("lengths", ctypes.c_void_p), ("q_start", ctypes.c_void_p),
+                ("n_seq", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("n_rows", ctypes.c_int32),
+                ("max_q", ctypes.c_int32), ("n_q_heads", ctypes.c_int32), ("window", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("q", ctypes.c_void_p),
+                ("slopes", ctypes.c_void_p), ("out", ctypes.c_void_p), ("out_dtype", ctypes.c_int),
+                ("update_mass", ctypes.c_int32), ("lse", ctypes.c_void_p)]
+
+
 class TrdcLayer(ctypes.Structure):
     """spectra_trdc_layer: one layer record of a TRDC container."""
     _fields_ = [("name", ctypes.c_char * 96), ("n", ctypes.c_int32), ("k", ctypes.c_int32),
@@ -60,8 +79,8 @@ class TrdcLayer(ctypes.Structure):
 
 # name -> (restype, argtypes), mirroring spectra.h
 P = ctypes.c_void_p
-i32, f64, sz = ctypes.c_int32, ctypes.c_double, ctypes.c_size_t
-LP = ctypes.POINTER(Layer)
+i32, i64, f64, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_double, ctypes.c_size_t
+LP, PP = ctypes.POINTER(Layer), ctypes.POINTER(KVPool)
 SIGNATURES = {
     "spectra_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "spectra_version": (i32, []),
@@ -93,6 +112,14 @@ SIGNATURES = {
     "spectra_attention_workspace_size": (sz, [i32, i32, i32]),
     "spectra_attention_decode": (ctypes.c_int, [ctypes.POINTER(KV), ctypes.POINTER(KV), P, i32, i32,
                                                 ctypes.c_float, P, P, sz, P]),
+    "spectra_kv_pool_sizes": (ctypes.c_int, [i32, i32, i32, i32] + [ctypes.POINTER(sz)] * 4),
+    "spectra_kv_pool_append": (ctypes.c_int, [PP, P, P, i32, i64, i64, P, P]),
+    "spectra_kv_pool_read": (ctypes.c_int, [PP, P, i32, P, P, ctypes.c_int, P]),
+    "spectra_attention_paged_workspace_size": (sz, [PP, i32, i32]),
+    "spectra_attention_paged": (ctypes.c_int, [PP, ctypes.POINTER(PagedQuery), P, sz, P]),
+    "spectra_kv_evict_workspace_size": (sz, [PP, i32, i32]),
+    "spectra_kv_evict": (ctypes.c_int, [PP, P, i32, P, i32, P, i32, i32, i32, P, P, sz, P]),
+    "spectra_sample": (ctypes.c_int, [P, i32, i32, i64, P, P, P, P, P, P, P, P]),
     "spectra_trdc_write": (ctypes.c_int, [ctypes.c_char_p, i32, P, LP, P, ctypes.c_int, P, sz, P]),
     "spectra_trdc_open": (ctypes.c_int, [ctypes.c_char_p, ctypes.POINTER(P)]),
     "spectra_trdc_count": (i32, [P]),

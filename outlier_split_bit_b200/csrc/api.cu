@@ -543,6 +543,169 @@ spectra_status spectra_attention_decode(const spectra_kv *k, const spectra_kv *v
                             (cudaStream_t)stream);
 }
 
+static spectra_status check_pool_shape(int32_t n_heads, int32_t head_dim, int32_t page_size, int32_t n_pages) {
+    if (n_heads < 1 || n_heads > 65535 || head_dim < 32 || head_dim > 256 || head_dim % 32 != 0 ||
+        page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)) != 0 || n_pages < 1)
+        return SPECTRA_ERR_SHAPE;
+    const int64_t slots = (int64_t)n_pages * page_size;
+    if (slots >= ((int64_t)1 << 31) || slots * n_heads > ((int64_t)1 << 40) / head_dim) return SPECTRA_ERR_SHAPE;
+    return SPECTRA_OK;
+}
+
+static spectra_status check_pool(const spectra_kv_pool *p) {
+    if (!p) return SPECTRA_ERR_INVALID_ARG;
+    const spectra_status st = check_pool_shape(p->n_heads, p->head_dim, p->page_size, p->n_pages);
+    if (st != SPECTRA_OK) return st;
+    if (!p->k_codes || !p->k_scales || !p->k_zeros || !p->v_codes || !p->v_scales || !p->v_zeros)
+        return SPECTRA_ERR_INVALID_ARG;
+    if (!aligned16(p->k_codes) || !aligned16(p->k_scales) || !aligned16(p->k_zeros) ||
+        !aligned16(p->v_codes) || !aligned16(p->v_scales) || !aligned16(p->v_zeros) || !aligned16(p->mass))
+        return SPECTRA_ERR_ALIGN;
+    return SPECTRA_OK;
+}
+
+spectra_status spectra_kv_pool_sizes(int32_t n_heads, int32_t head_dim, int32_t page_size,
+                                     int32_t n_pages, size_t *codes_bytes, size_t *scales_bytes,
+                                     size_t *zeros_bytes, size_t *mass_bytes) {
+    if (!codes_bytes || !scales_bytes || !zeros_bytes || !mass_bytes) return SPECTRA_ERR_INVALID_ARG;
+    const spectra_status st = check_pool_shape(n_heads, head_dim, page_size, n_pages);
+    if (st != SPECTRA_OK) return st;
+    const size_t slots = (size_t)n_pages * page_size * n_heads;
+    *codes_bytes = slots * (head_dim / 2);
+    *scales_bytes = slots * (head_dim / 32) * 2;
+    *zeros_bytes = slots * 4;
+    *mass_bytes = slots * 4;
+    return SPECTRA_OK;
+}
+
+spectra_status spectra_kv_pool_append(const spectra_kv_pool *pool, const uint16_t *k, const uint16_t *v,
+                                      int32_t n_tok, int64_t k_stride, int64_t v_stride,
+                                      const int32_t *slots, void *stream) {
+    spectra_status st = check_pool(pool);
+    if (st != SPECTRA_OK) return st;
+    if (n_tok < 0) return SPECTRA_ERR_INVALID_ARG;
+    if (n_tok == 0) return SPECTRA_OK;
+    if (!k || !v || !slots) return SPECTRA_ERR_INVALID_ARG;
+    const int64_t row = (int64_t)pool->n_heads * pool->head_dim;
+    if (k_stride < row || v_stride < row || k_stride > ((int64_t)1 << 40) || v_stride > ((int64_t)1 << 40))
+        return SPECTRA_ERR_SHAPE;
+    // every warp's item must have a number, and the grid must fit
+    if ((int64_t)n_tok * pool->n_heads > ((int64_t)1 << 30)) return SPECTRA_ERR_SHAPE;
+    if (!aligned16(k) || !aligned16(v) || k_stride % 8 != 0 || v_stride % 8 != 0 || !aligned4(slots))
+        return SPECTRA_ERR_ALIGN;
+    DeviceInfo dev;
+    st = current_device(&dev);
+    if (st != SPECTRA_OK) return st;
+    return launch_pool_append(*pool, k, v, n_tok, k_stride, v_stride, slots, (cudaStream_t)stream);
+}
+
+spectra_status spectra_kv_pool_read(const spectra_kv_pool *pool, const int32_t *slots, int32_t n,
+                                    void *k_out, void *v_out, spectra_dtype out_dtype, void *stream) {
+    spectra_status st = check_pool(pool);
+    if (st != SPECTRA_OK) return st;
+    if (n < 0 || (out_dtype != SPECTRA_F32 && out_dtype != SPECTRA_BF16)) return SPECTRA_ERR_INVALID_ARG;
+    if (n == 0) return SPECTRA_OK;
+    if (!slots || (!k_out && !v_out)) return SPECTRA_ERR_INVALID_ARG;
+    if ((int64_t)n * pool->n_heads > ((int64_t)1 << 30)) return SPECTRA_ERR_SHAPE;
+    if (!aligned4(slots) || !aligned16(k_out) || !aligned16(v_out)) return SPECTRA_ERR_ALIGN;
+    DeviceInfo dev;
+    st = current_device(&dev);
+    if (st != SPECTRA_OK) return st;
+    return launch_pool_read(*pool, slots, n, k_out, v_out, out_dtype == SPECTRA_BF16, (cudaStream_t)stream);
+}
+
+static bool paged_heads_ok(const spectra_kv_pool *pool, int32_t n_q_heads) {
+    return n_q_heads >= 1 && n_q_heads % pool->n_heads == 0 && n_q_heads / pool->n_heads <= 64;
+}
+
+size_t spectra_attention_paged_workspace_size(const spectra_kv_pool *pool, int32_t n_rows, int32_t n_q_heads) {
+    if (!pool || check_pool_shape(pool->n_heads, pool->head_dim, pool->page_size, pool->n_pages) != SPECTRA_OK ||
+        n_rows < 0 || !paged_heads_ok(pool, n_q_heads))
+        return 0;
+    return paged_workspace_bytes(n_rows, n_q_heads, pool->head_dim);
+}
+
+spectra_status spectra_attention_paged(const spectra_kv_pool *pool, const spectra_paged_query *x,
+                                       void *workspace, size_t workspace_bytes, void *stream) {
+    spectra_status st = check_pool(pool);
+    if (st != SPECTRA_OK) return st;
+    if (!x || x->n_seq < 0 || x->n_rows < 0) return SPECTRA_ERR_INVALID_ARG;
+    if (!paged_heads_ok(pool, x->n_q_heads)) return SPECTRA_ERR_SHAPE;
+    if (x->n_seq > 65535 || x->max_pages < 1 || x->max_q < 1 || x->window < 0) return SPECTRA_ERR_SHAPE;
+    if ((int64_t)x->max_pages * pool->page_size >= ((int64_t)1 << 31)) return SPECTRA_ERR_SHAPE;
+    if (x->out_dtype != SPECTRA_F32 && x->out_dtype != SPECTRA_BF16) return SPECTRA_ERR_INVALID_ARG;
+    if (!std::isfinite(x->scale) || !std::isfinite(x->softcap) || x->softcap < 0.f) return SPECTRA_ERR_INVALID_ARG;
+    if (x->update_mass && !pool->mass) return SPECTRA_ERR_INVALID_ARG;
+    if (x->n_seq == 0 || x->n_rows == 0) return SPECTRA_OK;
+    if (!x->pages || !x->lengths || !x->q || !x->out || !workspace) return SPECTRA_ERR_INVALID_ARG;
+    if (!x->q_start && x->n_rows != x->n_seq) return SPECTRA_ERR_SHAPE;
+    if ((int64_t)x->n_rows * x->n_q_heads >= ((int64_t)1 << 31)) return SPECTRA_ERR_SHAPE;
+    if (!aligned4(x->pages) || !aligned4(x->lengths) || !aligned4(x->q_start) || !aligned4(x->slopes) ||
+        !aligned4(x->lse) || !aligned16(x->q) || !aligned16(x->out) || !aligned16(workspace))
+        return SPECTRA_ERR_ALIGN;
+    if (workspace_bytes < paged_workspace_bytes(x->n_rows, x->n_q_heads, pool->head_dim))
+        return SPECTRA_ERR_BUFFER_TOO_SMALL;
+    DeviceInfo dev;
+    st = current_device(&dev);
+    if (st != SPECTRA_OK) return st;
+    return launch_paged_attention(*pool, *x, workspace, (cudaStream_t)stream, dev);
+}
+
+size_t spectra_kv_evict_workspace_size(const spectra_kv_pool *pool, int32_t n_seq, int32_t max_pages) {
+    if (!pool || check_pool_shape(pool->n_heads, pool->head_dim, pool->page_size, pool->n_pages) != SPECTRA_OK ||
+        n_seq < 0 || n_seq > 65535 || max_pages < 1 || (int64_t)max_pages * pool->page_size >= ((int64_t)1 << 31))
+        return 0;
+    return evict_workspace_bytes(n_seq, pool->n_heads, (int64_t)max_pages * pool->page_size);
+}
+
+spectra_status spectra_kv_evict(const spectra_kv_pool *pool, const int32_t *pages, int32_t max_pages,
+                                const int32_t *lengths, int32_t n_seq, const int32_t *dst_pages,
+                                int32_t dst_max_pages, int32_t budget, int32_t recent,
+                                int32_t *new_lengths, void *workspace, size_t workspace_bytes,
+                                void *stream) {
+    spectra_status st = check_pool(pool);
+    if (st != SPECTRA_OK) return st;
+    if (!pool->mass || n_seq < 0) return SPECTRA_ERR_INVALID_ARG;
+    if (n_seq > 65535 || max_pages < 1 || dst_max_pages < 1 || budget < 1 || recent < 0 || recent > budget)
+        return SPECTRA_ERR_SHAPE;
+    if ((int64_t)max_pages * pool->page_size >= ((int64_t)1 << 31) ||
+        (int64_t)dst_max_pages * pool->page_size >= ((int64_t)1 << 31) ||
+        (int64_t)dst_max_pages * pool->page_size < budget)
+        return SPECTRA_ERR_SHAPE;
+    if (n_seq == 0) return SPECTRA_OK;
+    if (!pages || !lengths || !dst_pages || !new_lengths || !workspace) return SPECTRA_ERR_INVALID_ARG;
+    const uintptr_t from = (uintptr_t)lengths, to = (uintptr_t)new_lengths, span = (uintptr_t)n_seq * 4;
+    if (from < to + span && to < from + span) return SPECTRA_ERR_INVALID_ARG;
+    if (!aligned4(pages) || !aligned4(lengths) || !aligned4(dst_pages) || !aligned4(new_lengths) ||
+        !aligned16(workspace))
+        return SPECTRA_ERR_ALIGN;
+    if (workspace_bytes < evict_workspace_bytes(n_seq, pool->n_heads, (int64_t)max_pages * pool->page_size))
+        return SPECTRA_ERR_BUFFER_TOO_SMALL;
+    DeviceInfo dev;
+    st = current_device(&dev);
+    if (st != SPECTRA_OK) return st;
+    return launch_evict(*pool, pages, max_pages, lengths, n_seq, dst_pages, dst_max_pages, budget, recent,
+                        new_lengths, workspace, (cudaStream_t)stream);
+}
+
+spectra_status spectra_sample(const float *logits, int32_t rows, int32_t vocab, int64_t stride,
+                              const float *u, const float *temperature, const int32_t *top_k,
+                              const float *top_p, const float *min_p, int32_t *ids, float *logprob,
+                              void *stream) {
+    if (rows < 0 || vocab < 1 || vocab > sample_max_vocab() || stride < vocab || stride > ((int64_t)1 << 40))
+        return SPECTRA_ERR_SHAPE;
+    if (rows == 0) return SPECTRA_OK;
+    if (!logits || !u || !ids) return SPECTRA_ERR_INVALID_ARG;
+    if (!aligned4(logits) || !aligned4(u) || !aligned4(temperature) || !aligned4(top_k) || !aligned4(top_p) ||
+        !aligned4(min_p) || !aligned4(ids) || !aligned4(logprob))
+        return SPECTRA_ERR_ALIGN;
+    DeviceInfo dev;
+    const spectra_status st = current_device(&dev);
+    if (st != SPECTRA_OK) return st;
+    return launch_sample(logits, rows, vocab, stride, u, temperature, top_k, top_p, min_p, ids, logprob,
+                         (cudaStream_t)stream);
+}
+
 spectra_status spectra_selftest_wait(int32_t kind, void *stream) {
     if (kind != 0 && kind != 1) return SPECTRA_ERR_INVALID_ARG;
     DeviceInfo dev;
@@ -563,9 +726,17 @@ spectra_status spectra_device_status(void *stream) {
     if (st != SPECTRA_OK) return st;
     st = kv_device_error(&kv_bits, (cudaStream_t)stream);
     if (st != SPECTRA_OK) return st;
+    unsigned int pool_bits = 0, paged_bits = 0, sample_bits = 0;
+    st = pool_device_error(&pool_bits, (cudaStream_t)stream);
+    if (st != SPECTRA_OK) return st;
+    st = paged_device_error(&paged_bits, (cudaStream_t)stream);
+    if (st != SPECTRA_OK) return st;
+    st = sample_device_error(&sample_bits, (cudaStream_t)stream);
+    if (st != SPECTRA_OK) return st;
+    kv_bits |= pool_bits;
     if (mv_bits & 1u) return SPECTRA_ERR_INTERNAL;
-    if (embed_bits) return SPECTRA_ERR_INVALID_ARG;
-    if (kv_bits & 1u) return SPECTRA_ERR_NONFINITE;
+    if (embed_bits || ((pool_bits | paged_bits) & 4u) || (sample_bits & 2u)) return SPECTRA_ERR_INVALID_ARG;
+    if ((kv_bits & 1u) || (sample_bits & 1u)) return SPECTRA_ERR_NONFINITE;
     if ((kv_bits & 2u) || (mv_bits & 2u)) return SPECTRA_ERR_RANGE;
     return SPECTRA_OK;
 }

@@ -135,4 +135,34 @@ int attention_max_group();
 // Reads (and clears) the append's flag: bit 0 non-finite value, bit 1 FP16 range.
 spectra_status kv_device_error(unsigned int *bits, cudaStream_t s);
 
+// ---- paged KV pool (pool.cu) ----
+spectra_status launch_pool_append(const spectra_kv_pool &pool, const uint16_t *k, const uint16_t *v,
+                                  int n_tok, int64_t k_stride, int64_t v_stride, const int32_t *slots,
+                                  cudaStream_t s);
+spectra_status launch_pool_read(const spectra_kv_pool &pool, const int32_t *slots, int n, void *k_out,
+                                void *v_out, bool bf16, cudaStream_t s);
+size_t evict_workspace_bytes(int n_seq, int n_heads, int64_t positions);
+spectra_status launch_evict(const spectra_kv_pool &pool, const int32_t *pages, int max_pages,
+                            const int32_t *lengths, int n_seq, const int32_t *dst_pages,
+                            int dst_max_pages, int budget, int recent, int32_t *new_lengths, void *ws,
+                            cudaStream_t s);
+// Reads (and clears) the pool's flags: bit 0 non-finite value, bit 1 FP16
+// range, bit 2 a slot, page or length out of bounds.
+spectra_status pool_device_error(unsigned int *bits, cudaStream_t s);
+
+// ---- attention over the pool (paged.cu) ----
+size_t paged_workspace_bytes(int n_rows, int n_q_heads, int head_dim);
+spectra_status launch_paged_attention(const spectra_kv_pool &pool, const spectra_paged_query &x, void *ws,
+                                      cudaStream_t s, const DeviceInfo &dev);
+// Reads (and clears) its flag (bit 2 as pool_device_error).
+spectra_status paged_device_error(unsigned int *bits, cudaStream_t s);
+
+// ---- token choice (sample.cu) ----
+int sample_max_vocab();
+spectra_status launch_sample(const float *logits, int rows, int vocab, int64_t stride, const float *u,
+                             const float *temperature, const int32_t *top_k, const float *top_p,
+                             const float *min_p, int32_t *ids, float *logp, cudaStream_t s);
+// Reads (and clears) its flags: bit 0 a NaN logit, bit 1 a row with nothing to choose.
+spectra_status sample_device_error(unsigned int *bits, cudaStream_t s);
+
 }  // namespace spectra

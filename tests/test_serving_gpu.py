@@ -1,0 +1,752 @@
+"""The paged 4-bit pool (append, read, attention, eviction) and the sampler on
+the GPU against plain 64-bit forms (tests/serving_reference.py).  The pools
+start out full of infinities and NaN, so that whatever a mask or a length
+should hide would show."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import outlier_split_bit_b200 as sp
+from outlier_split_bit_b200 import workload as wl
+
+import serving_reference as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF16_HALF = 2.0 ** -8
+
+
+def device_pool(p: ref.Pool, mass=True) -> sp.KVPool:
+    t = [torch.from_numpy(np.ascontiguousarray(b).view(kind).ravel()).to(DEV)
+         for b, kind in zip(p.buffers(), (np.uint8, np.int16, np.int32) * 2)]
+    m = torch.from_numpy(p.mass.copy()).to(DEV) if mass else None
+    return sp.KVPool.from_buffers(p.H, p.D, p.P, p.n_pages, *t, m)
+
+
+def same_buffers(g: sp.KVPool, p: ref.Pool):
+    for name, t, b in zip(("kc", "ks", "kz", "vc", "vs", "vz"),
+                          (g.k_codes, g.k_scales, g.k_zeros, g.v_codes, g.v_scales, g.v_zeros), p.buffers()):
+        assert np.array_equal(t.cpu().numpy().view(np.uint8).ravel(),
+                              np.ascontiguousarray(b).view(np.uint8).ravel()), name
+    if g.mass is not None:
+        assert np.array_equal(g.mass.cpu().numpy(), p.mass, equal_nan=True)
+
+
+def tables(rng, lengths, P, spare=2):
+    need = [-(-n // P) for n in lengths]
+    order = rng.permutation(sum(need) + spare)
+    width = max(1, max(need))
+    pages = np.full((len(need), width), -7, np.int32)  # never looked at
+    at = 0
+    for b, n in enumerate(need):
+        pages[b, :n] = order[at:at + n]
+        at += n
+    return pages, sum(need) + spare, order[at:].astype(np.int32)
+
+
+def token_slots(pages, n, P):
+    return np.array([int(pages[t // P]) * P + t % P for t in range(n)], np.int32)
+
+
+def filled(rng, lengths, H, D, P, spare=2, scale=1.0):
+    """A reference pool holding quantised normal tokens, its page table and spare pages."""
+    pages, n_pages, free = tables(rng, lengths, P, spare)
+    p = ref.Pool(H, D, P, n_pages, rng)
+    for b, n in enumerate(lengths):
+        if n:
+            x = torch.from_numpy(rng.standard_normal((2, n, H, D)) * scale).to(torch.bfloat16)
+            p.append(wl.bits(x[0]), wl.bits(x[1]), token_slots(pages[b], n, P))
+    return p, pages, free
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device=DEV)
+
+
+# ---------------------------------------------------------------- append and read
+
+@pytest.mark.parametrize("H,D,P,n", [(2, 128, 16, 1), (8, 64, 32, 53), (1, 256, 128, 70), (3, 32, 16, 33),
+                                     (2, 96, 64, 40), (5, 160, 16, 21), (1, 192, 16, 9), (4, 224, 16, 18)])
+def test_append_bit_exact(H, D, P, n):
+    rng = np.random.default_rng(H * 1000 + D)
+    p = ref.Pool(H, D, P, -(-n // P) + 3, rng)
+    g = device_pool(p)
+    slots = rng.permutation(p.n_pages * P)[:n].astype(np.int32)
+    slots[rng.random(n) < 0.2] = -3
+    # magnitudes from subnormal scales to thousands, constant groups, zeros of both signs, exact halves
+    x = rng.standard_normal((2, n, H, D)) * np.exp2(rng.integers(-26, 12, (2, n, H, 1)))
+    x += np.where(rng.random((2, n, H, 1)) < 0.2, 300.0, 0.0)
+    x[0, ::3] = np.round(x[0, ::3] * 2) / 2
+    x[1, 1::4] = np.where(rng.random((n, H, D)) < 0.5, -0.0, 0.0)[1::4]
+    x[0, :, :, :32] = np.where(rng.random((n, 1, 1)) < 0.2, 1.5, x[0, :, :, :32])
+    t = torch.from_numpy(x).to(torch.bfloat16)
+    g.append(t[0].to(DEV), t[1].to(DEV), i32(slots))
+    p.append(wl.bits(t[0]), wl.bits(t[1]), slots)
+    same_buffers(g, p)
+    sp.spectra_device_status()
+    # read back, in FP32 exactly and in BF16 with one rounding
+    want = np.zeros((2, n, H, D))
+    for w, which in enumerate("kv"):
+        for i, ts in enumerate(slots):
+            for h in range(H if ts >= 0 else 0):
+                want[w, i, h] = p.value(which, int(ts), h)
+    for dt in (torch.float32, torch.bfloat16):
+        got = g.read(i32(slots), out_dtype=dt)
+        for w in range(2):
+            assert torch.equal(got[w].cpu(), torch.from_numpy(want[w]).float().to(dt))
+
+
+def test_append_many_groups_bit_exact():
+    """A quarter of a million groups of every spread against the oracle."""
+    n, H, D, P = 512, 8, 256, 64
+    gen = torch.Generator().manual_seed(11)
+    x = torch.randn((2, n, H, D), generator=gen) * torch.exp2(torch.randint(-8, 8, (2, n, H, 1), generator=gen).float())
+    # coarse values: many quotients are exact halves
+    x[:, ::2] = torch.round(x[:, ::2] * 4) / 4
+    x = x.to(torch.bfloat16)
+    g = sp.KVPool(H, D, P, n // P)
+    g.append(x[0].to(DEV), x[1].to(DEV), torch.arange(n, dtype=torch.int32, device=DEV))
+    got = g.read(torch.arange(n, dtype=torch.int32, device=DEV), out_dtype=torch.float32)
+    for w in range(2):
+        c = oracle.kv_cache(H, n, D)
+        oracle.kv_quantize(c, wl.bits(x[w]), 0)
+        v = (c.codes.astype(np.float64) - np.repeat(c.zeros, 32, axis=2)) * \
+            np.repeat(c.scales.view(np.float16).astype(np.float64), 32, axis=2)
+        assert np.array_equal(got[w].cpu().numpy().astype(np.float64), v.transpose(1, 0, 2))
+
+
+def test_append_strided_projection():
+    """K and V as slices of one fused projection's rows."""
+    H, D, P, n = 2, 64, 16, 19
+    rng = np.random.default_rng(4)
+    qkv = torch.from_numpy(rng.standard_normal((n, 5 * H * D))).to(torch.bfloat16).to(DEV)
+    k = qkv[:, 3 * H * D:4 * H * D].unflatten(1, (H, D))
+    v = qkv[:, 4 * H * D:].unflatten(1, (H, D))
+    a, b = sp.KVPool(H, D, P, 2), sp.KVPool(H, D, P, 2)
+    slots = torch.arange(n, dtype=torch.int32, device=DEV)
+    a.append(k, v, slots)
+    b.append(k.contiguous(), v.contiguous(), slots)
+    assert torch.equal(a.k_codes, b.k_codes) and torch.equal(a.v_codes, b.v_codes) and a.k_codes.any()
+    with pytest.raises(ValueError):
+        a.append(k.transpose(1, 2), v, slots)
+    with pytest.raises(ValueError):
+        a.append(k.float(), v, slots)
+
+
+def test_append_reports_bad_values_and_slots():
+    H, D, P = 2, 64, 16
+    g = sp.KVPool(H, D, P, 2, mass=True)
+    sp.spectra_device_status()
+    x = torch.ones((3, H, D), dtype=torch.bfloat16, device=DEV) * torch.arange(D, device=DEV)
+    x[1, 0, 40] = float("nan")
+    g.append(x, x, i32([0, 1, 2]))
+    with pytest.raises(sp.SpectraError) as e:
+        sp.spectra_device_status()
+    assert e.value.status == 4
+    k, v = g.read(i32([0, 1, 2]), out_dtype=torch.float32)
+    assert not k[1, 0, 32:].any() and k[1, 0, 2:32].all() and k[2, 0, 33:].all()
+    x[1, 0, 40] = 3e38
+    g.append(x, x, i32([0, 1, 2]))
+    with pytest.raises(sp.SpectraError) as e:
+        sp.spectra_device_status()
+    assert e.value.status == 5
+    before = g.k_codes.clone()
+    g.append(x[:1], x[:1], i32([2 * P]))
+    with pytest.raises(sp.SpectraError) as e:
+        sp.spectra_device_status()
+    assert e.value.status == 1 and torch.equal(before, g.k_codes)
+    assert not g.read(i32([2 * P]))[0].any()
+    with pytest.raises(sp.SpectraError):
+        sp.spectra_device_status()
+    sp.spectra_device_status()
+    g.append(x[:0], x[:0], i32([]))
+    assert g.read(i32([]))[0].shape == (0, H, D)
+
+
+# ---------------------------------------------------------------- attention
+
+def check_attention(rng, lengths, m, Hq, H, D, P, *, out_dtype=torch.bfloat16, softcap=0.0, slopes=None, window=0,
+                    scale=None, value_scale=1.0, q_scale=1.0, gap_rows=0):
+    p, pages, _ = filled(rng, lengths, H, D, P, scale=value_scale)
+    used = np.concatenate([[s for h in range(H) for s in p.slot(token_slots(pages[b], n, P), h)]
+                           for b, n in enumerate(lengths)]).astype(np.int64)
+    p.mass[used] = rng.random(len(used)).astype(np.float32)
+    g = device_pool(p)
+    start = np.concatenate([[0], np.cumsum(m)]) + gap_rows
+    rows = int(start[-1]) + gap_rows
+    q = (torch.from_numpy(rng.standard_normal((rows, Hq, D))) * q_scale).to(torch.bfloat16)
+    scale = D ** -0.5 if scale is None else scale
+    out = torch.full((rows, Hq, D), 123.0, dtype=out_dtype, device=DEV)
+    sl = None if slopes is None else torch.tensor(slopes, dtype=torch.float32)
+    got, lse = sp.spectra_attention_paged(
+        g, i32(pages), i32(lengths), q.to(DEV), i32(start), max_q=max(1, max(m)), scale=scale, softcap=softcap,
+        slopes=None if sl is None else sl.to(DEV), window=window, out=out, want_lse=True, update_mass=True)
+    assert got is out
+    sp.spectra_device_status()
+    want, wl_, add, to, tl, tm = ref.attention(p, pages, lengths, q.double().numpy(), start, float(np.float32(scale)),
+                                               softcap, None if sl is None else sl.double().numpy(), window)
+    a = out.double().cpu().numpy()
+    mine = slice(int(start[0]), int(start[-1]))
+    assert (a[:int(start[0])] == 123.0).all() and (a[int(start[-1]):] == 123.0).all()
+    tol = to + (BF16_HALF * (np.abs(want) + to) if out_dtype is torch.bfloat16 else 2.0 ** -23 * np.abs(want))
+    err = np.abs(a - want)[mine]
+    assert np.isfinite(a).all() and (err <= tol[mine]).all(), f"out: worst ratio {(err / tol[mine]).max():.3g}"
+    l = lse.double().cpu().numpy()[mine]
+    empty = np.isneginf(wl_[mine])
+    assert (np.isneginf(l) == empty).all()
+    with np.errstate(invalid="ignore"):
+        assert (empty | (np.abs(l - wl_[mine]) <= tl[mine])).all()
+    base = p.mass.astype(np.float64)
+    mg = g.mass.double().cpu().numpy()
+    touched = np.zeros(len(mg), bool)
+    touched[used] = True
+    assert np.array_equal(g.mass.cpu().numpy()[~touched], p.mass[~touched], equal_nan=True)
+    err = np.abs(mg - base - add)[touched]
+    assert (err <= tm[touched] + 2.0 ** -23 * (base + add)[touched]).all()
+    # a second pass: the same bits
+    again = sp.spectra_attention_paged(
+        g, i32(pages), i32(lengths), q.to(DEV), i32(start), max_q=max(1, max(m)), scale=scale, softcap=softcap,
+        slopes=None if sl is None else sl.to(DEV), window=window, out_dtype=out_dtype)
+    assert torch.equal(again[mine], out[mine])
+    return p, g, pages
+
+
+DECODE = [  # Hq, H, D, P, lengths
+    (12, 2, 128, 16, [1]),
+    (12, 2, 128, 64, [300]),
+    (8, 8, 64, 16, [0, 1, 15, 16, 17, 31, 33]),
+    (16, 2, 256, 32, [63, 64, 65, 127, 128, 129]),
+    (4, 4, 32, 16, [5, 0, 200]),
+    (6, 2, 96, 128, [250, 3]),
+    (10, 2, 160, 16, [70]),
+    (9, 3, 192, 16, [81, 2]),
+    (2, 1, 224, 1024, [100]),
+    (32, 2, 64, 16, [90, 35]),       # 16 query heads per KV head
+    (64, 1, 128, 32, [40]),          # 64 of them
+    (7, 1, 128, 16, [129, 64]),
+]
+
+
+@pytest.mark.parametrize("Hq,H,D,P,lengths", DECODE, ids=[f"q{c[0]}-kv{c[1]}-d{c[2]}-p{c[3]}" for c in DECODE])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+def test_decode(Hq, H, D, P, lengths, out_dtype):
+    check_attention(np.random.default_rng(Hq * D), lengths, [1] * len(lengths), Hq, H, D, P, out_dtype=out_dtype)
+
+
+@pytest.mark.parametrize("kw", [dict(softcap=3.0), dict(window=1), dict(window=40), dict(window=17, softcap=20.0),
+                                dict(slopes=[0.5, 0.25, 0.0, -0.01, 2.0, 0.03]),
+                                dict(slopes=[0.5, 0.25, 0.0, 0.01, 2.0, 0.03], window=50, softcap=1.0),
+                                dict(scale=0.0), dict(scale=-0.2)],
+                         ids=["cap", "window1", "window40", "window-cap", "slopes", "all", "scale0", "negative"])
+@pytest.mark.parametrize("m", [[1, 1, 1, 1], [3, 0, 7, 20]], ids=["decode", "chunks"])
+def test_score_options(kw, m):
+    check_attention(np.random.default_rng(5), [100, 33, 5, 20], m, 6, 3, 64, 16, out_dtype=torch.float32, **kw)
+
+
+CHUNKS = [  # Hq, H, D, P, lengths, rows
+    (12, 2, 128, 16, [40, 17, 0, 100], [16, 17, 0, 5]),
+    (8, 8, 64, 32, [9, 130], [9, 33]),
+    (6, 1, 96, 16, [20, 5], [3, 12]),       # 12 rows over 5 positions: the first see nothing
+    (4, 2, 256, 64, [70, 1, 2], [7, 1, 6]),
+    (3, 3, 32, 16, [0, 0, 12], [2, 0, 12]),  # rows of an empty sequence
+    (16, 1, 64, 16, [65], [64]),
+    (5, 1, 128, 16, [150], [150]),           # a whole prompt
+]
+
+
+@pytest.mark.parametrize("Hq,H,D,P,lengths,m", CHUNKS, ids=[f"q{c[0]}-kv{c[1]}-d{c[2]}-{max(c[5])}" for c in CHUNKS])
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32], ids=["bf16", "fp32"])
+def test_chunks(Hq, H, D, P, lengths, m, out_dtype):
+    check_attention(np.random.default_rng(D + Hq), lengths, m, Hq, H, D, P, out_dtype=out_dtype, gap_rows=3)
+
+
+@pytest.mark.parametrize("value_scale,q_scale", [(1e-6, 1.0), (3e3, 1e-3), (1.0, 30.0), (100.0, 100.0)])
+def test_magnitudes(value_scale, q_scale):
+    """Subnormal FP16 scales, large values, scores far apart."""
+    check_attention(np.random.default_rng(9), [77, 300], [1, 4], 4, 2, 64, 16, out_dtype=torch.float32,
+                    value_scale=value_scale, q_scale=q_scale)
+
+
+def test_many_sequences_ragged():
+    rng = np.random.default_rng(21)
+    lengths = [int(n) for n in rng.integers(0, 120, 70)]
+    check_attention(rng, lengths, [1] * 70, 2, 1, 32, 16)
+
+
+def _big(n_seq, length, H, Hq, D, P, seed=0):
+    """A device pool of random finite entries with shuffled pages, and queries."""
+    gen = torch.Generator(device=DEV).manual_seed(seed)
+    width = -(-length // P)
+    g = sp.KVPool(H, D, P, n_seq * width)
+    for c in (g.k_codes, g.v_codes):
+        c.random_(0, 256, generator=gen)
+    for s in (g.k_scales, g.v_scales):
+        s.copy_((0.05 + 0.3 * torch.rand(s.shape, generator=gen, device=DEV)).half().view(torch.int16))
+    for z in (g.k_zeros, g.v_zeros):
+        z.copy_(torch.randint(0, 1 << (4 * (D // 32) - 1), z.shape, generator=gen, device=DEV).to(torch.int32))
+    pages = torch.randperm(n_seq * width, generator=gen, device=DEV).to(torch.int32).reshape(n_seq, width)
+    q = torch.randn((n_seq, Hq, D), generator=gen, device=DEV).bfloat16()
+    return g, pages, q
+
+
+def _plain_rows(g, pages, q, lengths, scale):
+    """FP64 attention of one token per sequence from the pool's read-back."""
+    out, P = [], g.page_size
+    for b, n in enumerate(lengths):
+        t = torch.arange(n, device=DEV)
+        k, v = (x.double() for x in g.read((pages[b, t // P] * P + t % P).to(torch.int32), out_dtype=torch.float32))
+        grp = q.shape[1] // g.n_heads
+        s = torch.einsum("hgd,thd->hgt", q[b].double().unflatten(0, (g.n_heads, grp)), k) * scale
+        out.append((torch.einsum("hgt,thd->hgd", torch.softmax(s, -1), v).flatten(0, 1),
+                    torch.logsumexp(s, -1).flatten()))
+    return torch.stack([o for o, _ in out]), torch.stack([l for _, l in out])
+
+
+@pytest.mark.parametrize("n_seq,length,H,Hq,D,P", [(1, 8192, 2, 12, 128, 64), (3, 40000, 8, 32, 128, 16),
+                                                   (130, 700, 4, 8, 64, 32), (2, 30000, 1, 16, 256, 128)])
+def test_long_and_many(n_seq, length, H, Hq, D, P):
+    g, pages, q = _big(n_seq, length, H, Hq, D, P)
+    lengths = [length - 997 * b % length for b in range(n_seq)]
+    out, lse = sp.spectra_attention_paged(g, pages, i32(lengths), q, out_dtype=torch.float32, want_lse=True)
+    want, wl_ = _plain_rows(g, pages, q, lengths, D ** -0.5)
+    # relative to the row: the FP32 score and weight roundings of the tolerances above, 2^-14 all told
+    assert ((out - want).norm(dim=-1) <= 2.0 ** -14 * want.norm(dim=-1)).all()
+    assert ((lse - wl_).abs() <= 2.0 ** -14).all()
+
+
+def test_offsets_past_32_bits():
+    """Entries whose code words lie more than 2^31 words into the pool."""
+    H, D, P = 8, 128, 1024
+    n_pages = 17000  # 139 M slots: 8.9 GB of K codes
+    g = sp.KVPool(H, D, P, n_pages, mass=True)
+    small = sp.KVPool(H, D, P, 2, mass=True)
+    x = torch.randn((2, 1500, H, D), device=DEV).bfloat16()
+    q = torch.randn((1, 16, D), device=DEV).bfloat16()
+    n = i32([1500])
+    far = torch.tensor([[n_pages - 1, n_pages - 9]], dtype=torch.int32, device=DEV)
+    near = i32([[0, 1]])
+    t = torch.arange(1500, device=DEV)
+    got = []
+    for pool, table, free in ((g, far, n_pages - 3), (small, near, None)):
+        slots = (table[0, t // P] * P + t % P).to(torch.int32)
+        pool.append(x[0], x[1], slots)
+        got.append([*pool.read(slots), sp.spectra_attention_paged(pool, table, n, q, update_mass=True)])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    m = sp.spectra_kv_evict(g, far, n, i32([[n_pages - 3]]), 300, 10)
+    t = torch.arange(300, device=DEV, dtype=torch.int32)
+    k, _ = g.read(t + (n_pages - 3) * P)
+    head = g.mass.view(n_pages, H, P)
+    for h in (0, 7):
+        mass = torch.cat([head[n_pages - 1, h], head[n_pages - 9, h]])[:1500].cpu().numpy()
+        keep = ref.evict(mass, 1500, 300, 10)
+        assert torch.equal(k[:, h], got[0][0][keep, h])
+    assert int(m) == 300
+
+
+def test_attention_refuses_values_out_of_bounds():
+    rng = np.random.default_rng(2)
+    p, pages, _ = filled(rng, [40, 40], 2, 64, 16)
+    g = device_pool(p)
+    q = torch.randn((2, 4, 64), device=DEV).bfloat16()
+    good = sp.spectra_attention_paged(g, i32(pages), i32([40, 40]), q, out_dtype=torch.float32)
+    sp.spectra_device_status()
+
+    def status():
+        with pytest.raises(sp.SpectraError) as e:
+            sp.spectra_device_status()
+        return e.value.status
+
+    # a page outside the pool hides its positions
+    for bad in (-1, p.n_pages, 2 ** 31 - 1):
+        hurt = pages.copy()
+        hurt[0, 1] = bad
+        out = sp.spectra_attention_paged(g, i32(hurt), i32([40, 40]), q, out_dtype=torch.float32)
+        assert status() == 1
+        assert torch.equal(out[1], good[1])
+        left = pages.copy()
+        left[0, 1] = pages[0, 2]  # the 16 + 8 positions that remain
+        want = sp.spectra_attention_paged(g, i32(left), i32([24, 40]), q, out_dtype=torch.float32)
+        assert torch.allclose(out[0], want[0], rtol=1e-4, atol=1e-5)
+    # a length out of range counts as 0
+    for bad in (-5, 3 * 16 + 1):
+        out = sp.spectra_attention_paged(g, i32(pages), i32([bad, 40]), q, out_dtype=torch.float32)
+        assert status() == 1 and not out[0].any() and torch.equal(out[1], good[1])
+    # rows out of range, or more than max_q, are left as they were
+    for start, max_q in (([0, 3, 2], 3), ([-1, 1, 2], 2), ([0, 1, 9], 9), ([0, 1, 2], 1), ([0, 2, 2], 1)):
+        out = torch.full((2, 4, 64), 7.0, device=DEV)
+        sp.spectra_attention_paged(g, i32(pages), i32([40, 40]), q, i32(start), max_q=max_q, out=out)
+        if start == [0, 1, 2]:
+            assert torch.equal(out, good)
+            sp.spectra_device_status()
+        else:
+            assert status() == 1 and (out == 7.0).any()
+
+
+def test_attention_streams_graphs_and_shared_workspace():
+    """Two captured graphs that share a workspace, replayed in turn with lengths
+    and pages changed in place; and calls on two streams at once."""
+    g, pages, q = _big(3, 2000, 2, 12, 128, 16, seed=3)
+    n = i32([2000, 777, 31])
+    ws = torch.empty(sp.library().spectra_attention_paged_workspace_size(g._ref, 3, 12), dtype=torch.uint8, device=DEV)
+    o1, o2 = torch.empty_like(q), torch.empty_like(q)
+    q2 = (q * 0.5).bfloat16()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    with torch.cuda.stream(s):
+        for qq, o in ((q, o1), (q2, o2)):
+            gr = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(gr, stream=s):
+                sp.spectra_attention_paged(g, pages, n, qq, out=o, workspace=ws)
+            graphs.append(gr)
+    for lengths in ([2000, 777, 31], [5, 0, 2000], [1024, 1, 16]):
+        n.copy_(i32(lengths))
+        pages.copy_(pages.flip(1))
+        torch.cuda.synchronize()
+        for gr in graphs + graphs:
+            gr.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o1, sp.spectra_attention_paged(g, pages, n, q))
+        assert torch.equal(o2, sp.spectra_attention_paged(g, pages, n, q2))
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = [sp.spectra_attention_paged(g, pages, n, qq, stream=st) for _ in range(20) for qq, st in ((q, a), (q2, b))]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, (o1, o2)[i % 2]) for i, o in enumerate(outs))
+    sp.spectra_device_status()
+
+
+# ---------------------------------------------------------------- eviction
+
+def check_evict(rng, lengths, H, D, P, budget, recent, ties=False, bad=False):
+    kept_pages = -(-budget // P)
+    p, pages, free = filled(rng, lengths, H, D, P, spare=kept_pages * len(lengths) + 1)
+    dst = free[:kept_pages * len(lengths)].reshape(len(lengths), kept_pages)
+    for b, n in enumerate(lengths):
+        for h in range(H):
+            m = np.exp(2 * rng.standard_normal(n)).astype(np.float32)
+            if ties:
+                m = np.round(m)
+            if bad and n > 3:
+                m[rng.integers(0, n, n // 4)] = np.nan
+                m[rng.integers(0, n)] = np.inf
+                m[rng.integers(0, n)] = -1.0
+                m[rng.integers(0, n)] = -0.0
+            p.mass[p.slot(token_slots(pages[b], n, P), h)] = m
+    g = device_pool(p)
+    got = sp.spectra_kv_evict(g, i32(pages), i32(lengths), i32(dst), budget, recent)
+    sp.spectra_device_status()
+    assert got.tolist() == [min(n, budget) for n in lengths]
+    for b, n in enumerate(lengths):
+        src, to = token_slots(pages[b], n, P), token_slots(dst[b], min(n, budget), P)
+        for h in range(H):
+            s = p.slot(src, h)
+            keep = ref.evict(p.mass[s], n, budget, recent)
+            s, d = s[keep] if n else s, p.slot(to, h)
+            for buf in p.buffers() + [p.mass]:
+                buf[d] = buf[s].copy()
+    same_buffers(g, p)  # everything else as it was
+
+
+@pytest.mark.parametrize("lengths,budget,recent", [([100, 20, 0, 33, 1], 32, 8), ([300], 299, 0), ([700, 257], 40, 40),
+                                                   ([256, 255, 513], 100, 1), ([64], 64, 10), ([50], 1, 0), ([50], 1, 1)])
+@pytest.mark.parametrize("kind", ["plain", "ties", "bad"])
+def test_evict(lengths, budget, recent, kind):
+    check_evict(np.random.default_rng(len(lengths) + budget), lengths, 2, 64, 16, budget, recent, kind == "ties",
+                kind == "bad")
+
+
+@pytest.mark.parametrize("H,D,P", [(1, 32, 16), (3, 96, 32), (2, 128, 128), (2, 256, 16), (1, 160, 64)])
+def test_evict_shapes(H, D, P):
+    check_evict(np.random.default_rng(D), [90, 150], H, D, P, 70, 5)
+
+
+def test_evict_long():
+    """A long sequence on the GPU alone: the entries that stay, by a stable sort."""
+    g, pages, _ = _big(2, 30000, 2, 2, 64, 64)
+    budget, recent, n = 5000, 100, [30000, 21111]
+    width = -(-budget // 64)
+    big = sp.KVPool(2, 64, 64, g.n_pages + 2 * width, mass=True)
+    for a, b in zip((big.k_codes, big.k_scales, big.k_zeros, big.v_codes, big.v_scales, big.v_zeros),
+                    (g.k_codes, g.k_scales, g.k_zeros, g.v_codes, g.v_scales, g.v_zeros)):
+        a[:b.numel()].copy_(b)
+    big.mass.exponential_()
+    big.mass.mul_(64).round_()  # many ties
+    dst = torch.arange(g.n_pages, big.n_pages, dtype=torch.int32, device=DEV).reshape(2, width)
+    got = sp.spectra_kv_evict(big, pages, i32(n), dst, budget, recent)
+    assert got.tolist() == [budget, budget]
+    i = torch.arange(budget, device=DEV)
+    for b in range(2):
+        t = torch.arange(n[b], device=DEV)
+        k, v = big.read((pages[b, t // 64] * 64 + t % 64).to(torch.int32))
+        kk, vv = big.read((dst[b, i // 64] * 64 + i % 64).to(torch.int32))
+        for h in range(2):
+            m = big.mass.view(-1, 2, 64)[pages[b].long(), h].flatten()[:n[b]]
+            old = n[b] - recent
+            best = torch.sort(m[:old], descending=True, stable=True).indices[:budget - recent].sort().values
+            keep = torch.cat([best, t[old:]])
+            assert torch.equal(kk[:, h], k[keep, h]) and torch.equal(vv[:, h], v[keep, h])
+            assert torch.equal(big.mass.view(-1, 2, 64)[dst[b].long(), h].flatten()[:budget], m[keep])
+
+
+def test_evict_reports_pages_out_of_bounds():
+    rng = np.random.default_rng(6)
+    p, pages, free = filled(rng, [60], 1, 64, 16, spare=4)
+    p.mass[p.slot(token_slots(pages[0], 60, 16), 0)] = rng.random(60)
+    g = device_pool(p)
+    before = [t.clone() for t in (g.k_codes, g.v_codes)]
+    sp.spectra_device_status()
+    got = sp.spectra_kv_evict(g, i32(pages), i32([60]), i32([[p.n_pages, -1]]), 20, 4)
+    with pytest.raises(sp.SpectraError) as e:
+        sp.spectra_device_status()
+    assert e.value.status == 1 and int(got) == 20
+    assert torch.equal(before[0], g.k_codes) and torch.equal(before[1], g.v_codes)
+    got = sp.spectra_kv_evict(g, i32(pages), i32([65]), i32(free[None, :2]), 20, 4)  # longer than its pages
+    with pytest.raises(sp.SpectraError):
+        sp.spectra_device_status()
+    assert int(got) == 0
+    with pytest.raises(sp.SpectraError) as e:
+        n = i32([60])
+        sp.spectra_kv_evict(g, i32(pages), n, i32(free[None, :2]), 20, 4, new_lengths=n)
+    assert e.value.status == 1
+    with pytest.raises(sp.SpectraError):
+        sp.spectra_kv_evict(device_pool(p, mass=False), i32(pages), i32([60]), i32(free[None, :2]), 20, 4)
+
+
+# ---------------------------------------------------------------- token choice
+
+def check_sample(x, u, temperature=None, top_k=None, top_p=None, min_p=None):
+    """x [rows, vocab] float32 (host).  Weights are rounded to 2^-45 of the
+    largest, so a running sum is off by vocab * 2^-45 at most; a row whose u is
+    nearer to a border than that may go either way and must not occur here.
+    The logarithm's tolerance: FP32's half step and the weights' rounding."""
+    dev = lambda a, dt=torch.float32: None if a is None else torch.tensor(a, dtype=dt, device=DEV)  # noqa: E731
+    ids, logp = sp.spectra_sample(torch.from_numpy(x).to(DEV), dev(u), temperature=dev(temperature),
+                                  top_k=dev(top_k, torch.int32), top_p=dev(top_p), min_p=dev(min_p))
+    f = lambda a, r, off: off if a is None else float(np.float32(a[r]))  # noqa: E731
+    for r in range(len(x)):
+        t, l, room = ref.sample(x[r], f(u, r, 0), f(temperature, r, 1.0), 0 if top_k is None else int(top_k[r]),
+                                f(top_p, r, 1.0), f(min_p, r, 0.0))
+        assert room > x.shape[1] * 2.0 ** -45
+        assert int(ids[r]) == t, (r, int(ids[r]), t)
+        assert float(logp[r]) == l or abs(float(logp[r]) - l) <= 2.0 ** -24 * abs(l) + x.shape[1] * 2.0 ** -44
+    return ids
+
+
+SETTINGS = [dict(), dict(top_k=[1, 3, 50, 0]), dict(top_p=[0.9, 0.5, 1e-6, 0.999]), dict(min_p=[0.0, 0.1, 0.9, 2.0]),
+            dict(top_k=[40, 7, 10 ** 6, 2], top_p=[0.8, 0.3, 0.95, 1.5], min_p=[0.02, 0.0, 0.05, 0.0]),
+            dict(temperature=[1.0, 0.3, 5.0, 0.01]), dict(temperature=[0.0, -1.0, float("nan"), 1e-20]),
+            dict(temperature=[0.7, 1.3, 2.0, 0.5], top_k=[20, 0, 300, 64], top_p=[0.0, 0.7, 0.99, 0.5])]
+
+
+@pytest.mark.parametrize("kw", SETTINGS, ids=range(len(SETTINGS)))
+@pytest.mark.parametrize("vocab", [1, 2, 31, 1000, 1025, 32003, 131072])
+def test_sample(vocab, kw):
+    rng = np.random.default_rng(vocab)
+    x = (3 * rng.standard_normal((4, vocab))).astype(np.float32)
+    check_sample(x, rng.random(4).astype(np.float32), **kw)
+
+
+def test_sample_largest_vocabulary():
+    rng = np.random.default_rng(1)
+    x = (2 * rng.standard_normal((2, 524288))).astype(np.float32)
+    check_sample(x, [0.3, 0.9999999], top_p=[0.9, 1.0], top_k=[0, 500])
+    check_sample(np.zeros((2, 524288), np.float32), [0.25 + 1e-7, 0.9999999])  # all equal: the largest sum
+
+
+def test_sample_ties_and_masks():
+    rng = np.random.default_rng(2)
+    inf = np.inf
+    x = np.full((8, 3000), -inf, np.float32)
+    x[0, 17] = 5.0                      # one token left
+    x[1, [5, 9, 2000]] = 1.0            # ties, cut by top-k: the lower indexes
+    x[2] = 0.0                          # all equal: top-p keeps the first 1500
+    x[3, ::7] = rng.standard_normal(429)
+    x[4] = rng.integers(0, 3, 3000)     # three values: ties everywhere
+    x[5, [3, 2900]] = inf
+    x[6] = np.where(rng.random(3000) < 0.5, 0.0, -0.0)
+    x[7, 1] = -3e38
+    x[7, 2] = 3e38
+    top_k = [0, 2, 0, 100, 1200, 0, 700, 0]
+    top_p = [1.0, 1.0, 0.5, 0.9, 0.6, 1.0, 0.5, 1.0]
+    for u in (0.01, 0.51, 0.985):
+        check_sample(x, [u] * 8, top_k=top_k, top_p=top_p)
+    check_sample(x, [0.985] * 8, top_k=top_k, top_p=top_p, temperature=[0.5] * 8)
+    assert check_sample(x, [0.985] * 8, temperature=[0.0] * 8).tolist()[:3] == [17, 5, 0]
+
+
+def test_sample_u_at_its_ends():
+    x = np.log(np.array([[1.0, 2.0, 0.0, 5.0, 0.0]] * 3, np.float64) + 1e-300).astype(np.float32)
+    x[:, [2, 4]] = -np.inf
+    ids, _ = sp.spectra_sample(torch.from_numpy(x).to(DEV), torch.tensor([0.0, 1.0, float("nan")], device=DEV))
+    assert ids.tolist() == [0, 3, 0]  # never a masked token
+    ids, _ = sp.spectra_sample(torch.from_numpy(x).to(DEV), torch.tensor([-3.0, 7.0, float("inf")], device=DEV))
+    assert ids.tolist() == [0, 3, 3]
+
+
+def test_sample_reports_nan_and_empty_rows():
+    sp.spectra_device_status()
+    x = torch.zeros((3, 100), device=DEV)
+    x[1] = -float("inf")
+    u = torch.tensor([0.5, 0.5, 0.5], device=DEV)
+    ids, logp = sp.spectra_sample(x, u)
+    assert ids.tolist()[1] == -1 and float(logp[1]) == -float("inf") and ids.tolist()[0] >= 0
+    with pytest.raises(sp.SpectraError) as e:
+        sp.spectra_device_status()
+    assert e.value.status == 1
+    x[1] = 0.0
+    x[2] = float("nan")
+    x[2, 60] = 1.0
+    ids, _ = sp.spectra_sample(x, u, top_p=torch.full((3,), 0.9, device=DEV))
+    assert int(ids[2]) == 60
+    with pytest.raises(sp.SpectraError) as e:
+        sp.spectra_device_status()
+    assert e.value.status == 4
+    sp.spectra_device_status()
+
+
+def test_sample_strided_rows_and_one_row():
+    rng = np.random.default_rng(8)
+    wide = torch.from_numpy(rng.standard_normal((5, 4001)).astype(np.float32)).to(DEV)
+    u = torch.from_numpy(rng.random(5).astype(np.float32)).to(DEV)
+    a, la = sp.spectra_sample(wide[:, 1:3998], u)
+    b, lb = sp.spectra_sample(wide[:, 1:3998].contiguous(), u)
+    assert torch.equal(a, b) and torch.equal(la, lb)
+    c, _ = sp.spectra_sample(wide[2, 1:3998], u[2:3])
+    assert int(c) == int(a[2])
+    assert sp.spectra_sample(wide[:0], u[:0])[0].shape == (0,)
+    with pytest.raises(ValueError):
+        sp.spectra_sample(wide.t(), torch.zeros(4001, device=DEV))
+
+
+# ---------------------------------------------------------------- together
+
+def test_decoding_a_batch():
+    """A prompt and a few steps of one attention layer and the LM head, as a
+    batch decodes: project, append, attend with accumulated weights, project,
+    choose a token, embed it; then evict and go on.  Every operator's inputs
+    are the previous one's outputs; each is checked against its 64-bit form."""
+    rng = np.random.default_rng(30)
+    H, Hq, D, P, vocab, n_seq = 2, 6, 64, 16, 1000, 3
+    hidden = Hq * D
+    mk = lambda n, k: sp.pack_layer((torch.randn((n, k), device=DEV) * 0.05).bfloat16(), None, 3.0)  # noqa: E731
+    torch.manual_seed(1)
+    wq, wk, wv, wo, head = mk(hidden, hidden), mk(H * D, hidden), mk(H * D, hidden), mk(hidden, hidden), mk(vocab, hidden)
+    prompts = [20, 7, 33]
+    p = ref.Pool(H, D, P, 40, rng)
+    g = device_pool(p)
+    free = list(rng.permutation(40))
+    pages = np.array([[free.pop() for _ in range(4)] for _ in range(n_seq)], np.int32)
+    length = [0] * n_seq
+
+    def step(x, rows):
+        """x BF16 [sum(rows), hidden]: the new tokens of every sequence."""
+        n = x.shape[0]
+        proj = lambda w: torch.cat([sp.spectra_gemm_small(w, x[i:i + 32].contiguous(), y_dtype=torch.bfloat16)  # noqa: E731
+                                    for i in range(0, n, 32)])
+        q, k, v = proj(wq), proj(wk), proj(wv)
+        slots = np.concatenate([token_slots(pages[b], length[b] + m, P)[length[b]:] for b, m in enumerate(rows)])
+        for b, m in enumerate(rows):
+            length[b] += m
+        k, v, q = (t.unflatten(1, (-1, D)) for t in (k, v, q))
+        g.append(k, v, i32(slots))
+        p.append(wl.bits(k), wl.bits(v), slots)
+        start = np.concatenate([[0], np.cumsum(rows)])
+        o = sp.spectra_attention_paged(g, i32(pages), i32(length), q.contiguous(), i32(start), max_q=max(rows),
+                                       update_mass=True)
+        want, _, add, to, _, tm = ref.attention(p, pages, length, q.double().cpu().numpy(), start,
+                                                float(np.float32(D ** -0.5)))
+        assert (np.abs(o.double().cpu().numpy() - want) <= to + BF16_HALF * (np.abs(want) + to)).all()
+        err = np.abs(g.mass.double().cpu().numpy() - (p.mass + add))
+        used = add > 0
+        assert (err[used] <= (tm + 2.0 ** -23 * (p.mass + add))[used]).all()
+        p.mass = g.mass.cpu().numpy()
+        last = i32(start[1:] - 1).long()
+        y = sp.spectra_gemm_small(wo, o.flatten(1)[last].contiguous(), y_dtype=torch.bfloat16)
+        logits = sp.spectra_gemm_small(head, y)
+        u = torch.from_numpy(rng.random(n_seq).astype(np.float32)).to(DEV)
+        kw = dict(temperature=torch.full((n_seq,), 0.8, device=DEV), top_p=torch.full((n_seq,), 0.9, device=DEV),
+                  top_k=i32([50] * n_seq))
+        ids, _ = sp.spectra_sample(logits, u, **kw)
+        for b in range(n_seq):
+            assert int(ids[b]) == ref.sample(logits[b].cpu().numpy(), float(u[b]), float(np.float32(0.8)), 50,
+                                             float(np.float32(0.9)))[0]
+        return sp.spectra_embed(head, ids)
+
+    x = step(torch.randn((sum(prompts), hidden), device=DEV).bfloat16(), prompts)
+    for _ in range(4):
+        x = step(x, [1] * n_seq)
+    fresh = np.array([[free.pop() for _ in range(2)] for _ in range(n_seq)], np.int32)
+    n = sp.spectra_kv_evict(g, i32(pages), i32(length), i32(fresh), 18, 6)
+    for b in range(n_seq):
+        src, to = token_slots(pages[b], length[b], P), token_slots(fresh[b], min(length[b], 18), P)
+        for h in range(H):
+            s, d = p.slot(src, h), p.slot(to, h)
+            s = s[ref.evict(p.mass[s], length[b], 18, 6)]
+            for buf in p.buffers() + [p.mass]:
+                buf[d] = buf[s].copy()
+    same_buffers(g, p)
+    length = n.tolist()
+    pages = fresh
+    for _ in range(3):
+        x = step(x, [1] * n_seq)
+    sp.spectra_device_status()
+
+
+def test_calls_on_a_stream_of_their_own():
+    """append, read, evict and sample on a side stream, ordered there alone."""
+    H, D, P, n = 2, 128, 16, 64
+    s = torch.cuda.Stream()
+    x = torch.randn((2, n, H, D), device=DEV).bfloat16()
+    slots = torch.arange(n, dtype=torch.int32, device=DEV)
+    g = sp.KVPool(H, D, P, 8, mass=True)
+    logits = torch.randn((2, 5000), device=DEV)
+    u = torch.tensor([0.2, 0.7], device=DEV)
+    want = sp.spectra_sample(logits, u)[0]
+    ref_pool = sp.KVPool(H, D, P, 8, mass=True)
+    ref_pool.append(x[0], x[1], slots)
+    torch.cuda.synchronize()
+    g.append(x[0], x[1], slots, stream=s)
+    k, v = g.read(slots, stream=s)
+    m = sp.spectra_kv_evict(g, i32([[0, 1, 2, 3]]), i32([n]), i32([[5]]), 16, 16, stream=s)
+    ids, _ = sp.spectra_sample(logits, u, stream=s.cuda_stream)
+    s.synchronize()
+    assert torch.equal(k, ref_pool.read(slots)[0]) and torch.equal(v, ref_pool.read(slots)[1])
+    assert int(m) == 16 and torch.equal(ids, want)
+    assert torch.equal(g.read(slots[:16] + 5 * P)[0], k[-16:])
+
+
+def test_all_operators_captured():
+    """append, attention, eviction and the sampler in one graph, replayed."""
+    H, Hq, D, P = 2, 4, 64, 16
+    g = sp.KVPool(H, D, P, 12, mass=True)
+    x = torch.randn((2, 40, H, D), device=DEV).bfloat16()
+    slots = torch.arange(40, dtype=torch.int32, device=DEV)
+    table, n, dst = i32([[0, 1, 2]]), i32([40]), i32([[7, 8]])
+    q = torch.randn((1, Hq, D), device=DEV).bfloat16()
+    logits, u = torch.randn((1, 3001), device=DEV), torch.tensor([0.4], device=DEV)
+
+    def all_of():
+        g.append(x[0], x[1], slots)
+        o = sp.spectra_attention_paged(g, table, n, q, update_mass=True)
+        m = sp.spectra_kv_evict(g, table, n, dst, 20, 4)
+        return o, m, *g.read(slots[:20] + 7 * P), *sp.spectra_sample(logits, u)
+
+    want = [t.clone() for t in all_of()]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr, stream=s):
+        got = all_of()
+    for _ in range(3):
+        gr.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    x.copy_(x.flip(1))
+    gr.replay()
+    torch.cuda.synchronize()
+    assert not torch.equal(got[2], want[2])  # the entries; attention alone does not see their order
+    want = all_of()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
