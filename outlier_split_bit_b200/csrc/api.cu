@@ -622,7 +622,7 @@ size_t spectra_attention_paged_workspace_size(const spectra_kv_pool *pool, int32
     if (!pool || check_pool_shape(pool->n_heads, pool->head_dim, pool->page_size, pool->n_pages) != SPECTRA_OK ||
         n_rows < 0 || !paged_heads_ok(pool, n_q_heads))
         return 0;
-    return paged_workspace_bytes(n_rows, n_q_heads, pool->head_dim);
+    return paged_workspace_bytes(n_rows, n_q_heads, pool->n_heads, pool->head_dim);
 }
 
 spectra_status spectra_attention_paged(const spectra_kv_pool *pool, const spectra_paged_query *x,
@@ -640,10 +640,12 @@ spectra_status spectra_attention_paged(const spectra_kv_pool *pool, const spectr
     if (!x->pages || !x->lengths || !x->q || !x->out || !workspace) return SPECTRA_ERR_INVALID_ARG;
     if (!x->q_start && x->n_rows != x->n_seq) return SPECTRA_ERR_SHAPE;
     if ((int64_t)x->n_rows * x->n_q_heads >= ((int64_t)1 << 31)) return SPECTRA_ERR_SHAPE;
+    const int64_t longest = x->max_q < x->n_rows ? x->max_q : x->n_rows;
+    if (longest * (x->n_q_heads / pool->n_heads) >= ((int64_t)1 << 24)) return SPECTRA_ERR_SHAPE;
     if (!aligned4(x->pages) || !aligned4(x->lengths) || !aligned4(x->q_start) || !aligned4(x->slopes) ||
         !aligned4(x->lse) || !aligned16(x->q) || !aligned16(x->out) || !aligned16(workspace))
         return SPECTRA_ERR_ALIGN;
-    if (workspace_bytes < paged_workspace_bytes(x->n_rows, x->n_q_heads, pool->head_dim))
+    if (workspace_bytes < paged_workspace_bytes(x->n_rows, x->n_q_heads, pool->n_heads, pool->head_dim))
         return SPECTRA_ERR_BUFFER_TOO_SMALL;
     DeviceInfo dev;
     st = current_device(&dev);

@@ -151,7 +151,7 @@ spectra_status launch_evict(const spectra_kv_pool &pool, const int32_t *pages, i
 spectra_status pool_device_error(unsigned int *bits, cudaStream_t s);
 
 // ---- attention over the pool (paged.cu) ----
-size_t paged_workspace_bytes(int n_rows, int n_q_heads, int head_dim);
+size_t paged_workspace_bytes(int n_rows, int n_q_heads, int n_kv_heads, int head_dim);
 spectra_status launch_paged_attention(const spectra_kv_pool &pool, const spectra_paged_query &x, void *ws,
                                       cudaStream_t s, const DeviceInfo &dev);
 // Reads (and clears) its flag (bit 2 as pool_device_error).

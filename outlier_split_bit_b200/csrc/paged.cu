@@ -11,14 +11,55 @@
 //   over the t with 0 <= pos - t (and pos - t < window, with a window),
 //   out = sum_t softmax(s)_t v_t,  lse = log sum_t exp(s_t),
 //   mass[h][t] += sum over the group's heads and the tokens of softmax(s)_t.
+//
+// One pass over K and V.  A KV head's queries (tokens x group heads) are the
+// columns of a tile of 8 * NT; a warp takes 16 positions (a unit) at a time
+// and multiplies them on the tensor cores, m16n8k16 with FP32 accumulation:
+//   scores: A = 16 positions x 16 channels of K, B = q.  A code enters as the
+//     exact BF16 integer c - z (128 + c by or-ing the nibble under 0x4300,
+//     minus 128 + z), so the product sums are exact up to FP32 accumulation,
+//     and each group's sum is multiplied by its scale in FP32;
+//   weighted sum: A = 16 channels x 16 positions of V (the same integers), B =
+//     weight times V's scale, one per position and group, split into two BF16
+//     pieces (2^-16 of a weight is lost), each a product of its own.
+// The scores' accumulator layout (positions in rows) is transposed into the
+// weights' operand layout inside the warp (movmatrix on the two halves of the
+// FP32 bits).  Which lane holds which channel or position is free as long as
+// both operands agree, so the pool's words are laid out to be read with one
+// load per position: lane (g, t) = (lane / 4, lane % 4) reads K's word t of
+// every group of positions g', g' + 8 and V's halfword g of every group of
+// positions t, t + 4, t + 8, t + 12.
+//
+// The running maximum is only a reference: it moves when a score passes it by
+// 8 or more (in base 2), so most units need no reduction over the lanes and no
+// rescaling; weights up to 2^8 are as good as weights up to 1 in FP32.
+//
+// Work split: the tiles (64 positions, one unit per warp) of every (sequence,
+// head, column tile) make one list, cut into equal runs, one per CTA, from
+// the lengths on the device; so ragged batches balance and the host need not
+// know the lengths.  A run's first and last piece may be part of a longer item;
+// such pieces go to the workspace (at most two per CTA) and a second kernel,
+// launched as a programmatic dependent, joins them in order.  Every order is
+// fixed, so results repeat bit for bit.
 #include "internal.cuh"
 #include "pool.cuh"
+#include "select.cuh"
 
 namespace spectra {
 namespace {
 
 // bit 2: a page outside the pool, a length or a row range out of bounds.
 __device__ unsigned int g_paged_error;
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kUnit = 16;                // positions of a warp's step
+constexpr int kTile = kUnit * kWarps;    // positions of a CTA's step
+constexpr int kMaxCtas = 148 * 4;        // runs: one wave of the smallest variant's CTAs
+constexpr int kMinTiles = 2;             // tiles of a run, at least (fewer pieces to join)
+constexpr float kSlack = 8.f;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 struct PagedArgs {
     PoolView p;
@@ -29,6 +70,9 @@ struct PagedArgs {
     const float *slopes;
     void *out;
     float *lse;
+    float *ws_acc;   // [2 * runs][columns][D]
+    float2 *ws_ml;   // [2 * runs][columns]: reference, sum
+    int4 *ws_item;   // [runs]: an item cut at the run's end: (last run, first row, columns, head); last run -1: none
     int max_pages, n_seq, n_rows, max_q, Hq, grp, window;
     float scale, cap;
     bool bf16;
@@ -49,140 +93,787 @@ __device__ __forceinline__ Sequence sequence_of(const PagedArgs &a, int b) {
         s.n = 0;
         bad = true;
     }
-    if (s.row0 < 0 || row1 > a.n_rows || s.m < 0 || s.m > a.max_q) {
+    if (s.row0 < 0 || row1 > a.n_rows || row1 < s.row0 || s.m > a.max_q) {
         s.m = 0;
         bad = true;
     }
-    if (bad && threadIdx.x == 0) atomicOr(&g_paged_error, 4u);
+    if (bad) atomicOr(&g_paged_error, 4u);
     return s;
 }
 
-constexpr int kThreads = 128;
-
-__device__ __forceinline__ float score(const PagedArgs &a, float dot, float slope, int gap) {
-    float s = dot * a.scale;
-    if (a.cap > 0.f) s = a.cap * tanhf(s / a.cap);
-    return s - slope * (float)gap;
+// Tiles of a sequence: from the one with the first visible position, at
+// least one (an item without positions still writes its zeros).
+struct Tiles {
+    int first, count;
+};
+__device__ __forceinline__ Tiles tiles_of(const PagedArgs &a, const Sequence &s) {
+    const int64_t lo = a.window > 0 ? (int64_t)s.n - s.m - a.window + 1 : 0;
+    Tiles t;
+    t.first = lo > 0 ? (int)(lo / kTile) : 0;
+    t.count = max(1, (s.n + kTile - 1) / kTile - t.first);
+    return t;
 }
 
-__device__ __forceinline__ float k_dot(const PagedArgs &a, int64_t slot, const uint16_t *q) {
-    const int G = a.p.G;
-    float dot = 0.f;
-    const uint32_t zw = a.p.kz[slot];
-    for (int g = 0; g < G; ++g) {
-        float part = 0.f;
-        const int z = (int)((zw >> (4 * g)) & 15u);
-        for (int w = 0; w < 4; ++w) {
-            const uint32_t word = a.p.kc[slot * 4 * G + w * G + g];
-            for (int i = 0; i < 8; ++i)
-                part = fmaf((float)((int)((word >> (4 * i)) & 15u) - z),
-                            __uint_as_float((uint32_t)q[32 * g + 8 * w + i] << 16), part);
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// (hi, lo) rounded to BF16, lo in the lower half.
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+    uint32_t y;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+    return y;
+}
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&a),
+                                     *reinterpret_cast<const __nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+// Nibble j of both halfwords as the BF16 pair 128 + c, 128 + c'.
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, int j) { return ((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u; }
+
+// Row r of a unit's 16 (as the tensor core counts them) is its position
+// unit_position(r): rows 2t, 2t+1, 2t+8, 2t+9 are t, t+4, t+8, t+12.
+__device__ __forceinline__ int unit_position(int r) { return (r & 8) | ((r & 1) << 2) | ((r & 7) >> 1); }
+
+// N 32-bit words, or N halfwords in (N + 1) / 2 words, from p with the widest
+// loads that their alignment (the size's own) allows.
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&r)[N], const uint32_t *p) {
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p + i);
+            r[i] = v.x; r[i + 1] = v.y; r[i + 2] = v.z; r[i + 3] = v.w;
         }
-        dot = fmaf(__half2float(__ushort_as_half(a.p.ks[slot * G + g])), part, dot);
+    } else if constexpr (N % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(p + i);
+            r[i] = v.x; r[i + 1] = v.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) r[i] = p[i];
     }
-    return dot;
+}
+template <int N>
+__device__ __forceinline__ void load_halfwords(uint32_t (&r)[(N + 1) / 2], const uint16_t *p) {
+    if constexpr (N % 2 == 0) {
+        load_words<N / 2>(r, reinterpret_cast<const uint32_t *>(p));
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) r[i / 2] = (uint32_t)p[i] | (i + 1 < N ? (uint32_t)p[i + 1] << 16 : 0u);
+    }
+}
+__device__ __forceinline__ float half_of(uint32_t w, int which) {
+    return __half2float(__ushort_as_half((unsigned short)(which ? w >> 16 : w & 0xFFFFu)));
 }
 
-// One CTA per sequence, query row and query head; a thread per position for
-// the scores, a thread per channel for the weighted sum.
-__global__ void __launch_bounds__(kThreads) paged_attention_kernel(PagedArgs a) {
-    __shared__ float w[kThreads];
-    __shared__ int64_t at[kThreads];
-    __shared__ float red[kThreads / 32];
-    const int i = blockIdx.x, j = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, D = 32 * a.p.G;
-    const Sequence s = sequence_of(a, b);
-    if (j >= s.m) return;
-    const int h = i / a.grp, pos = s.n - s.m + j;
-    const int first = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-    const int64_t row = (int64_t)(s.row0 + j) * a.Hq + i;
-    const uint16_t *q = a.q + row * D;
-    const float slope = a.slopes ? a.slopes[i] : 0.f;
-    const int32_t *pages = a.pages + (int64_t)b * a.max_pages;
-    float m = -INFINITY, l = 0.f, acc[2] = {0.f, 0.f};
-    for (int t0 = first; t0 <= pos; t0 += kThreads) {
-        const int t = t0 + tid;
-        float x = -INFINITY;
-        int64_t slot = -1;
-        if (t <= pos) {
-            const int32_t ts = a.p.token_slot(pages, t);
-            if (ts < 0) {
-                atomicOr(&g_paged_error, 4u);
+// One unit's K for this lane: rows lane/4 and lane/4 + 8.
+template <int G>
+struct KUnit {
+    uint32_t w[2][G];
+    uint32_t s[2][(G + 1) / 2];
+    uint32_t z[2];
+    __device__ __forceinline__ void load(const PoolView &p, int64_t base, int lane) {
+        const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int64_t slot = base + unit_position(g + 8 * r);
+            load_words<G>(w[r], p.kc + slot * (4 * G) + t * G);
+            load_halfwords<G>(s[r], p.ks + slot * G);
+            z[r] = p.kz[slot];
+        }
+    }
+    // The A operands of group gr, k-steps 0 and 1.
+    __device__ __forceinline__ void operands(int gr, uint32_t (&a0)[4], uint32_t (&a1)[4]) const {
+        uint32_t x[2][4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const uint32_t zz = (((z[r] >> (4 * gr)) & 0xFu) | 0x4300u) * 0x10001u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[r][j] = sub_bf16x2(code_pair(w[r][gr], j), zz);
+        }
+        a0[0] = x[0][0]; a0[1] = x[1][0]; a0[2] = x[0][1]; a0[3] = x[1][1];
+        a1[0] = x[0][2]; a1[1] = x[1][2]; a1[2] = x[0][3]; a1[3] = x[1][3];
+    }
+};
+
+// One unit's V for this lane: positions t, t + 4, t + 8, t + 12 (t = lane % 4),
+// channels 4g .. 4g + 3 of every group (g = lane / 4).
+template <int G>
+struct VUnit {
+    static constexpr int W = (G + 1) / 2;
+    uint32_t w[4][W];
+    uint32_t s[4][W];
+    uint32_t z[4];
+    // Entries past the sequence may hold anything: their scales become 0.
+    __device__ __forceinline__ void load(const PoolView &p, int64_t base, int lane, int left) {
+        const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t slot = base + t + 4 * i;
+            load_halfwords<G>(w[i], p.vc + slot * (8 * G) + g * G);
+            load_halfwords<G>(s[i], p.vs + slot * G);
+            z[i] = p.vz[slot];
+        }
+        if (left < kUnit) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (t + 4 * i >= left)
+#pragma unroll
+                    for (int k = 0; k < W; ++k) s[i][k] = 0u;
+        }
+    }
+    // The A operands of group gr: channels (4g, 4g + 1) and (4g + 2, 4g + 3).
+    __device__ __forceinline__ void operands(int gr, uint32_t (&a0)[4], uint32_t (&a1)[4]) const {
+        const uint32_t pick = gr & 1 ? 0x7632u : 0x5410u;
+        uint32_t x[2][4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const uint32_t c = __byte_perm(w[2 * r][gr / 2], w[2 * r + 1][gr / 2], pick);
+            // the two positions' zero points, each in its half
+            const uint32_t zz = code_pair(__byte_perm(z[2 * r], z[2 * r + 1], gr < 4 ? 0x5410u : 0x7632u), gr & 3);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[r][j] = sub_bf16x2(code_pair(c, j), zz);
+        }
+        a0[0] = x[0][0]; a0[1] = x[0][1]; a0[2] = x[1][0]; a0[3] = x[1][1];
+        a1[0] = x[0][2]; a1[1] = x[0][3]; a1[2] = x[1][2]; a1[3] = x[1][3];
+    }
+};
+
+// The B operands of one query vector's group gr (8 channels of the lane's t):
+// pairs (q0, q4), (q1, q5) of k-step 0 and (q2, q6), (q3, q7) of k-step 1, the
+// order in which code_pair takes a word's nibbles.
+__device__ __forceinline__ uint4 query_operands(const uint16_t *q, int gr, int t) {
+    const uint4 v = *reinterpret_cast<const uint4 *>(q + 32 * gr + 8 * t);
+    return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
+                      __byte_perm(v.y, v.w, 0x7632));
+}
+
+// tanh to an absolute 2^-21 or so.
+__device__ __forceinline__ float tanh_abs(float y) { return 1.f - __fdividef(2.f, ex2(2.f * kLog2e * y) + 1.f); }
+
+// What turns a product sum into a score in base 2.
+struct Score {
+    float mul, cap;  // without a cap: s = mul * dot; with: cap * tanh(mul * dot)
+    bool capped;
+    __device__ __forceinline__ explicit Score(const PagedArgs &a) {
+        capped = a.cap > 0.f;
+        mul = capped ? a.scale / a.cap : a.scale * kLog2e;
+        cap = a.cap * kLog2e;
+    }
+    __device__ __forceinline__ float operator()(float dot) const {
+        const float y = mul * dot;
+        return capped ? cap * tanh_abs(y) : y;
+    }
+};
+
+// The first position of the unit's page slots for head h, -1 without a page.
+__device__ __forceinline__ int64_t unit_base(const PoolView &p, int32_t page, int t0, int h) {
+    if ((uint32_t)page >= (uint32_t)p.n_pages) {
+        atomicOr(&g_paged_error, 4u);
+        return -1;
+    }
+    return (((int64_t)page * p.H + h) << p.lp) + (t0 & ((1 << p.lp) - 1));
+}
+
+// This CTA's run of the tile list and where it starts: sequence b, `off` tiles
+// into it.
+struct Run {
+    int64_t cur, end, total;
+    int64_t off;
+    int b, runs;
+};
+
+// per_seq(b): tiles of sequence b in the list.
+template <class F>
+__device__ __forceinline__ Run find_run(const F &per_seq, int n_seq, int run, int max_runs, int64_t *part,
+                                        int64_t *found) {
+    const int tid = threadIdx.x, per = (n_seq + kThreads - 1) / kThreads;
+    const int b0 = min(n_seq, tid * per), b1 = min(n_seq, b0 + per);
+    int64_t own = 0;
+    for (int b = b0; b < b1; ++b) own += per_seq(b);
+    Run r;
+    int64_t before = block_exclusive(own, part, &r.total);
+    const int64_t want = (r.total + kMinTiles - 1) / kMinTiles;
+    r.runs = (int)(want < max_runs ? want : max_runs);
+    if (run >= r.runs) {
+        r.cur = r.end = r.off = 0;
+        r.b = 0;
+        return r;
+    }
+    r.cur = run * r.total / r.runs;
+    r.end = (run + 1) * r.total / r.runs;
+    if (before <= r.cur && r.cur < before + own) {
+        for (int b = b0;; ++b) {
+            const int64_t n = per_seq(b);
+            if (r.cur < before + n) {
+                found[0] = b;
+                found[1] = r.cur - before;
+                break;
+            }
+            before += n;
+        }
+    }
+    __syncthreads();
+    r.b = (int)found[0];
+    r.off = found[1];
+    return r;
+}
+
+// The run that holds tile t of the list.
+__device__ __forceinline__ int run_of(int64_t t, const Run &r) { return (int)(((t + 1) * r.runs - 1) / r.total); }
+
+template <int G, int NT>
+constexpr int min_ctas() {
+    return G * NT <= 4 ? 4 : (G * NT <= 8 ? 2 : 1);
+}
+
+template <int G, int NT>
+__global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_kernel(const PagedArgs a) {
+    constexpr int D = 32 * G, C = 8 * NT, kRow = D + 4;  // kRow: a padded column of the exchange buffer
+    extern __shared__ __align__(16) unsigned char smem[];
+    float *xch = reinterpret_cast<float *>(smem);                      // [kWarps][8][kRow]
+    uint4 *qs = reinterpret_cast<uint4 *>(smem + kWarps * 8 * kRow * 4);  // NT > 1: [NT][G][32]
+    __shared__ float2 s_ml[kWarps][C];
+    __shared__ int64_t s_part[33], s_found[2];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+    const PoolView &p = a.p;
+    const Score score(a);
+
+    // the join may be launched: it waits for this grid's end before it reads
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    auto per_seq = [&](int b) -> int64_t {
+        const Sequence s = sequence_of(a, b);
+        return s.m == 0 ? 0 : (int64_t)p.H * ((s.m * a.grp + C - 1) / C) * tiles_of(a, s).count;
+    };
+    Run run = find_run(per_seq, a.n_seq, blockIdx.x, gridDim.x, s_part, s_found);
+    int4 cut = make_int4(-1, 0, 0, 0);
+    int b = run.b;
+    while (run.cur < run.end) {
+        const Sequence s = sequence_of(a, b);
+        const Tiles tiles = tiles_of(a, s);
+        const int ncols = s.m * a.grp, n_ct = (ncols + C - 1) / C;
+        if (s.m == 0 || run.off >= (int64_t)p.H * n_ct * tiles.count) {
+            ++b;
+            run.off = 0;
+            continue;
+        }
+        const int item = (int)(run.off / tiles.count);
+        const int ta = (int)(run.off - (int64_t)item * tiles.count);
+        const int tb = (int)min((int64_t)tiles.count, ta + (run.end - run.cur));
+        const int h = item / n_ct, c0 = (item - h * n_ct) * C;
+        const int cols = min(C, ncols - c0);
+        // the columns of this lane: 2 per n-tile, their positions and slopes
+        int pos[NT][2];
+        float slope[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int c = c0 + min(8 * nt + 2 * t4 + e, cols - 1);
+                pos[nt][e] = s.n - s.m + c / a.grp;
+                slope[nt][e] = a.slopes ? a.slopes[h * a.grp + c % a.grp] * kLog2e : 0.f;
+            }
+        const int pos_lo = s.n - s.m + c0 / a.grp, pos_hi = s.n - s.m + (c0 + cols - 1) / a.grp;
+        const int vis_lo = a.window > 0 ? max(0, pos_lo - a.window + 1) : 0;  // the first position any column sees
+        // queries: column g of every n-tile (zeros past the last column)
+        uint4 qf[G];
+        const uint16_t *qrow = nullptr;
+        {
+            if constexpr (NT == 1) {
+                if (g < cols) {
+                    const int c = c0 + g;
+                    qrow = a.q + ((int64_t)(s.row0 + c / a.grp) * a.Hq + h * a.grp + c % a.grp) * D;
+                }
+#pragma unroll
+                for (int gr = 0; gr < G; ++gr)
+                    qf[gr] = qrow ? query_operands(qrow, gr, t4) : make_uint4(0u, 0u, 0u, 0u);
             } else {
-                slot = a.p.slot(ts, h);
-                x = score(a, k_dot(a, slot, q), slope, pos - t);
+                for (int nt = warp; nt < NT; nt += kWarps) {
+                    qrow = nullptr;
+                    if (8 * nt + g < cols) {
+                        const int c = c0 + 8 * nt + g;
+                        qrow = a.q + ((int64_t)(s.row0 + c / a.grp) * a.Hq + h * a.grp + c % a.grp) * D;
+                    }
+#pragma unroll
+                    for (int gr = 0; gr < G; ++gr)
+                        qs[(nt * G + gr) * 32 + lane] = qrow ? query_operands(qrow, gr, t4) : make_uint4(0u, 0u, 0u, 0u);
+                }
+                __syncthreads();
             }
         }
-        float mx = x;
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        __syncthreads();
-        if ((tid & 31) == 0) red[tid >> 5] = mx;
-        __syncthreads();
-        mx = m;
-        for (int k = 0; k < kThreads / 32; ++k) mx = fmaxf(mx, red[k]);
-        const float old = mx == -INFINITY ? 1.f : expf(m - mx);
-        m = mx;
-        w[tid] = x == -INFINITY ? 0.f : expf(x - m);
-        at[tid] = slot;
-        __syncthreads();
-        l *= old;
-        for (int k = 0; k < kThreads; ++k) l += w[k];
-        for (int e = 0; e < 2; ++e) {
-            const int d = tid + e * kThreads;
-            acc[e] *= old;
-            if (d >= D) continue;
-            const int g = d >> 5, hw = (d & 31) >> 2, sh = 4 * (d & 3);
-            for (int k = 0; k < kThreads; ++k) {
-                if (at[k] < 0) continue;
-                const uint32_t word = a.p.vc[at[k] * 8 * a.p.G + hw * a.p.G + g];
-                const int z = (int)((a.p.vz[at[k]] >> (4 * g)) & 15u);
-                const float v = (float)((int)((word >> sh) & 15u) - z) *
-                                __half2float(__ushort_as_half(a.p.vs[at[k] * a.p.G + g]));
-                acc[e] = fmaf(w[k], v, acc[e]);
+        float ref[NT][2], sum[NT][2], o[NT][G][2][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            ref[nt][0] = ref[nt][1] = -INFINITY;
+            sum[nt][0] = sum[nt][1] = 0.f;
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[nt][gr][i >> 2][i & 3] = 0.f;
+        }
+
+        // this warp's units: tiles first + ta .. first + tb - 1 that any column sees
+        const int32_t *pages = a.pages + (int64_t)b * a.max_pages;
+        const int u_end = min((tiles.first + tb) * kTile, min(s.n, pos_hi + 1));
+        int t0 = (tiles.first + ta) * kTile + warp * kUnit;
+        while (t0 + kUnit <= vis_lo) t0 += kTile;
+        auto page_at = [&](int t) { return t < u_end ? pages[t >> p.lp] : 0; };
+        KUnit<G> ku;
+        VUnit<G> vu;
+        int64_t base = -1;
+        int32_t next_page = page_at(t0 + kTile);
+        if (t0 < u_end) {
+            base = unit_base(p, pages[t0 >> p.lp], t0, h);
+            if (base >= 0) {
+                ku.load(p, base, lane);
+                vu.load(p, base, lane, s.n - t0);
             }
         }
+        for (; t0 < u_end; t0 += kTile) {
+            const int t1 = t0 + kTile;
+            const bool live = base >= 0;
+            int64_t next = -1;
+            if (t1 < u_end) next = unit_base(p, next_page, t1, h);
+            next_page = page_at(t1 + kTile);
+            float x[NT][4];
+            if (live) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[nt][i] = 0.f;
+#pragma unroll
+                for (int gr = 0; gr < G; ++gr) {
+                    uint32_t a0[4], a1[4];
+                    ku.operands(gr, a0, a1);
+                    const float s0 = half_of(ku.s[0][gr / 2], gr & 1), s1 = half_of(ku.s[1][gr / 2], gr & 1);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        uint4 q4;
+                        if constexpr (NT == 1) q4 = qf[gr];
+                        else q4 = qs[(nt * G + gr) * 32 + lane];
+                        float d[4] = {0.f, 0.f, 0.f, 0.f};
+                        mma_bf16(d, a0, q4.x, q4.y);
+                        mma_bf16(d, a1, q4.z, q4.w);
+                        x[nt][0] = fmaf(d[0], s0, x[nt][0]);
+                        x[nt][1] = fmaf(d[1], s0, x[nt][1]);
+                        x[nt][2] = fmaf(d[2], s1, x[nt][2]);
+                        x[nt][3] = fmaf(d[3], s1, x[nt][3]);
+                    }
+                }
+            }
+            if (next >= 0) ku.load(p, next, lane);
+            if (live) {
+                const int tr[2] = {t0 + unit_position(g), t0 + unit_position(g + 8)};
+                const bool edge = t0 + kUnit - 1 > pos_lo || (a.window > 0 && t0 <= pos_hi - a.window);
+                bool up = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int gap = pos[nt][i & 1] - tr[i >> 1];
+                        float v = score(x[nt][i]);
+                        if (a.slopes) v = fmaf(-slope[nt][i & 1], (float)gap, v);
+                        if (edge && (gap < 0 || (a.window > 0 && gap >= a.window))) v = -INFINITY;
+                        x[nt][i] = v;
+                        up |= v > ref[nt][i & 1] + kSlack;
+                    }
+                if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float m = fmaxf(x[nt][e], x[nt][2 + e]);
+#pragma unroll
+                            for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+                            m = fmaxf(m, ref[nt][e]);
+                            const float f = ref[nt][e] == -INFINITY ? 0.f : ex2(ref[nt][e] - m);
+                            ref[nt][e] = m;
+                            sum[nt][e] *= f;
+#pragma unroll
+                            for (int gr = 0; gr < G; ++gr) {
+                                o[nt][gr][0][e] *= f;
+                                o[nt][gr][0][2 + e] *= f;
+                                o[nt][gr][1][e] *= f;
+                                o[nt][gr][1][2 + e] *= f;
+                            }
+                        }
+                }
+                // weights, transposed: f[nt][i] is column 8 nt + g at position t4 + 4 i
+                float f[NT][4];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float r = ref[nt][i & 1];
+                        x[nt][i] = ex2(x[nt][i] - (r == -INFINITY ? 0.f : r));
+                        sum[nt][i & 1] += x[nt][i];
+                    }
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const uint32_t u0 = __float_as_uint(x[nt][2 * r]), u1 = __float_as_uint(x[nt][2 * r + 1]);
+                        const uint32_t hi = transpose8x8(__byte_perm(u0, u1, 0x7632));
+                        const uint32_t lo = transpose8x8(__byte_perm(u0, u1, 0x5410));
+                        f[nt][2 * r] = __uint_as_float(__byte_perm(lo, hi, 0x5410));
+                        f[nt][2 * r + 1] = __uint_as_float(__byte_perm(lo, hi, 0x7632));
+                    }
+                }
+#pragma unroll
+                for (int gr = 0; gr < G; ++gr) {
+                    uint32_t a0[4], a1[4];
+                    vu.operands(gr, a0, a1);
+                    float s4[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) s4[i] = half_of(vu.s[i][gr / 2], gr & 1);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        uint32_t hi[2], lo[2];
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const float f0 = f[nt][2 * r] * s4[2 * r], f1 = f[nt][2 * r + 1] * s4[2 * r + 1];
+                            hi[r] = bf16_pair(f0, f1);
+                            lo[r] = bf16_pair(f0 - __uint_as_float(hi[r] << 16),
+                                              f1 - __uint_as_float(hi[r] & 0xFFFF0000u));
+                        }
+                        mma_bf16(o[nt][gr][0], a0, hi[0], hi[1]);
+                        mma_bf16(o[nt][gr][1], a1, hi[0], hi[1]);
+                        mma_bf16(o[nt][gr][0], a0, lo[0], lo[1]);
+                        mma_bf16(o[nt][gr][1], a1, lo[0], lo[1]);
+                    }
+                }
+            }
+            if (next >= 0) vu.load(p, next, lane, s.n - t1);
+            base = next;
+        }
+
+        // join the four warps; a whole item is written out, a piece of one kept
+        const bool whole = ta == 0 && tb == tiles.count;
+        const int64_t slot = 2 * (int64_t)blockIdx.x + (ta > 0 ? 0 : 1);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) sum[nt][e] += __shfl_xor_sync(0xffffffffu, sum[nt][e], d);
+                if (g == 0) s_ml[warp][8 * nt + 2 * t4 + e] = make_float2(ref[nt][e], sum[nt][e]);
+            }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            if (8 * nt >= cols) break;
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    *reinterpret_cast<float4 *>(xch + (warp * 8 + 2 * t4 + e) * kRow + 32 * gr + 4 * g) =
+                        make_float4(o[nt][gr][0][e], o[nt][gr][0][2 + e], o[nt][gr][1][e], o[nt][gr][1][2 + e]);
+            __syncthreads();
+            for (int i = tid; i < min(8, cols - 8 * nt) * (D / 4); i += kThreads) {
+                const int cl = i / (D / 4), d = 4 * (i - cl * (D / 4)), c = 8 * nt + cl;
+                float m = -INFINITY, l = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_ml[w][c].x);
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float f = s_ml[w][c].x == -INFINITY ? 0.f : ex2(s_ml[w][c].x - m);
+                    const float4 u = *reinterpret_cast<const float4 *>(xch + (w * 8 + cl) * kRow + d);
+                    l = fmaf(f, s_ml[w][c].y, l);
+                    v.x = fmaf(f, u.x, v.x);
+                    v.y = fmaf(f, u.y, v.y);
+                    v.z = fmaf(f, u.z, v.z);
+                    v.w = fmaf(f, u.w, v.w);
+                }
+                if (whole) {
+                    const int64_t row = (int64_t)(s.row0 + (c0 + c) / a.grp) * a.Hq + h * a.grp + (c0 + c) % a.grp;
+                    const float r = l > 0.f ? 1.f / l : 0.f;
+                    if (a.bf16)
+                        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + row * D + d) =
+                            make_uint2(bf16_pair(v.x * r, v.y * r), bf16_pair(v.z * r, v.w * r));
+                    else
+                        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row * D + d) =
+                            make_float4(v.x * r, v.y * r, v.z * r, v.w * r);
+                    if (d == 0 && a.lse) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+                } else {
+                    *reinterpret_cast<float4 *>(a.ws_acc + (slot * C + c) * D + d) = v;
+                    if (d == 0) a.ws_ml[slot * C + c] = make_float2(m, l);
+                }
+            }
+            __syncthreads();
+        }
+        if (ta == 0 && !whole) {
+            cut.x = run_of(run.cur + tiles.count - 1, run);
+            cut.y = s.row0;
+            cut.z = c0 | (cols << 24);
+            cut.w = h;
+        }
+        run.cur += tb - ta;
+        run.off += tb - ta;
     }
-    for (int e = 0; e < 2; ++e) {
-        const int d = tid + e * kThreads;
-        if (d >= D) continue;
-        const float v = l > 0.f ? acc[e] / l : 0.f;
-        if (a.bf16) reinterpret_cast<__nv_bfloat16 *>(a.out)[row * D + d] = __float2bfloat16_rn(v);
-        else reinterpret_cast<float *>(a.out)[row * D + d] = v;
-    }
-    if (tid == 0 && a.lse) a.lse[row] = l > 0.f ? m + logf(l) : -INFINITY;
+    if (tid == 0) a.ws_item[blockIdx.x] = cut;
 }
 
-// The accumulated weights: a thread per position of one head.
-__global__ void __launch_bounds__(kThreads) paged_mass_kernel(PagedArgs a) {
-    const int h = blockIdx.y, b = blockIdx.z;
-    const Sequence s = sequence_of(a, b);
-    const int t = blockIdx.x * kThreads + threadIdx.x;
-    if (t >= s.n || s.m == 0) return;
-    const int D = 32 * a.p.G;
-    const int32_t ts = a.p.token_slot(a.pages + (int64_t)b * a.max_pages, t);
-    if (ts < 0) return;
-    const int64_t slot = a.p.slot(ts, h);
-    float sum = 0.f;
-    for (int j = 0; j < s.m; ++j) {
-        const int gap = s.n - s.m + j - t;
-        if (gap < 0 || (a.window > 0 && gap >= a.window)) continue;
-        for (int i = h * a.grp; i < (h + 1) * a.grp; ++i) {
-            const int64_t row = (int64_t)(s.row0 + j) * a.Hq + i;
-            const float x = score(a, k_dot(a, slot, a.q + row * D), a.slopes ? a.slopes[i] : 0.f, gap);
-            sum += expf(x - a.lse[row]);
+// Joins the pieces of the item that was cut at the end of run blockIdx.x, for
+// column blockIdx.y: piece 0 in that run's second place, the others in the
+// first place of the following runs.
+template <int G, int NT>
+__global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedArgs a) {
+    constexpr int D = 32 * G, C = 8 * NT, Q = D / 4, kSplit = kThreads / Q;  // Q threads per piece, kSplit pieces at once
+    __shared__ float4 s_v[kThreads];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 cut = a.ws_item[blockIdx.x];
+    const int c0 = cut.z & 0xFFFFFF, cols = cut.z >> 24, c = blockIdx.y;
+    if (cut.x < 0 || c >= cols) return;
+    const int np = cut.x - (int)blockIdx.x + 1;
+    auto at = [&](int i) -> int64_t { return (2 * ((int64_t)blockIdx.x + i) + (i == 0)) * C + c; };
+    const int tid = threadIdx.x, lane = tid & 31;
+    float m = -INFINITY;
+    for (int i = lane; i < np; i += 32) m = fmaxf(m, a.ws_ml[at(i)].x);
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float mm = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    for (int i = lane; i < np; i += 32) {
+        const float2 x = a.ws_ml[at(i)];
+        l = fmaf(ex2(x.x - mm), x.y, l);
+    }
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const int part = tid / Q, d = 4 * (tid - part * Q);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (part < kSplit) {
+#pragma unroll 8
+        for (int i = part; i < np; i += kSplit) {
+            const float f = ex2(a.ws_ml[at(i)].x - mm);
+            const float4 u = *reinterpret_cast<const float4 *>(a.ws_acc + at(i) * D + d);
+            v.x = fmaf(f, u.x, v.x);
+            v.y = fmaf(f, u.y, v.y);
+            v.z = fmaf(f, u.z, v.z);
+            v.w = fmaf(f, u.w, v.w);
         }
     }
-    a.p.mass[slot] += sum;
+    s_v[tid] = v;
+    __syncthreads();
+    if (tid < Q) {
+#pragma unroll
+        for (int k = 1; k < kSplit; ++k) {
+            const float4 u = s_v[k * Q + tid];
+            v.x += u.x;
+            v.y += u.y;
+            v.z += u.z;
+            v.w += u.w;
+        }
+        const int h = cut.w;
+        const int64_t row = (int64_t)(cut.y + (c0 + c) / a.grp) * a.Hq + h * a.grp + (c0 + c) % a.grp;
+        const float r = l > 0.f ? 1.f / l : 0.f;
+        if (a.bf16)
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + row * D + d) =
+                make_uint2(bf16_pair(v.x * r, v.y * r), bf16_pair(v.z * r, v.w * r));
+        else
+            *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row * D + d) =
+                make_float4(v.x * r, v.y * r, v.z * r, v.w * r);
+        if (d == 0 && a.lse) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    }
+}
+
+// The accumulated weights, a second pass over K alone with the rows' lse: a
+// warp per unit, 8 columns at a time; a position belongs to one warp, so its
+// sum has one order and needs no atomics.
+template <int G>
+__global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 2) paged_mass_kernel(const PagedArgs a) {
+    constexpr int D = 32 * G;
+    __shared__ int64_t s_part[33], s_found[2];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+    const PoolView &p = a.p;
+    const Score score(a);
+    auto per_seq = [&](int b) -> int64_t {
+        const Sequence s = sequence_of(a, b);
+        return s.m == 0 || s.n == 0 ? 0 : (int64_t)p.H * tiles_of(a, s).count;
+    };
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    Run run = find_run(per_seq, a.n_seq, blockIdx.x, gridDim.x, s_part, s_found);
+    int b = run.b;
+    while (run.cur < run.end) {
+        const Sequence s = sequence_of(a, b);
+        const Tiles tiles = tiles_of(a, s);
+        if (s.m == 0 || s.n == 0 || run.off >= (int64_t)p.H * tiles.count) {
+            ++b;
+            run.off = 0;
+            continue;
+        }
+        const int h = (int)(run.off / tiles.count);
+        const int ta = (int)(run.off - (int64_t)h * tiles.count);
+        const int tb = (int)min((int64_t)tiles.count, ta + (run.end - run.cur));
+        const int32_t *pages = a.pages + (int64_t)b * a.max_pages;
+        const int ncols = s.m * a.grp;
+        for (int c0 = 0; c0 < ncols; c0 += 8) {
+            const int cols = min(8, ncols - c0);
+            int pos[2];
+            float slope[2], lse2[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int c = c0 + min(2 * t4 + e, cols - 1);
+                const int i = h * a.grp + c % a.grp;
+                pos[e] = s.n - s.m + c / a.grp;
+                slope[e] = a.slopes ? a.slopes[i] * kLog2e : 0.f;
+                // a column past the last, or one that saw nothing: weight 0
+                const float v = a.lse[(int64_t)(s.row0 + c / a.grp) * a.Hq + i] * kLog2e;
+                lse2[e] = 2 * t4 + e < cols && v > -INFINITY ? v : INFINITY;
+            }
+            const int pos_lo = s.n - s.m + c0 / a.grp, pos_hi = s.n - s.m + (c0 + cols - 1) / a.grp;
+            const int vis_lo = a.window > 0 ? max(0, pos_lo - a.window + 1) : 0;
+            uint4 qf[G];
+            const uint16_t *qrow = nullptr;
+            if (g < cols) {
+                const int c = c0 + g;
+                qrow = a.q + ((int64_t)(s.row0 + c / a.grp) * a.Hq + h * a.grp + c % a.grp) * D;
+            }
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr)
+                qf[gr] = qrow ? query_operands(qrow, gr, t4) : make_uint4(0u, 0u, 0u, 0u);
+            const int u_end = min((tiles.first + tb) * kTile, min(s.n, pos_hi + 1));
+            for (int t0 = (tiles.first + ta) * kTile + warp * kUnit; t0 < u_end; t0 += kTile) {
+                if (t0 + kUnit <= vis_lo) continue;
+                const int64_t base = unit_base(p, pages[t0 >> p.lp], t0, h);
+                if (base < 0) continue;
+                KUnit<G> ku;
+                ku.load(p, base, lane);
+                float *mass = p.mass + base;
+                float old[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) old[r] = mass[unit_position(g + 8 * r)];
+                float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int gr = 0; gr < G; ++gr) {
+                    uint32_t a0[4], a1[4];
+                    ku.operands(gr, a0, a1);
+                    const float s0 = half_of(ku.s[0][gr / 2], gr & 1), s1 = half_of(ku.s[1][gr / 2], gr & 1);
+                    float d[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma_bf16(d, a0, qf[gr].x, qf[gr].y);
+                    mma_bf16(d, a1, qf[gr].z, qf[gr].w);
+                    x[0] = fmaf(d[0], s0, x[0]);
+                    x[1] = fmaf(d[1], s0, x[1]);
+                    x[2] = fmaf(d[2], s1, x[2]);
+                    x[3] = fmaf(d[3], s1, x[3]);
+                }
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int u = unit_position(g + 8 * r), t = t0 + u;
+                    float w = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int gap = pos[e] - t;
+                        float v = score(x[2 * r + e]);
+                        if (a.slopes) v = fmaf(-slope[e], (float)gap, v);
+                        if (gap >= 0 && (a.window <= 0 || gap < a.window)) w += ex2(v - lse2[e]);
+                    }
+                    w += __shfl_xor_sync(0xffffffffu, w, 1);
+                    w += __shfl_xor_sync(0xffffffffu, w, 2);
+                    if (t4 == 0 && t < s.n) mass[u] = old[r] + w;
+                }
+            }
+        }
+        run.cur += tb - ta;
+        run.off += tb - ta;
+    }
+}
+
+// ---- host ----
+
+// n-tiles of 8 columns: as few as hold a KV head's queries, up to 4, and up to
+// 128 accumulator registers a thread.
+int n_tiles(int G, int64_t cols) {
+    const int most = G <= 4 ? 4 : 2;
+    return cols <= 8 ? 1 : (cols <= 16 || most == 2 ? 2 : 4);
+}
+
+size_t ceil16(size_t n) { return (n + 15) / 16 * 16; }
+
+struct Workspace {
+    size_t acc, ml, item, lse, total;
+    Workspace(int G, int C, int64_t n_rows, int Hq) {
+        acc = 0;
+        ml = acc + (size_t)2 * kMaxCtas * C * 32 * G * sizeof(float);
+        item = ml + (size_t)2 * kMaxCtas * C * sizeof(float2);
+        lse = item + kMaxCtas * sizeof(int4);
+        total = lse + ceil16((size_t)n_rows * Hq * sizeof(float));
+    }
+};
+
+template <class... A>
+cudaError_t launch(void (*kernel)(A...), dim3 grid, size_t smem, bool dependent, cudaStream_t s, const PagedArgs &a) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = dependent ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+template <int G, int NT>
+cudaError_t run_attention(const PagedArgs &a, const DeviceInfo &dev, bool mass, cudaStream_t s) {
+    constexpr int C = 8 * NT;
+    const size_t smem = kWarps * 8 * (32 * G + 4) * 4 + (NT > 1 ? NT * G * 512 : 0);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel<G, NT>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    // runs: one wave, and no more than the tables' width allows tiles for
+    const int64_t cols = (int64_t)a.max_q * a.grp, n_ct = (cols + C - 1) / C;
+    const int64_t tiles = (((int64_t)a.max_pages << a.p.lp) + kTile - 1) / kTile;
+    const int64_t heads = (int64_t)a.n_seq * a.p.H;
+    auto runs = [&](int64_t items, int per_sm) {
+        const int64_t most = (int64_t)dev.sm_count * per_sm < kMaxCtas ? (int64_t)dev.sm_count * per_sm : kMaxCtas;
+        if (items >= most * kMinTiles || tiles >= most * kMinTiles) return (unsigned)most;
+        const int64_t want = (items * tiles + kMinTiles - 1) / kMinTiles;
+        return (unsigned)(want < most ? want : most);
+    };
+    const unsigned grid = runs(heads * n_ct, min_ctas<G, NT>());
+    cudaError_t e = launch(paged_attention_kernel<G, NT>, dim3(grid), smem, false, s, a);
+    if (e != cudaSuccess) return e;
+    e = launch(paged_join_kernel<G, NT>, dim3(grid, (unsigned)(cols < C ? cols : C)), 0, true, s, a);
+    if (e != cudaSuccess || !mass) return e;
+    return launch(paged_mass_kernel<G>, dim3(runs(heads, G <= 4 ? 4 : 2)), 0, true, s, a);
+}
+
+template <int G>
+cudaError_t run_attention_g(const PagedArgs &a, const DeviceInfo &dev, bool mass, cudaStream_t s) {
+    switch (n_tiles(G, (int64_t)a.max_q * a.grp)) {
+        case 1: return run_attention<G, 1>(a, dev, mass, s);
+        case 2: return run_attention<G, 2>(a, dev, mass, s);
+        default:
+            if constexpr (G <= 4) return run_attention<G, 4>(a, dev, mass, s);
+            return cudaErrorInvalidValue;
+    }
 }
 
 }  // namespace
 
-size_t paged_workspace_bytes(int n_rows, int n_q_heads, int head_dim) {
-    (void)head_dim;
-    return ((size_t)n_rows * n_q_heads * 4 + 15) / 16 * 16;
+size_t paged_workspace_bytes(int n_rows, int n_q_heads, int n_kv_heads, int head_dim) {
+    const int G = head_dim / 32;
+    return Workspace(G, 8 * n_tiles(G, (int64_t)n_rows * (n_q_heads / n_kv_heads)), n_rows, n_q_heads).total;
 }
 
 spectra_status launch_paged_attention(const spectra_kv_pool &pool, const spectra_paged_query &x, void *ws,
-                                      cudaStream_t s, const DeviceInfo &) {
+                                      cudaStream_t s, const DeviceInfo &dev) {
     PagedArgs a;
     a.p = PoolView::of(pool);
     a.pages = x.pages;
@@ -191,26 +882,35 @@ spectra_status launch_paged_attention(const spectra_kv_pool &pool, const spectra
     a.q = x.q;
     a.slopes = x.slopes;
     a.out = x.out;
-    a.lse = x.lse ? x.lse : (x.update_mass ? static_cast<float *>(ws) : nullptr);
     a.max_pages = x.max_pages;
     a.n_seq = x.n_seq;
     a.n_rows = x.n_rows;
-    a.max_q = x.max_q;
+    a.max_q = x.max_q < x.n_rows ? x.max_q : x.n_rows;
     a.Hq = x.n_q_heads;
     a.grp = x.n_q_heads / pool.n_heads;
     a.window = x.window;
     a.scale = x.scale;
     a.cap = x.softcap;
     a.bf16 = x.out_dtype == SPECTRA_BF16;
-    paged_attention_kernel<<<dim3((unsigned)a.Hq, (unsigned)a.max_q, (unsigned)a.n_seq), kThreads, 0, s>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return SPECTRA_ERR_CUDA;
-    if (x.update_mass) {
-        const int64_t positions = (int64_t)x.max_pages << a.p.lp;
-        paged_mass_kernel<<<dim3((unsigned)cdiv(positions, kThreads), (unsigned)a.p.H, (unsigned)a.n_seq), kThreads,
-                            0, s>>>(a);
-        if (cudaGetLastError() != cudaSuccess) return SPECTRA_ERR_CUDA;
+    const Workspace w(a.p.G, 8 * n_tiles(a.p.G, (int64_t)a.max_q * a.grp), x.n_rows, x.n_q_heads);
+    char *base = static_cast<char *>(ws);
+    a.ws_acc = reinterpret_cast<float *>(base + w.acc);
+    a.ws_ml = reinterpret_cast<float2 *>(base + w.ml);
+    a.ws_item = reinterpret_cast<int4 *>(base + w.item);
+    a.lse = x.lse ? x.lse : (x.update_mass ? reinterpret_cast<float *>(base + w.lse) : nullptr);
+    cudaError_t e = cudaErrorInvalidValue;
+    const bool mass = x.update_mass != 0;
+    switch (a.p.G) {
+        case 1: e = run_attention_g<1>(a, dev, mass, s); break;
+        case 2: e = run_attention_g<2>(a, dev, mass, s); break;
+        case 3: e = run_attention_g<3>(a, dev, mass, s); break;
+        case 4: e = run_attention_g<4>(a, dev, mass, s); break;
+        case 5: e = run_attention_g<5>(a, dev, mass, s); break;
+        case 6: e = run_attention_g<6>(a, dev, mass, s); break;
+        case 7: e = run_attention_g<7>(a, dev, mass, s); break;
+        case 8: e = run_attention_g<8>(a, dev, mass, s); break;
     }
-    return SPECTRA_OK;
+    return e == cudaSuccess ? SPECTRA_OK : SPECTRA_ERR_CUDA;
 }
 
 spectra_status paged_device_error(unsigned int *bits, cudaStream_t s) {
