@@ -739,7 +739,7 @@ spectra_status spectra_device_status(void *stream) {
     if (mv_bits & 1u) return SPECTRA_ERR_INTERNAL;
     if (embed_bits || ((pool_bits | paged_bits) & 4u) || (sample_bits & 2u)) return SPECTRA_ERR_INVALID_ARG;
     if ((kv_bits & 1u) || (sample_bits & 1u)) return SPECTRA_ERR_NONFINITE;
-    if ((kv_bits & 2u) || (mv_bits & 2u)) return SPECTRA_ERR_RANGE;
+    if (((kv_bits | paged_bits | mv_bits) & 2u) != 0) return SPECTRA_ERR_RANGE;
     return SPECTRA_OK;
 }
 

@@ -16,12 +16,21 @@
 // columns of a tile of 8 * NT; a warp takes 16 positions (a unit) at a time
 // and multiplies them on the tensor cores, m16n8k16 with FP32 accumulation:
 //   scores: A = 16 positions x 16 channels of K, B = q.  A code enters as the
-//     exact BF16 integer c - z (128 + c by or-ing the nibble under 0x4300,
-//     minus 128 + z), so the product sums are exact up to FP32 accumulation,
-//     and each group's sum is multiplied by its scale in FP32;
-//   weighted sum: A = 16 channels x 16 positions of V (the same integers), B =
-//     weight times V's scale, one per position and group, split into two BF16
-//     pieces (2^-16 of a weight is lost), each a product of its own.
+//     exact FP16 integer c - z (a nibble or-ed under 0x6400 is 1024 + c, or
+//     1024 + 16c where it stands, which saves the shift; one half-precision add
+//     or multiply-add takes it to c - z), a query as FP16 after a power of two
+//     that brings its row's largest value to 2^14 (BF16 has fewer bits, so only
+//     values under 2^-28 of the largest lose any).  The product sums are exact
+//     up to FP32 accumulation, and each group's is multiplied by its scale in
+//     FP32;
+//   weighted sum, BF16 output: A = 16 channels x 16 positions of V, dequantised
+//     to FP16 (c - z) * s with one rounding, B = the weights in FP16, scaled so
+//     that they lie under 2^15: both roundings are 2^-12 at most, a sixteenth
+//     of the output's own.  A V beyond FP16's range turns the output
+//     non-finite, which is reported;
+//   weighted sum, FP32 output: A = the exact BF16 integers c - z, B = weight
+//     times V's scale, one per position and group, in three BF16 pieces (24
+//     bits), each a product of its own.
 // The scores' accumulator layout (positions in rows) is transposed into the
 // weights' operand layout inside the warp (movmatrix on the two halves of the
 // FP32 bits).  Which lane holds which channel or position is free as long as
@@ -30,9 +39,9 @@
 // every group of positions g', g' + 8 and V's halfword g of every group of
 // positions t, t + 4, t + 8, t + 12.
 //
-// The running maximum is only a reference: it moves when a score passes it by
-// 8 or more (in base 2), so most units need no reduction over the lanes and no
-// rescaling; weights up to 2^8 are as good as weights up to 1 in FP32.
+// The running maximum is only a reference: it moves when a weight would pass
+// 2^15, and then to 2^7 for the largest, so most units need no reduction over
+// the lanes and no rescaling.
 //
 // Work split: the tiles (64 positions, one unit per warp) of every (sequence,
 // head, column tile) make one list, cut into equal runs, one per CTA, from
@@ -48,7 +57,7 @@
 namespace spectra {
 namespace {
 
-// bit 2: a page outside the pool, a length or a row range out of bounds.
+// bit 1: a non-finite output; bit 2: a page outside the pool, a length or a row range out of bounds.
 __device__ unsigned int g_paged_error;
 
 constexpr int kWarps = 4;
@@ -57,7 +66,8 @@ constexpr int kUnit = 16;                // positions of a warp's step
 constexpr int kTile = kUnit * kWarps;    // positions of a CTA's step
 constexpr int kMaxCtas = 148 * 4;        // runs: one wave of the smallest variant's CTAs
 constexpr int kMinTiles = 2;             // tiles of a run, at least (fewer pieces to join)
-constexpr float kSlack = 8.f;
+constexpr float kRefBelow = 7.f;         // the reference lies 7 under the maximum (base 2) when it is set
+constexpr float kRefRoom = 15.f;         // and moves when a score is 15 over it
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -75,7 +85,6 @@ struct PagedArgs {
     int4 *ws_item;   // [runs]: an item cut at the run's end: (last run, first row, columns, head); last run -1: none
     int max_pages, n_seq, n_rows, max_q, Hq, grp, window;
     float scale, cap;
-    bool bf16;
 };
 
 // A sequence's length and rows; nothing for values out of bounds.
@@ -114,11 +123,18 @@ __device__ __forceinline__ Tiles tiles_of(const PagedArgs &a, const Sequence &s)
     return t;
 }
 
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                 "{%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+template <bool BF16>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (BF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
@@ -136,13 +152,49 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
     return y;
 }
+__device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
+    uint32_t y;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+    return y;
+}
+__device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
+__device__ __forceinline__ uint32_t as_bits(__half2 x) { return *reinterpret_cast<const uint32_t *>(&x); }
+
+// A group's zero points of two rows (or one, twice), as the FP16 pairs that
+// take 1024 + c and (1024 + 16c) / 16 to c - z.  zp: the rows' zero halfwords
+// side by side, four groups each, shifted down by 8 for groups 2 and 3; odd:
+// the group's lowest bit.
+struct ZeroPair {
+    __half2 a, b;  // -(1024 + z), -(64 + z)
+    __device__ __forceinline__ ZeroPair(uint32_t zp, bool odd) {
+        if (!odd) {
+            a = as_half2((zp & 0x000F000Fu) | 0xE400E400u);
+            b = __hadd2(a, __float2half2_rn(960.f));
+        } else {
+            const __half2 y = as_half2((zp & 0x00F000F0u) | 0xE400E400u);  // -(1024 + 16z)
+            b = __hmul2(y, __float2half2_rn(0.0625f));
+            a = __hfma2(y, __float2half2_rn(0.0625f), __float2half2_rn(-960.f));
+        }
+    }
+    // Nibble j of both halfwords of w, less the zero points, j = 0 .. 3.
+    __device__ __forceinline__ void codes(uint32_t w, __half2 (&x)[4]) const {
+        const uint32_t w8 = w >> 8;
+        const __half2 sixteenth = __float2half2_rn(0.0625f);
+        x[0] = __hadd2(as_half2((w & 0x000F000Fu) | 0x64006400u), a);
+        x[1] = __hfma2(as_half2((w & 0x00F000F0u) | 0x64006400u), sixteenth, b);
+        x[2] = __hadd2(as_half2((w8 & 0x000F000Fu) | 0x64006400u), a);
+        x[3] = __hfma2(as_half2((w8 & 0x00F000F0u) | 0x64006400u), sixteenth, b);
+    }
+};
+
+// Nibble j of both halfwords as the BF16 pair 128 + c, 128 + c'; and the
+// difference of two such pairs.
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, int j) { return ((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u; }
 __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
     const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&a),
                                      *reinterpret_cast<const __nv_bfloat162 *>(&b));
     return *reinterpret_cast<const uint32_t *>(&r);
 }
-// Nibble j of both halfwords as the BF16 pair 128 + c, 128 + c'.
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, int j) { return ((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u; }
 
 // Row r of a unit's 16 (as the tensor core counts them) is its position
 // unit_position(r): rows 2t, 2t+1, 2t+8, 2t+9 are t, t+4, t+8, t+12.
@@ -179,8 +231,26 @@ __device__ __forceinline__ void load_halfwords(uint32_t (&r)[(N + 1) / 2], const
     }
 }
 __device__ __forceinline__ float half_of(uint32_t w, int which) {
-    return __half2float(__ushort_as_half((unsigned short)(which ? w >> 16 : w & 0xFFFFu)));
+    return which ? __high2float(as_half2(w)) : __low2float(as_half2(w));
 }
+
+// A lane's own pointers into the pool; unit u (16 slots) is u strides further.
+struct LanePointers {
+    const uint32_t *kc, *kz, *vz;
+    const uint16_t *ks, *vc, *vs;
+    template <int G>
+    static __device__ __forceinline__ LanePointers of(const PoolView &p, int lane) {
+        const int g = lane >> 2, t = lane & 3, up = unit_position(g);
+        LanePointers l;
+        l.kc = p.kc + up * 4 * G + t * G;
+        l.ks = p.ks + up * G;
+        l.kz = p.kz + up;
+        l.vc = p.vc + t * 8 * G + g * G;
+        l.vs = p.vs + t * G;
+        l.vz = p.vz + t;
+        return l;
+    }
+};
 
 // One unit's K for this lane: rows lane/4 and lane/4 + 8.
 template <int G>
@@ -188,27 +258,26 @@ struct KUnit {
     uint32_t w[2][G];
     uint32_t s[2][(G + 1) / 2];
     uint32_t z[2];
-    __device__ __forceinline__ void load(const PoolView &p, int64_t base, int lane) {
-        const int g = lane >> 2, t = lane & 3;
+    __device__ __forceinline__ void load(const LanePointers &l, uint32_t u) {
+        const uint32_t *kc = l.kc + (uint64_t)u * (kUnit * 4 * G), *kz = l.kz + (uint64_t)u * kUnit;
+        const uint16_t *ks = l.ks + (uint64_t)u * (kUnit * G);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int64_t slot = base + unit_position(g + 8 * r);
-            load_words<G>(w[r], p.kc + slot * (4 * G) + t * G);
-            load_halfwords<G>(s[r], p.ks + slot * G);
-            z[r] = p.kz[slot];
+        for (int r = 0; r < 2; ++r) {  // unit_position(g + 8) = unit_position(g) + 8
+            load_words<G>(w[r], kc + r * 8 * 4 * G);
+            load_halfwords<G>(s[r], ks + r * 8 * G);
+            z[r] = kz[r * 8];
         }
     }
     // The A operands of group gr, k-steps 0 and 1.
     __device__ __forceinline__ void operands(int gr, uint32_t (&a0)[4], uint32_t (&a1)[4]) const {
-        uint32_t x[2][4];
+        __half2 x[2][4];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-            const uint32_t zz = (((z[r] >> (4 * gr)) & 0xFu) | 0x4300u) * 0x10001u;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[r][j] = sub_bf16x2(code_pair(w[r][gr], j), zz);
+            const uint32_t zp = __byte_perm(z[r], 0, gr < 4 ? 0x1010 : 0x3232) >> (gr & 2 ? 8 : 0);
+            ZeroPair(zp, gr & 1).codes(w[r][gr], x[r]);
         }
-        a0[0] = x[0][0]; a0[1] = x[1][0]; a0[2] = x[0][1]; a0[3] = x[1][1];
-        a1[0] = x[0][2]; a1[1] = x[1][2]; a1[2] = x[0][3]; a1[3] = x[1][3];
+        a0[0] = as_bits(x[0][0]); a0[1] = as_bits(x[1][0]); a0[2] = as_bits(x[0][1]); a0[3] = as_bits(x[1][1]);
+        a1[0] = as_bits(x[0][2]); a1[1] = as_bits(x[1][2]); a1[2] = as_bits(x[0][3]); a1[3] = as_bits(x[1][3]);
     }
 };
 
@@ -220,15 +289,16 @@ struct VUnit {
     uint32_t w[4][W];
     uint32_t s[4][W];
     uint32_t z[4];
-    // Entries past the sequence may hold anything: their scales become 0.
-    __device__ __forceinline__ void load(const PoolView &p, int64_t base, int lane, int left) {
-        const int g = lane >> 2, t = lane & 3;
+    // `left` positions belong to the sequence; entries past them may hold
+    // anything, and their scales become 0.
+    __device__ __forceinline__ void load(const LanePointers &l, uint32_t u, int t, int left) {
+        const uint16_t *vc = l.vc + (uint64_t)u * (kUnit * 8 * G), *vs = l.vs + (uint64_t)u * (kUnit * G);
+        const uint32_t *vz = l.vz + (uint64_t)u * kUnit;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t slot = base + t + 4 * i;
-            load_halfwords<G>(w[i], p.vc + slot * (8 * G) + g * G);
-            load_halfwords<G>(s[i], p.vs + slot * G);
-            z[i] = p.vz[slot];
+            load_halfwords<G>(w[i], vc + i * 4 * 8 * G);
+            load_halfwords<G>(s[i], vs + i * 4 * G);
+            z[i] = vz[i * 4];
         }
         if (left < kUnit) {
 #pragma unroll
@@ -238,36 +308,70 @@ struct VUnit {
                     for (int k = 0; k < W; ++k) s[i][k] = 0u;
         }
     }
-    // The A operands of group gr: channels (4g, 4g + 1) and (4g + 2, 4g + 3).
+    // The A operands of group gr, channels (4g, 4g + 1) and (4g + 2, 4g + 3):
+    // EXACT the BF16 integers c - z, otherwise the FP16 values (c - z) * s.
+    template <bool EXACT>
     __device__ __forceinline__ void operands(int gr, uint32_t (&a0)[4], uint32_t (&a1)[4]) const {
         const uint32_t pick = gr & 1 ? 0x7632u : 0x5410u;
         uint32_t x[2][4];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const uint32_t c = __byte_perm(w[2 * r][gr / 2], w[2 * r + 1][gr / 2], pick);
-            // the two positions' zero points, each in its half
-            const uint32_t zz = code_pair(__byte_perm(z[2 * r], z[2 * r + 1], gr < 4 ? 0x5410u : 0x7632u), gr & 3);
+            const uint32_t zp = __byte_perm(z[2 * r], z[2 * r + 1], gr < 4 ? 0x5410u : 0x7632u);
+            if constexpr (EXACT) {
+                const uint32_t zz = code_pair(zp, gr & 3);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[r][j] = sub_bf16x2(code_pair(c, j), zz);
+                for (int j = 0; j < 4; ++j) x[r][j] = sub_bf16x2(code_pair(c, j), zz);
+            } else {
+                __half2 v[4];
+                ZeroPair(zp >> (gr & 2 ? 8 : 0), gr & 1).codes(c, v);
+                const __half2 sc = as_half2(__byte_perm(s[2 * r][gr / 2], s[2 * r + 1][gr / 2], pick));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[r][j] = as_bits(__hmul2(v[j], sc));
+            }
         }
         a0[0] = x[0][0]; a0[1] = x[0][1]; a0[2] = x[1][0]; a0[3] = x[1][1];
         a1[0] = x[0][2]; a1[1] = x[0][3]; a1[2] = x[1][2]; a1[3] = x[1][3];
     }
 };
 
-// The B operands of one query vector's group gr (8 channels of the lane's t):
-// pairs (q0, q4), (q1, q5) of k-step 0 and (q2, q6), (q3, q7) of k-step 1, the
-// order in which code_pair takes a word's nibbles.
-__device__ __forceinline__ uint4 query_operands(const uint16_t *q, int gr, int t) {
-    const uint4 v = *reinterpret_cast<const uint4 *>(q + 32 * gr + 8 * t);
-    return make_uint4(__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632), __byte_perm(v.y, v.w, 0x5410),
-                      __byte_perm(v.y, v.w, 0x7632));
+// One query vector's operands: group gr of the lane's 8 channels (t = lane %
+// 4), pairs (q0, q4), (q1, q5) of k-step 0 and (q2, q6), (q3, q7) of k-step 1,
+// the order in which ZeroPair::codes takes a word's nibbles.  `back` undoes the
+// row's power of two.  Rows lie on groups of 4 lanes; all lanes of the warp call
+// it (q is null for a column without a query).
+template <int G>
+__device__ __forceinline__ void query_operands(const uint16_t *q, int t, uint4 (&f)[G], float &back) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int gr = 0; gr < G; ++gr) {
+        f[gr] = q ? *reinterpret_cast<const uint4 *>(q + 32 * gr + 8 * t) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t w[4] = {f[gr].x, f[gr].y, f[gr].z, f[gr].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+    }
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const uint32_t e = max(top >> 7, 16u);  // the largest value's exponent field (2^-111 or less: as 2^-111)
+    const float up = __uint_as_float((268u - e) << 23);
+    back = __uint_as_float((e - 14u) << 23);
+#pragma unroll
+    for (int gr = 0; gr < G; ++gr) {
+        const uint32_t w[4] = {f[gr].x, f[gr].y, f[gr].z, f[gr].w};
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16) * up;
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u) * up;
+        }
+        f[gr] = make_uint4(f16_pair(v[0], v[4]), f16_pair(v[1], v[5]), f16_pair(v[2], v[6]), f16_pair(v[3], v[7]));
+    }
 }
 
 // tanh to an absolute 2^-21 or so.
 __device__ __forceinline__ float tanh_abs(float y) { return 1.f - __fdividef(2.f, ex2(2.f * kLog2e * y) + 1.f); }
 
-// What turns a product sum into a score in base 2.
+// What turns a product sum (its factor taken in) into a score in base 2.
 struct Score {
     float mul, cap;  // without a cap: s = mul * dot; with: cap * tanh(mul * dot)
     bool capped;
@@ -276,19 +380,18 @@ struct Score {
         mul = capped ? a.scale / a.cap : a.scale * kLog2e;
         cap = a.cap * kLog2e;
     }
-    __device__ __forceinline__ float operator()(float dot) const {
-        const float y = mul * dot;
-        return capped ? cap * tanh_abs(y) : y;
-    }
+    __device__ __forceinline__ float cap_of(float y) const { return cap * tanh_abs(y); }
 };
 
-// The first position of the unit's page slots for head h, -1 without a page.
-__device__ __forceinline__ int64_t unit_base(const PoolView &p, int32_t page, int t0, int h) {
+constexpr uint32_t kNoUnit = 0xFFFFFFFFu;
+// The unit of the pool that holds positions t0 .. t0 + 15 of head h; kNoUnit
+// for a page outside the pool.  (Units number under 2^31.)
+__device__ __forceinline__ uint32_t unit_of(const PoolView &p, int32_t page, int t0, int h) {
     if ((uint32_t)page >= (uint32_t)p.n_pages) {
         atomicOr(&g_paged_error, 4u);
-        return -1;
+        return kNoUnit;
     }
-    return (((int64_t)page * p.H + h) << p.lp) + (t0 & ((1 << p.lp) - 1));
+    return (((uint32_t)page * (uint32_t)p.H + (uint32_t)h) << (p.lp - 4)) + ((uint32_t)(t0 & ((1 << p.lp) - 1)) >> 4);
 }
 
 // This CTA's run of the tile list and where it starts: sequence b, `off` tiles
@@ -338,22 +441,39 @@ __device__ __forceinline__ Run find_run(const F &per_seq, int n_seq, int run, in
 // The run that holds tile t of the list.
 __device__ __forceinline__ int run_of(int64_t t, const Run &r) { return (int)(((t + 1) * r.runs - 1) / r.total); }
 
+// Four channels of an output row: the weighted sum over the sum of weights.
+template <bool EXACT>
+__device__ __forceinline__ void store_out(const PagedArgs &a, int64_t at, float4 v, float l) {
+    const float r = l > 0.f ? 1.f / l : 0.f;
+    v = make_float4(v.x * r, v.y * r, v.z * r, v.w * r);
+    if (EXACT) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = v;
+    } else {
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) =
+            make_uint2(bf16_pair(v.x, v.y), bf16_pair(v.z, v.w));
+        if (!(isfinite(v.x) && isfinite(v.y) && isfinite(v.z) && isfinite(v.w))) atomicOr(&g_paged_error, 2u);
+    }
+}
+
 template <int G, int NT>
 constexpr int min_ctas() {
     return G * NT <= 4 ? 4 : (G * NT <= 8 ? 2 : 1);
 }
 
-template <int G, int NT>
+template <int G, int NT, bool EXACT>
 __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_kernel(const PagedArgs a) {
     constexpr int D = 32 * G, C = 8 * NT, kRow = D + 4;  // kRow: a padded column of the exchange buffer
     extern __shared__ __align__(16) unsigned char smem[];
     float *xch = reinterpret_cast<float *>(smem);                      // [kWarps][8][kRow]
     uint4 *qs = reinterpret_cast<uint4 *>(smem + kWarps * 8 * kRow * 4);  // NT > 1: [NT][G][32]
     __shared__ float2 s_ml[kWarps][C];
+    __shared__ float s_back[C];
     __shared__ int64_t s_part[33], s_found[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const PoolView &p = a.p;
+    const LanePointers lp = LanePointers::of<G>(p, lane);
     const Score score(a);
+    const bool shaped = score.capped || a.slopes;  // scores are more than a multiple of the products
 
     // the join may be launched: it waits for this grid's end before it reads
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -379,48 +499,43 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
         const int h = item / n_ct, c0 = (item - h * n_ct) * C;
         const int cols = min(C, ncols - c0);
         // the columns of this lane: 2 per n-tile, their positions and slopes
-        int pos[NT][2];
-        float slope[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int c = c0 + min(8 * nt + 2 * t4 + e, cols - 1);
-                pos[nt][e] = s.n - s.m + c / a.grp;
-                slope[nt][e] = a.slopes ? a.slopes[h * a.grp + c % a.grp] * kLog2e : 0.f;
-            }
+        auto col_pos = [&](int nt, int e) { return s.n - s.m + (c0 + min(8 * nt + 2 * t4 + e, cols - 1)) / a.grp; };
         const int pos_lo = s.n - s.m + c0 / a.grp, pos_hi = s.n - s.m + (c0 + cols - 1) / a.grp;
         const int vis_lo = a.window > 0 ? max(0, pos_lo - a.window + 1) : 0;  // the first position any column sees
-        // queries: column g of every n-tile (zeros past the last column)
+        // queries: column g of every n-tile (zeros past the last column); mul
+        // is what this lane's columns' products are multiplied with
         uint4 qf[G];
-        const uint16_t *qrow = nullptr;
-        {
-            if constexpr (NT == 1) {
-                if (g < cols) {
-                    const int c = c0 + g;
-                    qrow = a.q + ((int64_t)(s.row0 + c / a.grp) * a.Hq + h * a.grp + c % a.grp) * D;
-                }
+        float mul[NT][2];
+        auto query_row = [&](int nt) -> const uint16_t * {
+            const int c = c0 + 8 * nt + g;
+            return 8 * nt + g < cols
+                       ? a.q + ((int64_t)(s.row0 + c / a.grp) * a.Hq + h * a.grp + c % a.grp) * D : nullptr;
+        };
+        if constexpr (NT == 1) {
+            float back;
+            query_operands<G>(query_row(0), t4, qf, back);
 #pragma unroll
-                for (int gr = 0; gr < G; ++gr)
-                    qf[gr] = qrow ? query_operands(qrow, gr, t4) : make_uint4(0u, 0u, 0u, 0u);
-            } else {
-                for (int nt = warp; nt < NT; nt += kWarps) {
-                    qrow = nullptr;
-                    if (8 * nt + g < cols) {
-                        const int c = c0 + 8 * nt + g;
-                        qrow = a.q + ((int64_t)(s.row0 + c / a.grp) * a.Hq + h * a.grp + c % a.grp) * D;
-                    }
+            for (int e = 0; e < 2; ++e) mul[0][e] = score.mul * __shfl_sync(0xffffffffu, back, 4 * (2 * t4 + e));
+        } else {
+            for (int nt = warp; nt < NT; nt += kWarps) {
+                float back;
+                query_operands<G>(query_row(nt), t4, qf, back);
 #pragma unroll
-                    for (int gr = 0; gr < G; ++gr)
-                        qs[(nt * G + gr) * 32 + lane] = qrow ? query_operands(qrow, gr, t4) : make_uint4(0u, 0u, 0u, 0u);
-                }
-                __syncthreads();
+                for (int gr = 0; gr < G; ++gr) qs[(nt * G + gr) * 32 + lane] = qf[gr];
+                if (t4 == 0) s_back[8 * nt + g] = back;
             }
+            __syncthreads();
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) mul[nt][e] = score.mul * s_back[8 * nt + 2 * t4 + e];
         }
-        float ref[NT][2], sum[NT][2], o[NT][G][2][4];
+        // ref: what weights are relative to; limit: the score that moves it
+        float ref[NT][2], limit[NT][2], sum[NT][2], o[NT][G][2][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            ref[nt][0] = ref[nt][1] = -INFINITY;
+            ref[nt][0] = ref[nt][1] = 0.f;
+            limit[nt][0] = limit[nt][1] = -INFINITY;
             sum[nt][0] = sum[nt][1] = 0.f;
 #pragma unroll
             for (int gr = 0; gr < G; ++gr)
@@ -436,20 +551,20 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
         auto page_at = [&](int t) { return t < u_end ? pages[t >> p.lp] : 0; };
         KUnit<G> ku;
         VUnit<G> vu;
-        int64_t base = -1;
+        uint32_t unit = kNoUnit;
         int32_t next_page = page_at(t0 + kTile);
         if (t0 < u_end) {
-            base = unit_base(p, pages[t0 >> p.lp], t0, h);
-            if (base >= 0) {
-                ku.load(p, base, lane);
-                vu.load(p, base, lane, s.n - t0);
+            unit = unit_of(p, pages[t0 >> p.lp], t0, h);
+            if (unit != kNoUnit) {
+                ku.load(lp, unit);
+                vu.load(lp, unit, t4, s.n - t0);
             }
         }
         for (; t0 < u_end; t0 += kTile) {
             const int t1 = t0 + kTile;
-            const bool live = base >= 0;
-            int64_t next = -1;
-            if (t1 < u_end) next = unit_base(p, next_page, t1, h);
+            const bool live = unit != kNoUnit;
+            uint32_t next = kNoUnit;
+            if (t1 < u_end) next = unit_of(p, next_page, t1, h);
             next_page = page_at(t1 + kTile);
             float x[NT][4];
             if (live) {
@@ -468,8 +583,8 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
                         if constexpr (NT == 1) q4 = qf[gr];
                         else q4 = qs[(nt * G + gr) * 32 + lane];
                         float d[4] = {0.f, 0.f, 0.f, 0.f};
-                        mma_bf16(d, a0, q4.x, q4.y);
-                        mma_bf16(d, a1, q4.z, q4.w);
+                        mma<false>(d, a0, q4.x, q4.y);
+                        mma<false>(d, a1, q4.z, q4.w);
                         x[nt][0] = fmaf(d[0], s0, x[nt][0]);
                         x[nt][1] = fmaf(d[1], s0, x[nt][1]);
                         x[nt][2] = fmaf(d[2], s1, x[nt][2]);
@@ -477,22 +592,45 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
                     }
                 }
             }
-            if (next >= 0) ku.load(p, next, lane);
+            if (next != kNoUnit) ku.load(lp, next);
             if (live) {
-                const int tr[2] = {t0 + unit_position(g), t0 + unit_position(g + 8)};
-                const bool edge = t0 + kUnit - 1 > pos_lo || (a.window > 0 && t0 <= pos_hi - a.window);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[nt][i] *= mul[nt][i & 1];
+                if (shaped) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int c = c0 + min(8 * nt + 2 * t4 + e, cols - 1);
+                            const float slope = a.slopes ? a.slopes[h * a.grp + c % a.grp] * kLog2e : 0.f;
+                            const int gap = s.n - s.m + c / a.grp - t0 - unit_position(g);
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                float v = x[nt][2 * r + e];
+                                if (score.capped) v = score.cap_of(v);
+                                x[nt][2 * r + e] = fmaf(-slope, (float)(gap - 8 * r), v);
+                            }
+                        }
+                }
+                if (t0 + kUnit - 1 > pos_lo || (a.window > 0 && t0 <= pos_hi - a.window)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int gap = col_pos(nt, e) - t0 - unit_position(g);
+#pragma unroll
+                            for (int r = 0; r < 2; ++r)
+                                if (gap - 8 * r < 0 || (a.window > 0 && gap - 8 * r >= a.window))
+                                    x[nt][2 * r + e] = -INFINITY;
+                        }
+                }
                 bool up = false;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int gap = pos[nt][i & 1] - tr[i >> 1];
-                        float v = score(x[nt][i]);
-                        if (a.slopes) v = fmaf(-slope[nt][i & 1], (float)gap, v);
-                        if (edge && (gap < 0 || (a.window > 0 && gap >= a.window))) v = -INFINITY;
-                        x[nt][i] = v;
-                        up |= v > ref[nt][i & 1] + kSlack;
-                    }
+                    for (int e = 0; e < 2; ++e) up |= fmaxf(x[nt][e], x[nt][2 + e]) > limit[nt][e];
                 if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
@@ -501,9 +639,13 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
                             float m = fmaxf(x[nt][e], x[nt][2 + e]);
 #pragma unroll
                             for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-                            m = fmaxf(m, ref[nt][e]);
-                            const float f = ref[nt][e] == -INFINITY ? 0.f : ex2(ref[nt][e] - m);
-                            ref[nt][e] = m;
+                            // a column that saw nothing yet keeps its zeros
+                            const bool first = limit[nt][e] == -INFINITY;
+                            const float to = m == -INFINITY ? ref[nt][e]
+                                                            : (first ? m - kRefBelow : fmaxf(m - kRefBelow, ref[nt][e]));
+                            const float f = first ? 1.f : ex2(ref[nt][e] - to);
+                            if (m > -INFINITY) limit[nt][e] = to + kRefRoom;
+                            ref[nt][e] = to;
                             sum[nt][e] *= f;
 #pragma unroll
                             for (int gr = 0; gr < G; ++gr) {
@@ -514,51 +656,72 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
                             }
                         }
                 }
-                // weights, transposed: f[nt][i] is column 8 nt + g at position t4 + 4 i
-                float f[NT][4];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float r = ref[nt][i & 1];
-                        x[nt][i] = ex2(x[nt][i] - (r == -INFINITY ? 0.f : r));
+                        x[nt][i] = ex2(x[nt][i] - ref[nt][i & 1]);
                         sum[nt][i & 1] += x[nt][i];
                     }
+                if constexpr (EXACT) {
+                    // weights, transposed: f[nt][i] is column 8 nt + g at position t4 + 4 i
+                    float f[NT][4];
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const uint32_t u0 = __float_as_uint(x[nt][2 * r]), u1 = __float_as_uint(x[nt][2 * r + 1]);
-                        const uint32_t hi = transpose8x8(__byte_perm(u0, u1, 0x7632));
-                        const uint32_t lo = transpose8x8(__byte_perm(u0, u1, 0x5410));
-                        f[nt][2 * r] = __uint_as_float(__byte_perm(lo, hi, 0x5410));
-                        f[nt][2 * r + 1] = __uint_as_float(__byte_perm(lo, hi, 0x7632));
-                    }
-                }
-#pragma unroll
-                for (int gr = 0; gr < G; ++gr) {
-                    uint32_t a0[4], a1[4];
-                    vu.operands(gr, a0, a1);
-                    float s4[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) s4[i] = half_of(vu.s[i][gr / 2], gr & 1);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        uint32_t hi[2], lo[2];
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
-                            const float f0 = f[nt][2 * r] * s4[2 * r], f1 = f[nt][2 * r + 1] * s4[2 * r + 1];
-                            hi[r] = bf16_pair(f0, f1);
-                            lo[r] = bf16_pair(f0 - __uint_as_float(hi[r] << 16),
-                                              f1 - __uint_as_float(hi[r] & 0xFFFF0000u));
+                            const uint32_t u0 = __float_as_uint(x[nt][2 * r]), u1 = __float_as_uint(x[nt][2 * r + 1]);
+                            const uint32_t hi = transpose8x8(__byte_perm(u0, u1, 0x7632));
+                            const uint32_t lo = transpose8x8(__byte_perm(u0, u1, 0x5410));
+                            f[nt][2 * r] = __uint_as_float(__byte_perm(lo, hi, 0x5410));
+                            f[nt][2 * r + 1] = __uint_as_float(__byte_perm(lo, hi, 0x7632));
                         }
-                        mma_bf16(o[nt][gr][0], a0, hi[0], hi[1]);
-                        mma_bf16(o[nt][gr][1], a1, hi[0], hi[1]);
-                        mma_bf16(o[nt][gr][0], a0, lo[0], lo[1]);
-                        mma_bf16(o[nt][gr][1], a1, lo[0], lo[1]);
+#pragma unroll
+                    for (int gr = 0; gr < G; ++gr) {
+                        uint32_t a0[4], a1[4];
+                        vu.template operands<true>(gr, a0, a1);
+                        float s4[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) s4[i] = half_of(vu.s[i][gr / 2], gr & 1);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float rest[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) rest[i] = f[nt][i] * s4[i];
+#pragma unroll
+                            for (int piece = 0; piece < 3; ++piece) {
+                                uint32_t b[2];
+#pragma unroll
+                                for (int r = 0; r < 2; ++r) {
+                                    b[r] = bf16_pair(rest[2 * r], rest[2 * r + 1]);
+                                    rest[2 * r] -= __uint_as_float(b[r] << 16);
+                                    rest[2 * r + 1] -= __uint_as_float(b[r] & 0xFFFF0000u);
+                                }
+                                mma<true>(o[nt][gr][0], a0, b[0], b[1]);
+                                mma<true>(o[nt][gr][1], a1, b[0], b[1]);
+                            }
+                        }
+                    }
+                } else {
+                    uint32_t b[NT][2];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) b[nt][r] = transpose8x8(f16_pair(x[nt][2 * r], x[nt][2 * r + 1]));
+#pragma unroll
+                    for (int gr = 0; gr < G; ++gr) {
+                        uint32_t a0[4], a1[4];
+                        vu.template operands<false>(gr, a0, a1);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma<false>(o[nt][gr][0], a0, b[nt][0], b[nt][1]);
+                            mma<false>(o[nt][gr][1], a1, b[nt][0], b[nt][1]);
+                        }
                     }
                 }
             }
-            if (next >= 0) vu.load(p, next, lane, s.n - t1);
-            base = next;
+            if (next != kNoUnit) vu.load(lp, next, t4, s.n - t1);
+            unit = next;
         }
 
         // join the four warps; a whole item is written out, a piece of one kept
@@ -570,7 +733,9 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
             for (int e = 0; e < 2; ++e) {
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) sum[nt][e] += __shfl_xor_sync(0xffffffffu, sum[nt][e], d);
-                if (g == 0) s_ml[warp][8 * nt + 2 * t4 + e] = make_float2(ref[nt][e], sum[nt][e]);
+                if (g == 0)
+                    s_ml[warp][8 * nt + 2 * t4 + e] =
+                        make_float2(limit[nt][e] == -INFINITY ? -INFINITY : ref[nt][e], sum[nt][e]);
             }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -600,13 +765,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
                 }
                 if (whole) {
                     const int64_t row = (int64_t)(s.row0 + (c0 + c) / a.grp) * a.Hq + h * a.grp + (c0 + c) % a.grp;
-                    const float r = l > 0.f ? 1.f / l : 0.f;
-                    if (a.bf16)
-                        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + row * D + d) =
-                            make_uint2(bf16_pair(v.x * r, v.y * r), bf16_pair(v.z * r, v.w * r));
-                    else
-                        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row * D + d) =
-                            make_float4(v.x * r, v.y * r, v.z * r, v.w * r);
+                    store_out<EXACT>(a, row * D + d, v, l);
                     if (d == 0 && a.lse) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
                 } else {
                     *reinterpret_cast<float4 *>(a.ws_acc + (slot * C + c) * D + d) = v;
@@ -630,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
 // Joins the pieces of the item that was cut at the end of run blockIdx.x, for
 // column blockIdx.y: piece 0 in that run's second place, the others in the
 // first place of the following runs.
-template <int G, int NT>
+template <int G, int NT, bool EXACT>
 __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedArgs a) {
     constexpr int D = 32 * G, C = 8 * NT, Q = D / 4, kSplit = kThreads / Q;  // Q threads per piece, kSplit pieces at once
     __shared__ float4 s_v[kThreads];
@@ -677,13 +836,7 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedArgs a)
         }
         const int h = cut.w;
         const int64_t row = (int64_t)(cut.y + (c0 + c) / a.grp) * a.Hq + h * a.grp + (c0 + c) % a.grp;
-        const float r = l > 0.f ? 1.f / l : 0.f;
-        if (a.bf16)
-            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + row * D + d) =
-                make_uint2(bf16_pair(v.x * r, v.y * r), bf16_pair(v.z * r, v.w * r));
-        else
-            *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row * D + d) =
-                make_float4(v.x * r, v.y * r, v.z * r, v.w * r);
+        store_out<EXACT>(a, row * D + d, v, l);
         if (d == 0 && a.lse) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
     }
 }
@@ -697,6 +850,7 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 2) paged_mass_kernel(co
     __shared__ int64_t s_part[33], s_found[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const PoolView &p = a.p;
+    const LanePointers lp = LanePointers::of<G>(p, lane);
     const Score score(a);
     auto per_seq = [&](int b) -> int64_t {
         const Sequence s = sequence_of(a, b);
@@ -735,22 +889,20 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 2) paged_mass_kernel(co
             const int pos_lo = s.n - s.m + c0 / a.grp, pos_hi = s.n - s.m + (c0 + cols - 1) / a.grp;
             const int vis_lo = a.window > 0 ? max(0, pos_lo - a.window + 1) : 0;
             uint4 qf[G];
-            const uint16_t *qrow = nullptr;
-            if (g < cols) {
-                const int c = c0 + g;
-                qrow = a.q + ((int64_t)(s.row0 + c / a.grp) * a.Hq + h * a.grp + c % a.grp) * D;
-            }
+            const int cg = c0 + g;
+            float back, mul[2];
+            query_operands<G>(g < cols ? a.q + ((int64_t)(s.row0 + cg / a.grp) * a.Hq + h * a.grp + cg % a.grp) * D
+                                       : nullptr, t4, qf, back);
 #pragma unroll
-            for (int gr = 0; gr < G; ++gr)
-                qf[gr] = qrow ? query_operands(qrow, gr, t4) : make_uint4(0u, 0u, 0u, 0u);
+            for (int e = 0; e < 2; ++e) mul[e] = score.mul * __shfl_sync(0xffffffffu, back, 4 * (2 * t4 + e));
             const int u_end = min((tiles.first + tb) * kTile, min(s.n, pos_hi + 1));
             for (int t0 = (tiles.first + ta) * kTile + warp * kUnit; t0 < u_end; t0 += kTile) {
                 if (t0 + kUnit <= vis_lo) continue;
-                const int64_t base = unit_base(p, pages[t0 >> p.lp], t0, h);
-                if (base < 0) continue;
+                const uint32_t unit = unit_of(p, pages[t0 >> p.lp], t0, h);
+                if (unit == kNoUnit) continue;
                 KUnit<G> ku;
-                ku.load(p, base, lane);
-                float *mass = p.mass + base;
+                ku.load(lp, unit);
+                float *mass = p.mass + (uint64_t)unit * kUnit;
                 float old[2];
 #pragma unroll
                 for (int r = 0; r < 2; ++r) old[r] = mass[unit_position(g + 8 * r)];
@@ -761,8 +913,8 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 2) paged_mass_kernel(co
                     ku.operands(gr, a0, a1);
                     const float s0 = half_of(ku.s[0][gr / 2], gr & 1), s1 = half_of(ku.s[1][gr / 2], gr & 1);
                     float d[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma_bf16(d, a0, qf[gr].x, qf[gr].y);
-                    mma_bf16(d, a1, qf[gr].z, qf[gr].w);
+                    mma<false>(d, a0, qf[gr].x, qf[gr].y);
+                    mma<false>(d, a1, qf[gr].z, qf[gr].w);
                     x[0] = fmaf(d[0], s0, x[0]);
                     x[1] = fmaf(d[1], s0, x[1]);
                     x[2] = fmaf(d[2], s1, x[2]);
@@ -775,7 +927,8 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 2) paged_mass_kernel(co
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int gap = pos[e] - t;
-                        float v = score(x[2 * r + e]);
+                        float v = x[2 * r + e] * mul[e];
+                        if (score.capped) v = score.cap_of(v);
                         if (a.slopes) v = fmaf(-slope[e], (float)gap, v);
                         if (gap >= 0 && (a.window <= 0 || gap < a.window)) w += ex2(v - lse2[e]);
                     }
@@ -827,12 +980,12 @@ cudaError_t launch(void (*kernel)(A...), dim3 grid, size_t smem, bool dependent,
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-template <int G, int NT>
+template <int G, int NT, bool EXACT>
 cudaError_t run_attention(const PagedArgs &a, const DeviceInfo &dev, bool mass, cudaStream_t s) {
     constexpr int C = 8 * NT;
     const size_t smem = kWarps * 8 * (32 * G + 4) * 4 + (NT > 1 ? NT * G * 512 : 0);
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel<G, NT>,
+        const cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel<G, NT, EXACT>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
@@ -847,22 +1000,27 @@ cudaError_t run_attention(const PagedArgs &a, const DeviceInfo &dev, bool mass, 
         return (unsigned)(want < most ? want : most);
     };
     const unsigned grid = runs(heads * n_ct, min_ctas<G, NT>());
-    cudaError_t e = launch(paged_attention_kernel<G, NT>, dim3(grid), smem, false, s, a);
+    cudaError_t e = launch(paged_attention_kernel<G, NT, EXACT>, dim3(grid), smem, false, s, a);
     if (e != cudaSuccess) return e;
-    e = launch(paged_join_kernel<G, NT>, dim3(grid, (unsigned)(cols < C ? cols : C)), 0, true, s, a);
+    e = launch(paged_join_kernel<G, NT, EXACT>, dim3(grid, (unsigned)(cols < C ? cols : C)), 0, true, s, a);
     if (e != cudaSuccess || !mass) return e;
     return launch(paged_mass_kernel<G>, dim3(runs(heads, G <= 4 ? 4 : 2)), 0, true, s, a);
 }
 
-template <int G>
+template <int G, bool EXACT>
 cudaError_t run_attention_g(const PagedArgs &a, const DeviceInfo &dev, bool mass, cudaStream_t s) {
     switch (n_tiles(G, (int64_t)a.max_q * a.grp)) {
-        case 1: return run_attention<G, 1>(a, dev, mass, s);
-        case 2: return run_attention<G, 2>(a, dev, mass, s);
+        case 1: return run_attention<G, 1, EXACT>(a, dev, mass, s);
+        case 2: return run_attention<G, 2, EXACT>(a, dev, mass, s);
         default:
-            if constexpr (G <= 4) return run_attention<G, 4>(a, dev, mass, s);
+            if constexpr (G <= 4) return run_attention<G, 4, EXACT>(a, dev, mass, s);
             return cudaErrorInvalidValue;
     }
+}
+
+template <int G>
+cudaError_t run_attention_g(const PagedArgs &a, const DeviceInfo &dev, bool exact, bool mass, cudaStream_t s) {
+    return exact ? run_attention_g<G, true>(a, dev, mass, s) : run_attention_g<G, false>(a, dev, mass, s);
 }
 
 }  // namespace
@@ -891,7 +1049,6 @@ spectra_status launch_paged_attention(const spectra_kv_pool &pool, const spectra
     a.window = x.window;
     a.scale = x.scale;
     a.cap = x.softcap;
-    a.bf16 = x.out_dtype == SPECTRA_BF16;
     const Workspace w(a.p.G, 8 * n_tiles(a.p.G, (int64_t)a.max_q * a.grp), x.n_rows, x.n_q_heads);
     char *base = static_cast<char *>(ws);
     a.ws_acc = reinterpret_cast<float *>(base + w.acc);
@@ -899,16 +1056,16 @@ spectra_status launch_paged_attention(const spectra_kv_pool &pool, const spectra
     a.ws_item = reinterpret_cast<int4 *>(base + w.item);
     a.lse = x.lse ? x.lse : (x.update_mass ? reinterpret_cast<float *>(base + w.lse) : nullptr);
     cudaError_t e = cudaErrorInvalidValue;
-    const bool mass = x.update_mass != 0;
+    const bool mass = x.update_mass != 0, exact = x.out_dtype == SPECTRA_F32;
     switch (a.p.G) {
-        case 1: e = run_attention_g<1>(a, dev, mass, s); break;
-        case 2: e = run_attention_g<2>(a, dev, mass, s); break;
-        case 3: e = run_attention_g<3>(a, dev, mass, s); break;
-        case 4: e = run_attention_g<4>(a, dev, mass, s); break;
-        case 5: e = run_attention_g<5>(a, dev, mass, s); break;
-        case 6: e = run_attention_g<6>(a, dev, mass, s); break;
-        case 7: e = run_attention_g<7>(a, dev, mass, s); break;
-        case 8: e = run_attention_g<8>(a, dev, mass, s); break;
+        case 1: e = run_attention_g<1>(a, dev, exact, mass, s); break;
+        case 2: e = run_attention_g<2>(a, dev, exact, mass, s); break;
+        case 3: e = run_attention_g<3>(a, dev, exact, mass, s); break;
+        case 4: e = run_attention_g<4>(a, dev, exact, mass, s); break;
+        case 5: e = run_attention_g<5>(a, dev, exact, mass, s); break;
+        case 6: e = run_attention_g<6>(a, dev, exact, mass, s); break;
+        case 7: e = run_attention_g<7>(a, dev, exact, mass, s); break;
+        case 8: e = run_attention_g<8>(a, dev, exact, mass, s); break;
     }
     return e == cudaSuccess ? SPECTRA_OK : SPECTRA_ERR_CUDA;
 }
