@@ -64,7 +64,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kUnit = 16;                // positions of a warp's step
 constexpr int kTile = kUnit * kWarps;    // positions of a CTA's step
-constexpr int kMaxCtas = 148 * 4;        // runs: one wave of the smallest variant's CTAs
+constexpr int kMaxCtas = 148 * 5;        // runs: one wave of the smallest variant's CTAs
 constexpr int kMinTiles = 2;             // tiles of a run, at least (fewer pieces to join)
 constexpr float kRefBelow = 7.f;         // the reference lies 7 under the maximum (base 2) when it is set
 constexpr float kRefRoom = 15.f;         // and moves when a score is 15 over it
@@ -126,19 +126,26 @@ __device__ __forceinline__ Tiles tiles_of(const PagedArgs &a, const Sequence &s)
 template <bool BF16>
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     if constexpr (BF16)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
                      "{%0,%1,%2,%3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
                      "{%0,%1,%2,%3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// The same from zero (FP16).
+__device__ __forceinline__ void mma_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%10,%10,%10,%10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -160,6 +167,14 @@ __device__ __forceinline__ uint32_t f16_pair(float lo, float hi) {
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<const __half2 *>(&x); }
 __device__ __forceinline__ uint32_t as_bits(__half2 x) { return *reinterpret_cast<const uint32_t *>(&x); }
 
+// (w & MASK) | magic in one instruction, the magic number in a register.
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t masked_or(uint32_t w, uint32_t magic) {
+    uint32_t y;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(w), "n"(MASK), "r"(magic));
+    return y;
+}
+
 // A group's zero points of two rows (or one, twice), as the FP16 pairs that
 // take 1024 + c and (1024 + 16c) / 16 to c - z.  zp: the rows' zero halfwords
 // side by side, four groups each, shifted down by 8 for groups 2 and 3; odd:
@@ -168,10 +183,10 @@ struct ZeroPair {
     __half2 a, b;  // -(1024 + z), -(64 + z)
     __device__ __forceinline__ ZeroPair(uint32_t zp, bool odd) {
         if (!odd) {
-            a = as_half2((zp & 0x000F000Fu) | 0xE400E400u);
+            a = as_half2(masked_or<0x000F000Fu>(zp, 0xE400E400u));
             b = __hadd2(a, __float2half2_rn(960.f));
         } else {
-            const __half2 y = as_half2((zp & 0x00F000F0u) | 0xE400E400u);  // -(1024 + 16z)
+            const __half2 y = as_half2(masked_or<0x00F000F0u>(zp, 0xE400E400u));  // -(1024 + 16z)
             b = __hmul2(y, __float2half2_rn(0.0625f));
             a = __hfma2(y, __float2half2_rn(0.0625f), __float2half2_rn(-960.f));
         }
@@ -180,16 +195,18 @@ struct ZeroPair {
     __device__ __forceinline__ void codes(uint32_t w, __half2 (&x)[4]) const {
         const uint32_t w8 = w >> 8;
         const __half2 sixteenth = __float2half2_rn(0.0625f);
-        x[0] = __hadd2(as_half2((w & 0x000F000Fu) | 0x64006400u), a);
-        x[1] = __hfma2(as_half2((w & 0x00F000F0u) | 0x64006400u), sixteenth, b);
-        x[2] = __hadd2(as_half2((w8 & 0x000F000Fu) | 0x64006400u), a);
-        x[3] = __hfma2(as_half2((w8 & 0x00F000F0u) | 0x64006400u), sixteenth, b);
+        x[0] = __hadd2(as_half2(masked_or<0x000F000Fu>(w, 0x64006400u)), a);
+        x[1] = __hfma2(as_half2(masked_or<0x00F000F0u>(w, 0x64006400u)), sixteenth, b);
+        x[2] = __hadd2(as_half2(masked_or<0x000F000Fu>(w8, 0x64006400u)), a);
+        x[3] = __hfma2(as_half2(masked_or<0x00F000F0u>(w8, 0x64006400u)), sixteenth, b);
     }
 };
 
 // Nibble j of both halfwords as the BF16 pair 128 + c, 128 + c'; and the
 // difference of two such pairs.
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, int j) { return ((w >> (4 * j)) & 0x000F000Fu) | 0x43004300u; }
+__device__ __forceinline__ uint32_t code_pair(uint32_t w, int j) {
+    return masked_or<0x000F000Fu>(w >> (4 * j), 0x43004300u);
+}
 __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
     const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&a),
                                      *reinterpret_cast<const __nv_bfloat162 *>(&b));
@@ -234,21 +251,67 @@ __device__ __forceinline__ float half_of(uint32_t w, int which) {
     return which ? __high2float(as_half2(w)) : __low2float(as_half2(w));
 }
 
-// A lane's own pointers into the pool; unit u (16 slots) is u strides further.
-struct LanePointers {
-    const uint32_t *kc, *kz, *vz;
-    const uint16_t *ks, *vc, *vs;
-    template <int G>
-    static __device__ __forceinline__ LanePointers of(const PoolView &p, int lane) {
-        const int g = lane >> 2, t = lane & 3, up = unit_position(g);
-        LanePointers l;
-        l.kc = p.kc + up * 4 * G + t * G;
-        l.ks = p.ks + up * G;
-        l.kz = p.kz + up;
-        l.vc = p.vc + t * 8 * G + g * G;
-        l.vs = p.vs + t * G;
-        l.vz = p.vz + t;
-        return l;
+// A unit's 16 slots lie together in each of the pool's six arrays; a warp
+// copies them into its stage in shared memory (16 bytes a lane and copy,
+// asynchronous), at these places.
+template <int G>
+struct Stage {
+    static constexpr int kCodes = 256 * G, kScales = 32 * G, kZeros = 64;  // bytes per unit
+    static constexpr int kc = 0, vc = kc + kCodes, ks = vc + kCodes, vs = ks + kScales, kz = vs + kScales,
+                         vz = kz + kZeros, kBytes = vz + kZeros;
+    static constexpr int kSmall = 4 * G + 8;  // 16-byte pieces of the scales and zero words
+    static constexpr int kPer = (kSmall + 31) / 32;
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// What a lane copies of every unit.
+template <int G>
+struct Copier {
+    using S = Stage<G>;
+    const char *kc, *vc, *small[S::kPer];
+    uint32_t stride[S::kPer], to[S::kPer];
+    __device__ __forceinline__ Copier(const PoolView &p, int lane) {
+        kc = reinterpret_cast<const char *>(p.kc) + 16 * lane;
+        vc = reinterpret_cast<const char *>(p.vc) + 16 * lane;
+#pragma unroll
+        for (int j = 0; j < S::kPer; ++j) {
+            int m = lane + 32 * j;
+            if (m < 2 * G) {
+                small[j] = reinterpret_cast<const char *>(p.ks);
+                stride[j] = S::kScales;
+                to[j] = S::ks + 16 * m;
+            } else if ((m -= 2 * G) < 2 * G) {
+                small[j] = reinterpret_cast<const char *>(p.vs);
+                stride[j] = S::kScales;
+                to[j] = S::vs + 16 * m;
+            } else if ((m -= 2 * G) < 4) {
+                small[j] = reinterpret_cast<const char *>(p.kz);
+                stride[j] = S::kZeros;
+                to[j] = S::kz + 16 * m;
+            } else {
+                m = (m - 4) & 3;
+                small[j] = reinterpret_cast<const char *>(p.vz);
+                stride[j] = S::kZeros;
+                to[j] = S::vz + 16 * m;
+            }
+            small[j] += 16 * m;
+        }
+    }
+    __device__ __forceinline__ void copy(uint32_t dst, uint32_t unit, int lane) const {
+        const char *k = kc + (uint64_t)unit * S::kCodes, *v = vc + (uint64_t)unit * S::kCodes;
+#pragma unroll
+        for (int c = 0; c < 16 * G; c += 32)
+            if (c + 32 <= 16 * G || lane < 16 * G - c) {
+                copy16(dst + S::kc + 16 * (c + lane), k + 16 * c);
+                copy16(dst + S::vc + 16 * (c + lane), v + 16 * c);
+            }
+#pragma unroll
+        for (int j = 0; j < S::kPer; ++j)
+            if (32 * (j + 1) <= S::kSmall || lane < S::kSmall - 32 * j)
+                copy16(dst + to[j], small[j] + (uint64_t)unit * stride[j]);
     }
 };
 
@@ -258,14 +321,14 @@ struct KUnit {
     uint32_t w[2][G];
     uint32_t s[2][(G + 1) / 2];
     uint32_t z[2];
-    __device__ __forceinline__ void load(const LanePointers &l, uint32_t u) {
-        const uint32_t *kc = l.kc + (uint64_t)u * (kUnit * 4 * G), *kz = l.kz + (uint64_t)u * kUnit;
-        const uint16_t *ks = l.ks + (uint64_t)u * (kUnit * G);
+    // From a stage or from the pool (the addresses of the unit's first slot).
+    __device__ __forceinline__ void load(const void *kc, const void *ks, const void *kz, int lane) {
+        const int g = lane >> 2, t = lane & 3, up = unit_position(g);
 #pragma unroll
         for (int r = 0; r < 2; ++r) {  // unit_position(g + 8) = unit_position(g) + 8
-            load_words<G>(w[r], kc + r * 8 * 4 * G);
-            load_halfwords<G>(s[r], ks + r * 8 * G);
-            z[r] = kz[r * 8];
+            load_words<G>(w[r], static_cast<const uint32_t *>(kc) + (up + 8 * r) * 4 * G + t * G);
+            load_halfwords<G>(s[r], static_cast<const uint16_t *>(ks) + (up + 8 * r) * G);
+            z[r] = static_cast<const uint32_t *>(kz)[up + 8 * r];
         }
     }
     // The A operands of group gr, k-steps 0 and 1.
@@ -289,24 +352,23 @@ struct VUnit {
     uint32_t w[4][W];
     uint32_t s[4][W];
     uint32_t z[4];
-    // `left` positions belong to the sequence; entries past them may hold
-    // anything, and their scales become 0.
-    __device__ __forceinline__ void load(const LanePointers &l, uint32_t u, int t, int left) {
-        const uint16_t *vc = l.vc + (uint64_t)u * (kUnit * 8 * G), *vs = l.vs + (uint64_t)u * (kUnit * G);
-        const uint32_t *vz = l.vz + (uint64_t)u * kUnit;
+    __device__ __forceinline__ void load(const void *vc, const void *vs, const void *vz, int lane) {
+        const int g = lane >> 2, t = lane & 3;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            load_halfwords<G>(w[i], vc + i * 4 * 8 * G);
-            load_halfwords<G>(s[i], vs + i * 4 * G);
-            z[i] = vz[i * 4];
+            load_halfwords<G>(w[i], static_cast<const uint16_t *>(vc) + (t + 4 * i) * 8 * G + g * G);
+            load_halfwords<G>(s[i], static_cast<const uint16_t *>(vs) + (t + 4 * i) * G);
+            z[i] = static_cast<const uint32_t *>(vz)[t + 4 * i];
         }
-        if (left < kUnit) {
+    }
+    // `left` positions belong to the sequence; entries past them may hold
+    // anything, so their scales become 0.
+    __device__ __forceinline__ void cut_off(int left, int lane) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (t + 4 * i >= left)
+        for (int i = 0; i < 4; ++i)
+            if ((lane & 3) + 4 * i >= left)
 #pragma unroll
-                    for (int k = 0; k < W; ++k) s[i][k] = 0u;
-        }
+                for (int k = 0; k < W; ++k) s[i][k] = 0u;
     }
     // The A operands of group gr, channels (4g, 4g + 1) and (4g + 2, 4g + 3):
     // EXACT the BF16 integers c - z, otherwise the FP16 values (c - z) * s.
@@ -457,7 +519,16 @@ __device__ __forceinline__ void store_out(const PagedArgs &a, int64_t at, float4
 
 template <int G, int NT>
 constexpr int min_ctas() {
-    return G * NT <= 4 ? 4 : (G * NT <= 8 ? 2 : 1);
+    return G * NT <= 4 ? 5 : (G * NT <= 8 ? 3 : 2);
+}
+
+constexpr int kStages = 3;
+// Shared memory: the warps' stages, which the exchange of the warps' sums
+// takes over at an item's end; then the queries' operands of several n-tiles.
+template <int G>
+constexpr int ring_bytes() {
+    constexpr int ring = kWarps * kStages * Stage<G>::kBytes, xch = kWarps * 8 * (32 * G + 4) * 4;
+    return ring > xch ? ring : xch;
 }
 
 template <int G, int NT, bool EXACT>
@@ -465,13 +536,16 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
     constexpr int D = 32 * G, C = 8 * NT, kRow = D + 4;  // kRow: a padded column of the exchange buffer
     extern __shared__ __align__(16) unsigned char smem[];
     float *xch = reinterpret_cast<float *>(smem);                      // [kWarps][8][kRow]
-    uint4 *qs = reinterpret_cast<uint4 *>(smem + kWarps * 8 * kRow * 4);  // NT > 1: [NT][G][32]
+    uint4 *qs = reinterpret_cast<uint4 *>(smem + ring_bytes<G>());     // NT > 1: [NT][G][32]
     __shared__ float2 s_ml[kWarps][C];
     __shared__ float s_back[C];
     __shared__ int64_t s_part[33], s_found[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const PoolView &p = a.p;
-    const LanePointers lp = LanePointers::of<G>(p, lane);
+    const Copier<G> copier(p, lane);
+    using S = Stage<G>;
+    unsigned char *ring = smem + warp * kStages * S::kBytes;
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
     const Score score(a);
     const bool shaped = score.capped || a.slopes;  // scores are more than a multiple of the products
 
@@ -548,26 +622,51 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
         const int u_end = min((tiles.first + tb) * kTile, min(s.n, pos_hi + 1));
         int t0 = (tiles.first + ta) * kTile + warp * kUnit;
         while (t0 + kUnit <= vis_lo) t0 += kTile;
-        auto page_at = [&](int t) { return t < u_end ? pages[t >> p.lp] : 0; };
-        KUnit<G> ku;
-        VUnit<G> vu;
-        uint32_t unit = kNoUnit;
-        int32_t next_page = page_at(t0 + kTile);
-        if (t0 < u_end) {
-            unit = unit_of(p, pages[t0 >> p.lp], t0, h);
-            if (unit != kNoUnit) {
-                ku.load(lp, unit);
-                vu.load(lp, unit, t4, s.n - t0);
+        const int n_units = t0 < u_end ? (u_end - t0 + kTile - 1) / kTile : 0;
+        // Bookkeeping 32 units at a time: lane i finds unit f + i's place in the
+        // pool, and whether a position of it may be hidden from a column.
+        uint32_t units = kNoUnit, live_next = 0, edge_next = 0;
+        auto look_up = [&](int f) {
+            const int t = t0 + (f + lane) * kTile;
+            bool edge = false;
+            units = kNoUnit;
+            if (f + lane < n_units) {
+                units = unit_of(p, pages[t >> p.lp], t, h);
+                edge = t + kUnit - 1 > pos_lo || (a.window > 0 && t <= pos_hi - a.window);
             }
-        }
-        for (; t0 < u_end; t0 += kTile) {
-            const int t1 = t0 + kTile;
-            const bool live = unit != kNoUnit;
-            uint32_t next = kNoUnit;
-            if (t1 < u_end) next = unit_of(p, next_page, t1, h);
-            next_page = page_at(t1 + kTile);
-            float x[NT][4];
-            if (live) {
+            live_next = __ballot_sync(0xffffffffu, units != kNoUnit);
+            edge_next = __ballot_sync(0xffffffffu, edge);
+        };
+        // the ring: units kStages - 1 ahead, one group of copies each
+        auto fetch = [&](int f, int stage) {
+            if (f < n_units) {
+                if ((f & 31) == 0) look_up(f);
+                const uint32_t unit = __shfl_sync(0xffffffffu, units, f & 31);
+                if (unit != kNoUnit) copier.copy(ring_at + stage * S::kBytes, unit, lane);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) fetch(i, i);
+        uint32_t live = 0, edge = 0;
+        int stage = 0;
+        for (int i = 0; i < n_units; ++i) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+            __syncwarp();  // every lane's copies of this unit have landed, and nobody reads the last one's stage
+            if ((i & 31) == 0) {
+                live = live_next;
+                edge = edge_next;
+            }
+            fetch(i + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
+            const unsigned char *at = ring + stage * S::kBytes;
+            stage = stage == kStages - 1 ? 0 : stage + 1;
+            const bool here = live & 1u, hidden = edge & 1u;
+            live >>= 1;
+            edge >>= 1;
+            if (here) {
+                float x[NT][4];
+                KUnit<G> ku;
+                ku.load(at + S::kc, at + S::ks, at + S::kz, lane);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -582,8 +681,8 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
                         uint4 q4;
                         if constexpr (NT == 1) q4 = qf[gr];
                         else q4 = qs[(nt * G + gr) * 32 + lane];
-                        float d[4] = {0.f, 0.f, 0.f, 0.f};
-                        mma<false>(d, a0, q4.x, q4.y);
+                        float d[4];
+                        mma_first(d, a0, q4.x, q4.y);
                         mma<false>(d, a1, q4.z, q4.w);
                         x[nt][0] = fmaf(d[0], s0, x[nt][0]);
                         x[nt][1] = fmaf(d[1], s0, x[nt][1]);
@@ -591,9 +690,8 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
                         x[nt][3] = fmaf(d[3], s1, x[nt][3]);
                     }
                 }
-            }
-            if (next != kNoUnit) ku.load(lp, next);
-            if (live) {
+                VUnit<G> vu;
+                vu.load(at + S::vc, at + S::vs, at + S::vz, lane);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -605,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
                         for (int e = 0; e < 2; ++e) {
                             const int c = c0 + min(8 * nt + 2 * t4 + e, cols - 1);
                             const float slope = a.slopes ? a.slopes[h * a.grp + c % a.grp] * kLog2e : 0.f;
-                            const int gap = s.n - s.m + c / a.grp - t0 - unit_position(g);
+                            const int gap = s.n - s.m + c / a.grp - (t0 + i * kTile) - unit_position(g);
 #pragma unroll
                             for (int r = 0; r < 2; ++r) {
                                 float v = x[nt][2 * r + e];
@@ -614,12 +712,13 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
                             }
                         }
                 }
-                if (t0 + kUnit - 1 > pos_lo || (a.window > 0 && t0 <= pos_hi - a.window)) {
+                if (hidden) {
+                    vu.cut_off(s.n - (t0 + i * kTile), lane);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const int gap = col_pos(nt, e) - t0 - unit_position(g);
+                            const int gap = col_pos(nt, e) - (t0 + i * kTile) - unit_position(g);
 #pragma unroll
                             for (int r = 0; r < 2; ++r)
                                 if (gap - 8 * r < 0 || (a.window > 0 && gap - 8 * r >= a.window))
@@ -720,9 +819,10 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
                     }
                 }
             }
-            if (next != kNoUnit) vu.load(lp, next, t4, s.n - t1);
-            unit = next;
         }
+        // the exchange buffer takes the ring's place
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
 
         // join the four warps; a whole item is written out, a piece of one kept
         const bool whole = ta == 0 && tb == tiles.count;
@@ -850,7 +950,6 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 2) paged_mass_kernel(co
     __shared__ int64_t s_part[33], s_found[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const PoolView &p = a.p;
-    const LanePointers lp = LanePointers::of<G>(p, lane);
     const Score score(a);
     auto per_seq = [&](int b) -> int64_t {
         const Sequence s = sequence_of(a, b);
@@ -901,7 +1000,9 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 2) paged_mass_kernel(co
                 const uint32_t unit = unit_of(p, pages[t0 >> p.lp], t0, h);
                 if (unit == kNoUnit) continue;
                 KUnit<G> ku;
-                ku.load(lp, unit);
+                ku.load(reinterpret_cast<const char *>(p.kc) + (uint64_t)unit * Stage<G>::kCodes,
+                        reinterpret_cast<const char *>(p.ks) + (uint64_t)unit * Stage<G>::kScales,
+                        reinterpret_cast<const char *>(p.kz) + (uint64_t)unit * Stage<G>::kZeros, lane);
                 float *mass = p.mass + (uint64_t)unit * kUnit;
                 float old[2];
 #pragma unroll
@@ -912,8 +1013,8 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 2) paged_mass_kernel(co
                     uint32_t a0[4], a1[4];
                     ku.operands(gr, a0, a1);
                     const float s0 = half_of(ku.s[0][gr / 2], gr & 1), s1 = half_of(ku.s[1][gr / 2], gr & 1);
-                    float d[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma<false>(d, a0, qf[gr].x, qf[gr].y);
+                    float d[4];
+                    mma_first(d, a0, qf[gr].x, qf[gr].y);
                     mma<false>(d, a1, qf[gr].z, qf[gr].w);
                     x[0] = fmaf(d[0], s0, x[0]);
                     x[1] = fmaf(d[1], s0, x[1]);
@@ -983,7 +1084,7 @@ cudaError_t launch(void (*kernel)(A...), dim3 grid, size_t smem, bool dependent,
 template <int G, int NT, bool EXACT>
 cudaError_t run_attention(const PagedArgs &a, const DeviceInfo &dev, bool mass, cudaStream_t s) {
     constexpr int C = 8 * NT;
-    const size_t smem = kWarps * 8 * (32 * G + 4) * 4 + (NT > 1 ? NT * G * 512 : 0);
+    const size_t smem = ring_bytes<G>() + (NT > 1 ? NT * G * 512 : 0);
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel<G, NT, EXACT>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
