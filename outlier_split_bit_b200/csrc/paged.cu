@@ -138,10 +138,9 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
 }
 // The same from zero (FP16).
 __device__ __forceinline__ void mma_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                 "{%10,%10,%10,%10};"
-                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
@@ -217,34 +216,69 @@ __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
 // unit_position(r): rows 2t, 2t+1, 2t+8, 2t+9 are t, t+4, t+8, t+12.
 __device__ __forceinline__ int unit_position(int r) { return (r & 8) | ((r & 1) << 2) | ((r & 7) >> 1); }
 
-// N 32-bit words, or N halfwords in (N + 1) / 2 words, from p with the widest
-// loads that their alignment (the size's own) allows.
-template <int N>
-__device__ __forceinline__ void load_words(uint32_t (&r)[N], const uint32_t *p) {
+// Where a unit's data is read from: the pool, or a stage in shared memory (read
+// once each: left to itself the compiler reads some of it again).
+struct Global {
+    const unsigned char *at;
+    __device__ __forceinline__ Global operator+(uint32_t bytes) const { return {at + bytes}; }
+    __device__ __forceinline__ uint4 get16() const { return *reinterpret_cast<const uint4 *>(at); }
+    __device__ __forceinline__ uint2 get8() const { return *reinterpret_cast<const uint2 *>(at); }
+    __device__ __forceinline__ uint32_t get4() const { return *reinterpret_cast<const uint32_t *>(at); }
+    __device__ __forceinline__ uint32_t get2() const { return *reinterpret_cast<const uint16_t *>(at); }
+};
+struct Shared {
+    uint32_t at;
+    __device__ __forceinline__ Shared operator+(uint32_t bytes) const { return {at + bytes}; }
+    __device__ __forceinline__ uint4 get16() const {
+        uint4 v;
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+        return v;
+    }
+    __device__ __forceinline__ uint2 get8() const {
+        uint2 v;
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+        return v;
+    }
+    __device__ __forceinline__ uint32_t get4() const {
+        uint32_t v;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+        return v;
+    }
+    __device__ __forceinline__ uint32_t get2() const {
+        uint16_t v;
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+        return v;
+    }
+};
+
+// N 32-bit words, or N halfwords in (N + 1) / 2 words, with the widest loads
+// that their alignment (the size's own) allows.
+template <int N, class P>
+__device__ __forceinline__ void load_words(uint32_t (&r)[N], P p) {
     if constexpr (N % 4 == 0) {
 #pragma unroll
         for (int i = 0; i < N; i += 4) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(p + i);
+            const uint4 v = (p + 4 * i).get16();
             r[i] = v.x; r[i + 1] = v.y; r[i + 2] = v.z; r[i + 3] = v.w;
         }
     } else if constexpr (N % 2 == 0) {
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
-            const uint2 v = *reinterpret_cast<const uint2 *>(p + i);
+            const uint2 v = (p + 4 * i).get8();
             r[i] = v.x; r[i + 1] = v.y;
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) r[i] = p[i];
+        for (int i = 0; i < N; ++i) r[i] = (p + 4 * i).get4();
     }
 }
-template <int N>
-__device__ __forceinline__ void load_halfwords(uint32_t (&r)[(N + 1) / 2], const uint16_t *p) {
+template <int N, class P>
+__device__ __forceinline__ void load_halfwords(uint32_t (&r)[(N + 1) / 2], P p) {
     if constexpr (N % 2 == 0) {
-        load_words<N / 2>(r, reinterpret_cast<const uint32_t *>(p));
+        load_words<N / 2>(r, p);
     } else {
 #pragma unroll
-        for (int i = 0; i < N; i += 2) r[i / 2] = (uint32_t)p[i] | (i + 1 < N ? (uint32_t)p[i + 1] << 16 : 0u);
+        for (int i = 0; i < N; i += 2) r[i / 2] = (p + 2 * i).get2() | (i + 1 < N ? (p + 2 * i + 2).get2() << 16 : 0u);
     }
 }
 __device__ __forceinline__ float half_of(uint32_t w, int which) {
@@ -292,7 +326,7 @@ struct Copier {
                 stride[j] = S::kZeros;
                 to[j] = S::kz + 16 * m;
             } else {
-                m = (m - 4) & 3;
+                m = (m - 4) & 3;  // lanes past the last piece copy one of these again
                 small[j] = reinterpret_cast<const char *>(p.vz);
                 stride[j] = S::kZeros;
                 to[j] = S::vz + 16 * m;
@@ -309,9 +343,24 @@ struct Copier {
                 copy16(dst + S::vc + 16 * (c + lane), v + 16 * c);
             }
 #pragma unroll
-        for (int j = 0; j < S::kPer; ++j)
-            if (32 * (j + 1) <= S::kSmall || lane < S::kSmall - 32 * j)
-                copy16(dst + to[j], small[j] + (uint64_t)unit * stride[j]);
+        for (int j = 0; j < S::kPer; ++j) copy16(dst + to[j], small[j] + (uint64_t)unit * stride[j]);
+    }
+};
+
+// Byte offsets of a lane's own data within a unit's six arrays.  (Hidden from
+// the compiler's arithmetic: it would recompute them for every unit.)
+template <int G>
+struct LaneOffsets {
+    uint32_t kc, ks, kz, vc, vs, vz;
+    __device__ __forceinline__ explicit LaneOffsets(int lane) {
+        const int g = lane >> 2, t = lane & 3, up = unit_position(g);
+        kc = (up * 4 * G + t * G) * 4;
+        ks = up * G * 2;
+        kz = up * 4;
+        vc = (t * 8 * G + g * G) * 2;
+        vs = t * G * 2;
+        vz = t * 4;
+        asm volatile("" : "+r"(kc), "+r"(ks), "+r"(kz), "+r"(vc), "+r"(vs), "+r"(vz));
     }
 };
 
@@ -321,14 +370,14 @@ struct KUnit {
     uint32_t w[2][G];
     uint32_t s[2][(G + 1) / 2];
     uint32_t z[2];
-    // From a stage or from the pool (the addresses of the unit's first slot).
-    __device__ __forceinline__ void load(const void *kc, const void *ks, const void *kz, int lane) {
-        const int g = lane >> 2, t = lane & 3, up = unit_position(g);
+    // From the lane's places in a stage, or in the pool.
+    template <class P>
+    __device__ __forceinline__ void load(P kc, P ks, P kz) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {  // unit_position(g + 8) = unit_position(g) + 8
-            load_words<G>(w[r], static_cast<const uint32_t *>(kc) + (up + 8 * r) * 4 * G + t * G);
-            load_halfwords<G>(s[r], static_cast<const uint16_t *>(ks) + (up + 8 * r) * G);
-            z[r] = static_cast<const uint32_t *>(kz)[up + 8 * r];
+            load_words<G>(w[r], kc + r * 8 * 16 * G);
+            load_halfwords<G>(s[r], ks + r * 8 * 2 * G);
+            z[r] = (kz + r * 8 * 4).get4();
         }
     }
     // The A operands of group gr, k-steps 0 and 1.
@@ -352,13 +401,12 @@ struct VUnit {
     uint32_t w[4][W];
     uint32_t s[4][W];
     uint32_t z[4];
-    __device__ __forceinline__ void load(const void *vc, const void *vs, const void *vz, int lane) {
-        const int g = lane >> 2, t = lane & 3;
+    __device__ __forceinline__ void load(Shared vc, Shared vs, Shared vz) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            load_halfwords<G>(w[i], static_cast<const uint16_t *>(vc) + (t + 4 * i) * 8 * G + g * G);
-            load_halfwords<G>(s[i], static_cast<const uint16_t *>(vs) + (t + 4 * i) * G);
-            z[i] = static_cast<const uint32_t *>(vz)[t + 4 * i];
+            load_halfwords<G>(w[i], vc + i * 4 * 16 * G);
+            load_halfwords<G>(s[i], vs + i * 4 * 2 * G);
+            z[i] = (vz + i * 4 * 4).get4();
         }
     }
     // `left` positions belong to the sequence; entries past them may hold
@@ -445,7 +493,7 @@ struct Score {
     __device__ __forceinline__ float cap_of(float y) const { return cap * tanh_abs(y); }
 };
 
-constexpr uint32_t kNoUnit = 0xFFFFFFFFu;
+constexpr uint32_t kNoUnit = 0xFFFFFFFFu, kSpecial = 0x80000000u;
 // The unit of the pool that holds positions t0 .. t0 + 15 of head h; kNoUnit
 // for a page outside the pool.  (Units number under 2^31.)
 __device__ __forceinline__ uint32_t unit_of(const PoolView &p, int32_t page, int t0, int h) {
@@ -519,7 +567,7 @@ __device__ __forceinline__ void store_out(const PagedArgs &a, int64_t at, float4
 
 template <int G, int NT>
 constexpr int min_ctas() {
-    return G * NT <= 4 ? 5 : (G * NT <= 8 ? 3 : 2);
+    return G * NT <= 4 ? 4 : (G * NT <= 8 ? 3 : 2);
 }
 
 constexpr int kStages = 3;
@@ -543,9 +591,9 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const PoolView &p = a.p;
     const Copier<G> copier(p, lane);
+    const LaneOffsets<G> lo(lane);
     using S = Stage<G>;
-    unsigned char *ring = smem + warp * kStages * S::kBytes;
-    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(ring);
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(smem) + warp * kStages * S::kBytes;
     const Score score(a);
     const bool shaped = score.capped || a.slopes;  // scores are more than a multiple of the products
 
@@ -572,8 +620,6 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
         const int tb = (int)min((int64_t)tiles.count, ta + (run.end - run.cur));
         const int h = item / n_ct, c0 = (item - h * n_ct) * C;
         const int cols = min(C, ncols - c0);
-        // the columns of this lane: 2 per n-tile, their positions and slopes
-        auto col_pos = [&](int nt, int e) { return s.n - s.m + (c0 + min(8 * nt + 2 * t4 + e, cols - 1)) / a.grp; };
         const int pos_lo = s.n - s.m + c0 / a.grp, pos_hi = s.n - s.m + (c0 + cols - 1) / a.grp;
         const int vis_lo = a.window > 0 ? max(0, pos_lo - a.window + 1) : 0;  // the first position any column sees
         // queries: column g of every n-tile (zeros past the last column); mul
@@ -624,49 +670,44 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
         while (t0 + kUnit <= vis_lo) t0 += kTile;
         const int n_units = t0 < u_end ? (u_end - t0 + kTile - 1) / kTile : 0;
         // Bookkeeping 32 units at a time: lane i finds unit f + i's place in the
-        // pool, and whether a position of it may be hidden from a column.
-        uint32_t units = kNoUnit, live_next = 0, edge_next = 0;
+        // pool; the top bit marks a unit whose scores need more than their
+        // factor (hidden positions, a page outside the pool, a cap, a bias).
+        uint32_t units = 0;
         auto look_up = [&](int f) {
             const int t = t0 + (f + lane) * kTile;
-            bool edge = false;
-            units = kNoUnit;
             if (f + lane < n_units) {
                 units = unit_of(p, pages[t >> p.lp], t, h);
-                edge = t + kUnit - 1 > pos_lo || (a.window > 0 && t <= pos_hi - a.window);
+                if (units == kNoUnit) units = kSpecial;  // unit 0 instead, hidden whole
+                if (shaped || t + kUnit - 1 > pos_lo || (a.window > 0 && t <= pos_hi - a.window)) units |= kSpecial;
             }
-            live_next = __ballot_sync(0xffffffffu, units != kNoUnit);
-            edge_next = __ballot_sync(0xffffffffu, edge);
         };
-        // the ring: units kStages - 1 ahead, one group of copies each
-        auto fetch = [&](int f, int stage) {
+        // the ring: units kStages - 1 ahead, one group of copies each; marks: bit
+        // i is the mark of the unit fetched i steps ago
+        uint32_t marks = 0;
+        auto fetch = [&](int f, uint32_t dst) {
+            uint32_t unit = 0;
             if (f < n_units) {
                 if ((f & 31) == 0) look_up(f);
-                const uint32_t unit = __shfl_sync(0xffffffffu, units, f & 31);
-                if (unit != kNoUnit) copier.copy(ring_at + stage * S::kBytes, unit, lane);
+                unit = __shfl_sync(0xffffffffu, units, f);
+                copier.copy(dst, unit & ~kSpecial, lane);
             }
+            marks = __funnelshift_l(unit, marks, 1);
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
 #pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) fetch(i, i);
-        uint32_t live = 0, edge = 0;
-        int stage = 0;
+        for (int i = 0; i < kStages - 1; ++i) fetch(i, ring_at + i * S::kBytes);
+        uint32_t at = ring_at, done = ring_at + (kStages - 1) * S::kBytes;
         for (int i = 0; i < n_units; ++i) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
             __syncwarp();  // every lane's copies of this unit have landed, and nobody reads the last one's stage
-            if ((i & 31) == 0) {
-                live = live_next;
-                edge = edge_next;
-            }
-            fetch(i + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
-            const unsigned char *at = ring + stage * S::kBytes;
-            stage = stage == kStages - 1 ? 0 : stage + 1;
-            const bool here = live & 1u, hidden = edge & 1u;
-            live >>= 1;
-            edge >>= 1;
-            if (here) {
+            fetch(i + kStages - 1, done);
+            const Shared here = {at};
+            done = at;
+            at = at == ring_at + (kStages - 1) * S::kBytes ? ring_at : at + S::kBytes;
+            {
                 float x[NT][4];
                 KUnit<G> ku;
-                ku.load(at + S::kc, at + S::ks, at + S::kz, lane);
+                ku.load(here + S::kc + lo.kc, here + S::ks + lo.ks, here + S::kz + lo.kz);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -691,38 +732,30 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
                     }
                 }
                 VUnit<G> vu;
-                vu.load(at + S::vc, at + S::vs, at + S::vz, lane);
+                vu.load(here + S::vc + lo.vc, here + S::vs + lo.vs, here + S::vz + lo.vz);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) x[nt][i] *= mul[nt][i & 1];
-                if (shaped) {
+                if (marks & (1u << (kStages - 1))) {
+                    const int t = t0 + i * kTile;
+                    const bool gone = (uint32_t)pages[t >> p.lp] >= (uint32_t)p.n_pages;
+                    vu.cut_off(gone ? 0 : s.n - t, lane);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const int c = c0 + min(8 * nt + 2 * t4 + e, cols - 1);
                             const float slope = a.slopes ? a.slopes[h * a.grp + c % a.grp] * kLog2e : 0.f;
-                            const int gap = s.n - s.m + c / a.grp - (t0 + i * kTile) - unit_position(g);
 #pragma unroll
                             for (int r = 0; r < 2; ++r) {
+                                const int gap = s.n - s.m + c / a.grp - t - unit_position(g + 8 * r);
                                 float v = x[nt][2 * r + e];
                                 if (score.capped) v = score.cap_of(v);
-                                x[nt][2 * r + e] = fmaf(-slope, (float)(gap - 8 * r), v);
+                                if (a.slopes) v = fmaf(-slope, (float)gap, v);
+                                if (gone || gap < 0 || (a.window > 0 && gap >= a.window)) v = -INFINITY;
+                                x[nt][2 * r + e] = v;
                             }
-                        }
-                }
-                if (hidden) {
-                    vu.cut_off(s.n - (t0 + i * kTile), lane);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int gap = col_pos(nt, e) - (t0 + i * kTile) - unit_position(g);
-#pragma unroll
-                            for (int r = 0; r < 2; ++r)
-                                if (gap - 8 * r < 0 || (a.window > 0 && gap - 8 * r >= a.window))
-                                    x[nt][2 * r + e] = -INFINITY;
                         }
                 }
                 bool up = false;
@@ -950,6 +983,7 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 2) paged_mass_kernel(co
     __shared__ int64_t s_part[33], s_found[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const PoolView &p = a.p;
+    const LaneOffsets<G> lo(lane);
     const Score score(a);
     auto per_seq = [&](int b) -> int64_t {
         const Sequence s = sequence_of(a, b);
@@ -1000,9 +1034,9 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 2) paged_mass_kernel(co
                 const uint32_t unit = unit_of(p, pages[t0 >> p.lp], t0, h);
                 if (unit == kNoUnit) continue;
                 KUnit<G> ku;
-                ku.load(reinterpret_cast<const char *>(p.kc) + (uint64_t)unit * Stage<G>::kCodes,
-                        reinterpret_cast<const char *>(p.ks) + (uint64_t)unit * Stage<G>::kScales,
-                        reinterpret_cast<const char *>(p.kz) + (uint64_t)unit * Stage<G>::kZeros, lane);
+                ku.load(Global{reinterpret_cast<const unsigned char *>(p.kc) + (uint64_t)unit * Stage<G>::kCodes + lo.kc},
+                        Global{reinterpret_cast<const unsigned char *>(p.ks) + (uint64_t)unit * Stage<G>::kScales + lo.ks},
+                        Global{reinterpret_cast<const unsigned char *>(p.kz) + (uint64_t)unit * Stage<G>::kZeros + lo.kz});
                 float *mass = p.mass + (uint64_t)unit * kUnit;
                 float old[2];
 #pragma unroll
