@@ -705,7 +705,7 @@ spectra_status spectra_sample(const float *logits, int32_t rows, int32_t vocab, 
     const spectra_status st = current_device(&dev);
     if (st != SPECTRA_OK) return st;
     return launch_sample(logits, rows, vocab, stride, u, temperature, top_k, top_p, min_p, ids, logprob,
-                         (cudaStream_t)stream);
+                         (cudaStream_t)stream, dev);
 }
 
 spectra_status spectra_selftest_wait(int32_t kind, void *stream) {

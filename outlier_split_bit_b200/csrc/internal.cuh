@@ -161,7 +161,8 @@ spectra_status paged_device_error(unsigned int *bits, cudaStream_t s);
 int sample_max_vocab();
 spectra_status launch_sample(const float *logits, int rows, int vocab, int64_t stride, const float *u,
                              const float *temperature, const int32_t *top_k, const float *top_p,
-                             const float *min_p, int32_t *ids, float *logp, cudaStream_t s);
+                             const float *min_p, int32_t *ids, float *logp, cudaStream_t s,
+                             const DeviceInfo &dev);
 // Reads (and clears) its flags: bit 0 a NaN logit, bit 1 a row with nothing to choose.
 spectra_status sample_device_error(unsigned int *bits, cudaStream_t s);
 
