@@ -13,6 +13,7 @@ Architecture" (Dev.to abstract re-post), abstract paragraph.
 from __future__ import annotations
 
 import ctypes
+import struct
 from dataclasses import dataclass
 
 import torch
@@ -522,27 +523,32 @@ def spectra_attention_decode(k: KVCache, v: KVCache, q: torch.Tensor, length: in
 
 # ---------------------------------------------------------------- paged KV pool
 
-def _arg(t: torch.Tensor, name: str, dtype, shape, dev=None) -> int:
-    """The pointer of a contiguous device tensor of this type and shape."""
-    if t.dtype is not dtype or tuple(t.shape) != shape or not t.is_cuda or not t.is_contiguous() or \
-            (dev is not None and t.device != dev):
-        raise ValueError(f"{name}: a contiguous {dtype} tensor {list(shape)} on {dev or 'a CUDA device'} is "
-                         f"wanted, got {t.dtype} {list(t.shape)} with strides {t.stride()} on {t.device}")
-    return t.data_ptr()
+def _arg(t: torch.Tensor, name: str, dtype, shape, dev) -> int:
+    """The pointer of a contiguous tensor of this type and shape on dev."""
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name}: a contiguous {dtype} tensor {list(shape)} on {dev} is wanted, "
+                     f"got {t.dtype} {list(t.shape)} with strides {t.stride()} on {t.device}")
 
 
 def _opt(t, name, dtype, shape, dev):
     return None if t is None else _arg(t, name, dtype, shape, dev)
 
 
+# The current stream's handle without a Stream object around it, which costs
+# more than a launch; the public call where this torch has no such entry.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _on(dev: torch.device, stream, call):
     """call(stream handle) with dev as the current device, and with `stream`
     (when one is given) as the stream that allocations belong to."""
     if stream is None and torch.cuda.current_device() == dev.index:
-        return call(torch.cuda.current_stream().cuda_stream)
+        return call(_raw_stream(dev.index))
     with torch.cuda.device(dev):
         if stream is None:
-            return call(torch.cuda.current_stream().cuda_stream)
+            return call(_raw_stream(dev.index))
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(int(stream), device=dev)
         with torch.cuda.stream(stream):
@@ -581,6 +587,8 @@ class KVPool:
         """A pool over existing device buffers: codes uint8, scales int16 (FP16
         bits), zeros int32, mass float32, flat, of the sizes that ``sizes`` gives."""
         sz = cls.sizes(n_heads, head_dim, page_size, n_pages)
+        if not k_codes.is_cuda:
+            raise ValueError(f"k_codes: a tensor on a CUDA device is wanted, got one on {k_codes.device}")
         for t, name, dtype, item in ((k_codes, "codes", torch.uint8, 1), (k_scales, "scales", torch.int16, 2),
                                      (k_zeros, "zeros", torch.int32, 4), (v_codes, "codes", torch.uint8, 1),
                                      (v_scales, "scales", torch.int16, 2), (v_zeros, "zeros", torch.int32, 4)):
@@ -598,6 +606,7 @@ class KVPool:
         self.device = self.k_codes.device
         self._view = _lib.KVPool(n_heads, head_dim, page_size, n_pages, *map(_ptr, buffers), _ptr(mass))
         self._ref = ctypes.byref(self._view)
+        self._ws = {}  # workspace bytes of attention, by (rows, query heads)
 
     def view(self) -> _lib.KVPool:
         return self._view
@@ -628,7 +637,7 @@ class KVPool:
             raise ValueError("k and v hold different numbers of tokens")
         sp = _arg(slots, "slots", torch.int32, (n,), self.device)
         _on(self.device, stream, lambda s: _check(
-            _L.spectra_kv_pool_append(self._ref, kp, vp, n, ks, vs, sp, s), "spectra_kv_pool_append"))
+            _lib.load().spectra_kv_pool_append(self._ref, kp, vp, n, ks, vs, sp, s), "spectra_kv_pool_append"))
 
     def read(self, slots: torch.Tensor, *, out_dtype=torch.bfloat16, stream=None):
         """K and V of the token slots (int32 [n]; negative: zeros), dequantised:
@@ -637,12 +646,18 @@ class KVPool:
         sp = _arg(slots, "slots", torch.int32, (n,), self.device)
 
         def call(s):
-            k, v = torch.empty((2, n, self.n_heads, self.head_dim), dtype=out_dtype, device=self.device).unbind(0)
-            _check(_L.spectra_kv_pool_read(self._ref, sp, n, k.data_ptr(), v.data_ptr(), _DT[out_dtype], s),
+            k = torch.empty((n, self.n_heads, self.head_dim), dtype=out_dtype, device=self.device)
+            v = torch.empty_like(k)
+            _check(_lib.load().spectra_kv_pool_read(self._ref, sp, n, k.data_ptr(), v.data_ptr(), _DT[out_dtype], s),
                    "spectra_kv_pool_read")
             return k, v
 
         return _on(self.device, stream, call)
+
+
+# A spectra_paged_query as bytes (native alignment, as the C struct).
+_PAGED_QUERY = struct.Struct("@PPPiiiiiiffPPPiiP").pack
+assert struct.calcsize("@PPPiiiiiiffPPPiiP") == ctypes.sizeof(PagedQuery)
 
 
 def spectra_attention_paged(pool: KVPool, pages: torch.Tensor, lengths: torch.Tensor, q: torch.Tensor,
@@ -669,26 +684,37 @@ def spectra_attention_paged(pool: KVPool, pages: torch.Tensor, lengths: torch.Te
         raise ValueError(f"q has head_dim {d}, the pool {pool.head_dim}")
     if max_q is None:
         max_q = 1 if q_start is None else max(n_rows, 1)
-    x = PagedQuery(_arg(pages, "pages", torch.int32, (n_seq, max_pages), dev),
-                   _arg(lengths, "lengths", torch.int32, (n_seq,), dev),
-                   _opt(q_start, "q_start", torch.int32, (n_seq + 1,), dev), n_seq, max_pages, n_rows, max_q,
-                   hq, window, d ** -0.5 if scale is None else scale, softcap,
-                   _arg(q, "q", torch.bfloat16, (n_rows, hq, d), dev),
-                   _opt(slopes, "slopes", torch.float32, (hq,), dev), None, 0, int(update_mass), None)
+    heads = (n_rows, hq)
+    shape = (n_rows, hq, d)
+    at_pages = _arg(pages, "pages", torch.int32, (n_seq, max_pages), dev)
+    at_lengths = _arg(lengths, "lengths", torch.int32, (n_seq,), dev)
+    at_start = 0 if q_start is None else _arg(q_start, "q_start", torch.int32, (n_seq + 1,), dev)
+    at_q = _arg(q, "q", torch.bfloat16, shape, dev)
+    at_slopes = 0 if slopes is None else _arg(slopes, "slopes", torch.float32, (hq,), dev)
+    if out is not None:
+        out_dtype = out.dtype
+        _arg(out, "out", out_dtype, shape, dev)
 
     def call(s):
-        o, lse, ws = out, None, workspace
-        if o is None:
-            o = torch.empty((n_rows, hq, d), dtype=out_dtype, device=dev)
-        x.out, x.out_dtype = _arg(o, "out", o.dtype, (n_rows, hq, d), dev), _DT[o.dtype]
-        if want_lse:
-            lse = torch.empty((n_rows, hq), dtype=torch.float32, device=dev)
-            x.lse = lse.data_ptr()
+        lib = _lib.load()
+        if out is not None:
+            o = out
+        elif out_dtype is torch.bfloat16:
+            o = torch.empty_like(q)
+        else:
+            o = torch.empty(shape, dtype=out_dtype, device=dev)
+        lse = torch.empty(heads, dtype=torch.float32, device=dev) if want_lse else None
+        ws = workspace
         if ws is None:
-            need = _L.spectra_attention_paged_workspace_size(pool._ref, n_rows, hq)
+            need = pool._ws.get(heads)
+            if need is None:
+                need = pool._ws[heads] = lib.spectra_attention_paged_workspace_size(pool._ref, n_rows, hq)
             ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        _check(_L.spectra_attention_paged(pool._ref, ctypes.byref(x), ws.data_ptr(),
-                                          ws.numel() * ws.element_size(), s), "spectra_attention_paged")
+        x = _PAGED_QUERY(at_pages, at_lengths, at_start, n_seq, max_pages, n_rows, max_q, hq, window,
+                         d ** -0.5 if scale is None else scale, softcap, at_q, at_slopes, o.data_ptr(),
+                         _DT[out_dtype], 1 if update_mass else 0, lse.data_ptr() if want_lse else 0)
+        _check(lib.spectra_attention_paged(pool._ref, x, ws.data_ptr(), ws.numel() * ws.element_size(), s),
+               "spectra_attention_paged")
         return (o, lse) if want_lse else o
 
     return _on(dev, stream, call)
@@ -713,9 +739,9 @@ def spectra_kv_evict(pool: KVPool, pages: torch.Tensor, lengths: torch.Tensor, d
         if n is None:
             n = torch.empty(n_seq, dtype=torch.int32, device=dev)
         if ws is None:
-            need = _L.spectra_kv_evict_workspace_size(pool._ref, n_seq, max_pages)
+            need = _lib.load().spectra_kv_evict_workspace_size(pool._ref, n_seq, max_pages)
             ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        _check(_L.spectra_kv_evict(pool._ref, *args, _arg(n, "new_lengths", torch.int32, (n_seq,), dev),
+        _check(_lib.load().spectra_kv_evict(pool._ref, *args, _arg(n, "new_lengths", torch.int32, (n_seq,), dev),
                                    ws.data_ptr(), ws.numel() * ws.element_size(), s), "spectra_kv_evict")
         return n
 
@@ -747,7 +773,7 @@ def spectra_sample(logits: torch.Tensor, u: torch.Tensor, *, temperature: torch.
     def call(s):
         ids = torch.empty(rows, dtype=torch.int32, device=dev)
         logp = torch.empty(rows, dtype=f32, device=dev)
-        _check(_L.spectra_sample(logits.data_ptr(), rows, vocab, stride, *args, ids.data_ptr(), logp.data_ptr(),
+        _check(_lib.load().spectra_sample(logits.data_ptr(), rows, vocab, stride, *args, ids.data_ptr(), logp.data_ptr(),
                                  s), "spectra_sample")
         return ids, logp
 
