@@ -589,8 +589,8 @@ spectra_status spectra_kv_pool_append(const spectra_kv_pool *pool, const uint16_
     const int64_t row = (int64_t)pool->n_heads * pool->head_dim;
     if (k_stride < row || v_stride < row || k_stride > ((int64_t)1 << 40) || v_stride > ((int64_t)1 << 40))
         return SPECTRA_ERR_SHAPE;
-    // every warp's item must have a number, and the grid must fit
-    if ((int64_t)n_tok * pool->n_heads > ((int64_t)1 << 30)) return SPECTRA_ERR_SHAPE;
+    // every thread (four to a vector) must have a 32-bit number
+    if ((int64_t)n_tok * pool->n_heads > ((int64_t)1 << 29)) return SPECTRA_ERR_SHAPE;
     if (!aligned16(k) || !aligned16(v) || k_stride % 8 != 0 || v_stride % 8 != 0 || !aligned4(slots))
         return SPECTRA_ERR_ALIGN;
     DeviceInfo dev;
@@ -606,7 +606,7 @@ spectra_status spectra_kv_pool_read(const spectra_kv_pool *pool, const int32_t *
     if (n < 0 || (out_dtype != SPECTRA_F32 && out_dtype != SPECTRA_BF16)) return SPECTRA_ERR_INVALID_ARG;
     if (n == 0) return SPECTRA_OK;
     if (!slots || (!k_out && !v_out)) return SPECTRA_ERR_INVALID_ARG;
-    if ((int64_t)n * pool->n_heads > ((int64_t)1 << 30)) return SPECTRA_ERR_SHAPE;
+    if ((int64_t)n * pool->n_heads > ((int64_t)1 << 29)) return SPECTRA_ERR_SHAPE;
     if (!aligned4(slots) || !aligned16(k_out) || !aligned16(v_out)) return SPECTRA_ERR_ALIGN;
     DeviceInfo dev;
     st = current_device(&dev);
@@ -687,7 +687,7 @@ spectra_status spectra_kv_evict(const spectra_kv_pool *pool, const int32_t *page
     st = current_device(&dev);
     if (st != SPECTRA_OK) return st;
     return launch_evict(*pool, pages, max_pages, lengths, n_seq, dst_pages, dst_max_pages, budget, recent,
-                        new_lengths, workspace, (cudaStream_t)stream);
+                        new_lengths, workspace, (cudaStream_t)stream, dev);
 }
 
 spectra_status spectra_sample(const float *logits, int32_t rows, int32_t vocab, int64_t stride,

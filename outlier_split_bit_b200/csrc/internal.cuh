@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "spectra.h"
 
 namespace spectra {
@@ -26,6 +28,17 @@ struct DeviceInfo {
 // Cached per-device properties of the current device.  Returns
 // SPECTRA_ERR_UNSUPPORTED unless the device is compute capability 10.0.
 spectra_status current_device(DeviceInfo *out);
+
+// Lets a kernel use up to `bytes` of dynamic shared memory on this device,
+// once: `ready` holds a bit per device.  (Two threads may both set it; the
+// setting is the same.)
+inline cudaError_t allow_smem(const void *kernel, int bytes, const DeviceInfo &dev, std::atomic<uint64_t> *ready) {
+    const uint64_t bit = (uint64_t)1 << dev.device;
+    if (ready->load(std::memory_order_acquire) & bit) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) ready->fetch_or(bit, std::memory_order_release);
+    return e;
+}
 
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -145,7 +158,7 @@ size_t evict_workspace_bytes(int n_seq, int n_heads, int64_t positions);
 spectra_status launch_evict(const spectra_kv_pool &pool, const int32_t *pages, int max_pages,
                             const int32_t *lengths, int n_seq, const int32_t *dst_pages,
                             int dst_max_pages, int budget, int recent, int32_t *new_lengths, void *ws,
-                            cudaStream_t s);
+                            cudaStream_t s, const DeviceInfo &dev);
 // Reads (and clears) the pool's flags: bit 0 non-finite value, bit 1 FP16
 // range, bit 2 a slot, page or length out of bounds.
 spectra_status pool_device_error(unsigned int *bits, cudaStream_t s);

@@ -1119,11 +1119,9 @@ template <int G, int NT, bool EXACT>
 cudaError_t run_attention(const PagedArgs &a, const DeviceInfo &dev, bool mass, cudaStream_t s) {
     constexpr int C = 8 * NT;
     const size_t smem = ring_bytes<G>() + (NT > 1 ? NT * G * 512 : 0);
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(paged_attention_kernel<G, NT, EXACT>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    static std::atomic<uint64_t> ready{0};
+    cudaError_t e = allow_smem((const void *)paged_attention_kernel<G, NT, EXACT>, (int)smem, dev, &ready);
+    if (e != cudaSuccess) return e;
     // runs: one wave, and no more than the tables' width allows tiles for
     const int64_t cols = (int64_t)a.max_q * a.grp, n_ct = (cols + C - 1) / C;
     const int64_t tiles = (((int64_t)a.max_pages << a.p.lp) + kTile - 1) / kTile;
@@ -1135,7 +1133,7 @@ cudaError_t run_attention(const PagedArgs &a, const DeviceInfo &dev, bool mass, 
         return (unsigned)(want < most ? want : most);
     };
     const unsigned grid = runs(heads * n_ct, min_ctas<G, NT>());
-    cudaError_t e = launch(paged_attention_kernel<G, NT, EXACT>, dim3(grid), smem, false, s, a);
+    e = launch(paged_attention_kernel<G, NT, EXACT>, dim3(grid), smem, false, s, a);
     if (e != cudaSuccess) return e;
     e = launch(paged_join_kernel<G, NT, EXACT>, dim3(grid, (unsigned)(cols < C ? cols : C)), 0, true, s, a);
     if (e != cudaSuccess || !mass) return e;

@@ -13,157 +13,265 @@
 namespace spectra {
 namespace {
 
+// N words to or from p, in the widest pieces that N words lie aligned for.
+template <int N>
+__device__ __forceinline__ void store_words(uint32_t *p, const uint32_t (&r)[N]) {
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) *reinterpret_cast<uint4 *>(p + i) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
+    } else if constexpr (N % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) *reinterpret_cast<uint2 *>(p + i) = make_uint2(r[i], r[i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) p[i] = r[i];
+    }
+}
+template <int N>
+__device__ __forceinline__ void read_words(uint32_t (&r)[N], const uint32_t *p) {
+    if constexpr (N % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p + i);
+            r[i] = v.x; r[i + 1] = v.y; r[i + 2] = v.z; r[i + 3] = v.w;
+        }
+    } else if constexpr (N % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            const uint2 v = *reinterpret_cast<const uint2 *>(p + i);
+            r[i] = v.x; r[i + 1] = v.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) r[i] = p[i];
+    }
+}
+
 // bit 0: a non-finite value was appended; bit 1: a group's scale overflowed
 // FP16; bit 2: a slot or page outside the pool.
 __device__ unsigned int g_pool_error;
 
-// One thread quantises 8 channels: the four threads of a group share its
-// minimum and maximum, a head's 4G threads lie in one warp (32 / 4G heads per
-// warp).  Item = (token, K or V, head), heads innermost, so a warp reads
-// contiguous rows.
+// Four threads hold one vector (a token's K or V of one head): thread w the
+// channels 32g + 8w .. +7 of every group g, so its codes are the pool's word w
+// of every group, G words that lie together (V: halfwords 2w and 2w + 1, the
+// same bytes).
 //
-// The quantiser is quant.cuh's, bit for bit, with the scale's quotient in
-// double and the codes' in single precision: rint(v / S) only depends on how
-// v / S compares with k + 1/2.  For v != (k + 1/2) S, 2v - (2k+1)S is a
-// multiple of the smaller of S's and 2v's last place; S has 11 significant
-// bits and v has 8, so the quotient is at least 2^-12 from the tie.  It is at
-// most 15 * 2^8 in magnitude (two different BF16 values near v differ by
-// 2^-8 |v| or more, and S is their difference over 15), where a correctly
-// rounded FP32 quotient is off by at most 2^-13; so it lies on the same side,
-// and exact ties are exact in FP32.  (A subnormal S = j 2^-24 doubles both
-// the bound on the quotient and the distance.)
+// A group's minimum and maximum take two shuffles; its scale and zero point
+// are found by one of the four threads (group g by thread g % 4) and handed
+// round.  The arithmetic is quant.cuh's, bit for bit, without its divisions:
+//
+// Scale, RN16((hi - lo) / 15): where hi - lo is exact in FP32 (d, checked by
+// taking it apart again), the FP32 quotient q = RN(d / 15) rounds to FP16 as
+// d / 15 does.  It would not only if q fell on a midpoint of FP16 that d / 15
+// is not on; but a midpoint m has 12 bits, 15 m is a multiple of d's last
+// place u (or of a larger power of two), so |d / 15 - m| >= u / 15, and that
+// is more than q's half step, u / 16 at most.  Otherwise the double quotient
+// is taken.
+//
+// Codes, rint(v / S): q = v * (1 / S) in FP32, cut to [-32, 32] (what lies
+// beyond is cut to 0 or 15 in the end), is off by 2^-18 at most.  A true quotient
+// that is not k + 1/2 lies 2^-12 or more from it: 2v - (2k+1)S is a multiple of
+// the smaller of S's last place (2^-10 of S or more, or S / j for a subnormal
+// S = j 2^-24) and 2v's (2^-8 of S or more, near a tie).  So 2q within 2^-12 of
+// a whole number means that 2v / S is that number, or near an even one, where
+// it makes no difference; q is set to it, and rounding half to even gives the
+// double quotient's result.
+constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: a float sum with it is a whole number
+
+__device__ __forceinline__ uint32_t group_scale(float lo, float hi, bool bad, float *zero_out, unsigned int *flags) {
+    const float d = hi - lo;
+    unsigned short s;
+    if (hi - d == lo && d + lo == hi && d < 3e38f) {
+        s = __half_as_ushort(__float2half_rn(__fdiv_rn(d, 15.f)));
+    } else {
+        const double q15 = __ddiv_rn(__dsub_rn((double)hi, (double)lo), 15.0);
+        asm("cvt.rn.f16.f64 %0, %1;" : "=h"(s) : "d"(q15));
+    }
+    if (bad) {
+        *flags |= 1u;
+        s = 0;  // the group is stored as zeros
+    } else if ((s & 0x7FFFu) == 0x7C00u) {
+        *flags |= 2u;
+        s = 0;
+    }
+    const float S = __half2float(__ushort_as_half(s));
+    float z = 0.f;
+    if (S != 0.f) z = fminf(fmaxf(rintf(__fdiv_rn(-lo, S)), 0.f), 15.f);
+    *zero_out = z;
+    return s;
+}
+
+template <int G>
 __global__ void __launch_bounds__(256) pool_append_kernel(PoolView p, const uint16_t *__restrict__ k,
                                                           const uint16_t *__restrict__ v, int64_t k_stride,
                                                           int64_t v_stride, const int32_t *__restrict__ slots,
-                                                          int64_t n_items) {
-    const int G = p.G, tph = 4 * G, hpw = 32 / tph;  // threads per head, heads per warp
-    const int lane = threadIdx.x & 31;
-    const int sub = lane / tph, in = lane - sub * tph;
-    const int64_t warp = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    const int64_t item = warp * hpw + sub;  // (token * 2 + which) * H + h
-    bool live = sub < hpw && item < n_items;
-    int h = 0, which = 0, g = in >> 2, part = in & 3;
-    int32_t ts = -1;
-    uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-    if (live) {
-        const int64_t tw = item / p.H;
-        h = (int)(item - tw * p.H);
-        which = (int)(tw & 1);
-        const int64_t tok = tw >> 1;
-        ts = slots[tok];
-        if (ts >= p.token_slots()) {
-            if (in == 0) atomicOr(&g_pool_error, 4u);
-            ts = -1;
-        }
-        const uint16_t *src = which ? v + tok * v_stride : k + tok * k_stride;
-        raw = *reinterpret_cast<const uint4 *>(src + (int64_t)h * 32 * G + 8 * in);
+                                                          uint32_t n_vectors) {
+    const uint32_t i = (blockIdx.x * 256u + threadIdx.x) >> 2;  // token * H + head
+    const int w = threadIdx.x & 3, lane = threadIdx.x & 31, which = blockIdx.y;
+    const bool in = i < n_vectors;
+    const uint32_t tok = in ? i / (uint32_t)p.H : 0, h = in ? i - tok * (uint32_t)p.H : 0;
+    int32_t ts = in ? slots[tok] : -1;
+    if (ts >= p.token_slots()) {
+        atomicOr(&g_pool_error, 4u);
+        ts = -1;
     }
-    live = live && ts >= 0;
-    const uint32_t r4[4] = {raw.x, raw.y, raw.z, raw.w};
-    float x[8];
-    bool bad = false;
-    float lo = 0.f, hi = 0.f;
+    const uint16_t *src = (which ? v + tok * v_stride : k + tok * k_stride) + h * 32 * G + 8 * w;
+    uint4 raw[G];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t b = i & 1 ? r4[i >> 1] & 0xFFFF0000u : r4[i >> 1] << 16;
-        bad |= (b & 0x7F800000u) == 0x7F800000u;
-        x[i] = __uint_as_float(b) + 0.0f;  // -0 reads as +0
-        lo = i == 0 ? x[i] : fminf(lo, x[i]);
-        hi = i == 0 ? x[i] : fmaxf(hi, x[i]);
+    for (int g = 0; g < G; ++g)
+        raw[g] = ts >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src + 32 * g)) : make_uint4(0u, 0u, 0u, 0u);
+    float lo[G], hi[G];
+    uint32_t bad = 0;  // bit g: group g holds a NaN or infinity
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const uint32_t r4[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
+        float top = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float a = __uint_as_float(r4[j] << 16) + 0.f, b = __uint_as_float(r4[j] & 0xFFFF0000u) + 0.f;
+            lo[g] = j == 0 ? fminf(a, b) : fminf(lo[g], fminf(a, b));
+            hi[g] = j == 0 ? fmaxf(a, b) : fmaxf(hi[g], fmaxf(a, b));
+            top = fmaf(a, 0.f, fmaf(b, 0.f, top));  // NaN if one of them is not finite
+        }
+        bad |= top == 0.f ? 0u : 1u << g;
     }
 #pragma unroll
     for (int o = 1; o <= 2; o <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        bad |= (bool)__shfl_xor_sync(0xffffffffu, (int)bad, o);
-    }
-    const double q15 = __ddiv_rn(__dsub_rn((double)hi, (double)lo), 15.0);
-    unsigned short sbits;
-    asm("cvt.rn.f16.f64 %0, %1;" : "=h"(sbits) : "d"(q15));
-    unsigned int flags = 0;
-    if (bad) flags = 1u;
-    else if ((sbits & 0x7FFFu) == 0x7C00u) flags = 2u;
-    if (flags) sbits = 0;  // the group is stored as zeros
-    const float S = __half2float(__ushort_as_half(sbits));
-    uint32_t z = 0, word = 0;
-    if (S != 0.f) {
-        const float zf = fminf(fmaxf(rintf(__fdiv_rn(-lo, S)), 0.f), 15.f);
-        z = (uint32_t)zf;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float c = fminf(fmaxf(rintf(__fdiv_rn(x[i], S)) + zf, 0.f), 15.f);
-            word |= (uint32_t)c << (4 * i);
+        for (int g = 0; g < G; ++g) {
+            lo[g] = fminf(lo[g], __shfl_xor_sync(0xffffffffu, lo[g], o));
+            hi[g] = fmaxf(hi[g], __shfl_xor_sync(0xffffffffu, hi[g], o));
+        }
+        bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+    }
+    constexpr int kOwn = (G + 3) / 4;  // groups of a thread's own: w, w + 4
+    float own_z[kOwn];
+    uint32_t own_s[kOwn];
+    unsigned int flags = 0;
+#pragma unroll
+    for (int e = 0; e < kOwn; ++e) {
+        float l = lo[4 * e], u = hi[4 * e];
+#pragma unroll
+        for (int j = 1; j < 4; ++j)
+            if (4 * e + j < G && w == j) {
+                l = lo[4 * e + j];
+                u = hi[4 * e + j];
+            }
+        own_s[e] = group_scale(l, u, (bad >> (4 * e + w)) & 1u, &own_z[e], &flags);
+    }
+    if (flags && ts >= 0) atomicOr(&g_pool_error, flags);
+    uint32_t word[G], sc[G], zw = 0;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        sc[g] = __shfl_sync(0xffffffffu, own_s[g / 4], (lane & ~3) + (g & 3));
+        const int z = (int)__shfl_sync(0xffffffffu, own_z[g / 4], (lane & ~3) + (g & 3));
+        zw |= (uint32_t)z << (4 * g);
+        const float S = __half2float(__ushort_as_half((unsigned short)sc[g]));
+        const float r2 = S != 0.f ? __fdiv_rn(2.f, S) : 0.f;  // 0: codes 0 below (z is 0, and every q)
+        const uint32_t r4[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
+        uint32_t c8 = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float x = __uint_as_float(j & 1 ? r4[j >> 1] & 0xFFFF0000u : r4[j >> 1] << 16);
+            const float q2 = fminf(fmaxf(x * r2, -64.f), 64.f);
+            const float near = (q2 + kMagic) - kMagic;
+            const float q = (fabsf(q2 - near) < 0x1p-12f ? near : q2) * 0.5f;
+            const int c = __float_as_int(q + kMagic) - __float_as_int(kMagic) + z;
+            c8 |= (uint32_t)min(max(c, 0), 15) << (4 * j);
+        }
+        word[g] = sc[g] ? c8 : 0u;  // (a bad group's values are NaN here)
+    }
+    if (ts < 0) return;
+    const int64_t slot = p.slot(ts, (int)h);
+    if (which) {
+        // halfwords 2w and 2w + 1 of every group: G and G of them
+        uint32_t v16[G];
+#pragma unroll
+        for (int e = 0; e < 2 * G; ++e) {
+            const uint32_t half = e < G ? word[e] & 0xFFFFu : word[e - G] >> 16;
+            if (e & 1) v16[e / 2] |= half << 16;
+            else v16[e / 2] = half;
+        }
+        store_words<G>(reinterpret_cast<uint32_t *>(p.vc + slot * 8 * G + 2 * w * G), v16);
+    } else {
+        store_words<G>(p.kc + slot * 4 * G + w * G, word);
+    }
+    if (w == 0) {
+        uint16_t *s = (which ? p.vs : p.ks) + slot * G;
+        if constexpr (G % 2 == 0) {
+            uint32_t pair[G / 2];
+#pragma unroll
+            for (int g = 0; g < G; g += 2) pair[g / 2] = sc[g] | sc[g + 1] << 16;
+            store_words<G / 2>(reinterpret_cast<uint32_t *>(s), pair);
+        } else {
+#pragma unroll
+            for (int g = 0; g < G; ++g) s[g] = (uint16_t)sc[g];
         }
     }
-    // the head's zero word: nibble g from the first thread of group g
-    uint32_t zw = 0;
-    const int base = sub < hpw ? sub * tph : 0;
-    for (int j = 0; j < G; ++j) zw |= __shfl_sync(0xffffffffu, z, base + 4 * j) << (4 * j);
-    if (!live) return;
-    if (flags && part == 0) atomicOr(&g_pool_error, flags);
-    const int64_t slot = p.slot(ts, h);
-    if (which == 0) {
-        p.kc[slot * 4 * G + part * G + g] = word;
-        if (part == 0) p.ks[slot * G + g] = sbits;
-        if (in == 0) p.kz[slot] = zw;
-        if (in == 1 && p.mass) p.mass[slot] = 0.f;
-    } else {
-        uint16_t *c = p.vc + slot * 8 * G + (2 * part) * G + g;
-        c[0] = (uint16_t)word;
-        c[G] = (uint16_t)(word >> 16);
-        if (part == 0) p.vs[slot * G + g] = sbits;
-        if (in == 0) p.vz[slot] = zw;
-    }
+    if (w == 1) (which ? p.vz : p.kz)[slot] = zw;
+    if (w == 2 && which == 0 && p.mass) p.mass[slot] = 0.f;
 }
 
-// Token slots dequantised: one thread per 8 channels of (token, head).
-template <bool BF16>
+// Token slots dequantised, four threads to a vector as above.
+template <int G, bool BF16>
 __global__ void __launch_bounds__(256) pool_read_kernel(PoolView p, const int32_t *__restrict__ slots,
-                                                        int64_t n_threads, void *__restrict__ k_out,
+                                                        uint32_t n_vectors, void *__restrict__ k_out,
                                                         void *__restrict__ v_out) {
-    const int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (e >= n_threads) return;
-    const int G = p.G, per = p.H * 4 * G;
-    const int64_t tok = e / per;
-    const int in = (int)(e - tok * per);
-    const int h = in / (4 * G), gp = in - h * 4 * G, g = gp >> 2, part = gp & 3;
+    const uint32_t i = (blockIdx.x * 256u + threadIdx.x) >> 2;
+    const int w = threadIdx.x & 3, which = blockIdx.y;
+    void *out = which ? v_out : k_out;
+    if (i >= n_vectors || !out) return;
+    const uint32_t tok = i / (uint32_t)p.H, h = i - tok * (uint32_t)p.H;
     int32_t ts = slots[tok];
     if (ts >= p.token_slots()) {
-        if (in == 0) atomicOr(&g_pool_error, 4u);
+        atomicOr(&g_pool_error, 4u);
         ts = -1;
     }
-    const int64_t slot = ts >= 0 ? p.slot(ts, h) : 0;
+    uint32_t word[G], s[G], zw = 0;
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        void *out = which ? v_out : k_out;
-        if (!out) continue;
-        float x[8];
-        if (ts >= 0) {
-            uint32_t word;
-            if (which == 0) {
-                word = p.kc[slot * 4 * G + part * G + g];
-            } else {
-                const uint16_t *c = p.vc + slot * 8 * G + (2 * part) * G + g;
-                word = (uint32_t)c[0] | ((uint32_t)c[G] << 16);
-            }
-            const float s = __half2float(__ushort_as_half((which ? p.vs : p.ks)[slot * G + g]));
-            const int z = (int)(((which ? p.vz : p.kz)[slot] >> (4 * g)) & 15u);
+    for (int g = 0; g < G; ++g) word[g] = s[g] = 0;
+    if (ts >= 0) {
+        const int64_t slot = p.slot(ts, (int)h);
+        zw = (which ? p.vz : p.kz)[slot];
+        const uint16_t *sp = (which ? p.vs : p.ks) + slot * G;
+        if constexpr (G % 2 == 0) {
+            uint32_t pair[G / 2];
+            read_words<G / 2>(pair, reinterpret_cast<const uint32_t *>(sp));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = (float)((int)((word >> (4 * i)) & 15u) - z) * s;
+            for (int g = 0; g < G; ++g) s[g] = g & 1 ? pair[g / 2] >> 16 : pair[g / 2] & 0xFFFFu;
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = 0.f;
+            for (int g = 0; g < G; ++g) s[g] = sp[g];
         }
-        if (BF16) {
-            uint32_t w[4];
+        if (which) {
+            uint32_t v16[G];
+            read_words<G>(v16, reinterpret_cast<const uint32_t *>(p.vc + slot * 8 * G + 2 * w * G));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-                w[i] = *reinterpret_cast<const uint32_t *>(&b);
+            for (int e = 0; e < 2 * G; ++e) {
+                const uint32_t half = e & 1 ? v16[e / 2] >> 16 : v16[e / 2] & 0xFFFFu;
+                if (e < G) word[e] = half;
+                else word[e - G] |= half << 16;
             }
-            reinterpret_cast<uint4 *>(out)[e] = make_uint4(w[0], w[1], w[2], w[3]);
         } else {
-            float4 *o = reinterpret_cast<float4 *>(out) + 2 * e;
+            read_words<G>(word, p.kc + slot * 4 * G + w * G);
+        }
+    }
+    const int64_t at = (int64_t)i * 32 * G + 8 * w;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const float S = __half2float(__ushort_as_half((unsigned short)s[g]));
+        const float z = (float)((zw >> (4 * g)) & 15u);
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = ((float)((word[g] >> (4 * j)) & 15u) - z) * S;
+        if (BF16) {
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[j]) : "f"(x[2 * j + 1]), "f"(x[2 * j]));
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + at + 32 * g) = make_uint4(o[0], o[1], o[2], o[3]);
+        } else {
+            float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(out) + at + 32 * g);
             o[0] = make_float4(x[0], x[1], x[2], x[3]);
             o[1] = make_float4(x[4], x[5], x[6], x[7]);
         }
@@ -172,10 +280,15 @@ __global__ void __launch_bounds__(256) pool_read_kernel(PoolView p, const int32_
 
 // ---- eviction ----
 // Two launches: select (one CTA per sequence and head) finds the smallest
-// kept key and, per chunk of positions, the number of kept positions before
-// it; move (one CTA per chunk) copies the chunk's kept entries to their
-// places in the fresh pages.
+// kept key by a radix descent and, per chunk of positions, the number of kept
+// positions before it; move (one CTA per chunk, launched as a programmatic
+// dependent) copies the chunk's kept entries to their places in the fresh
+// pages.  Select reads every weight once, through the page table with eight
+// look-ups in flight per thread, and keeps the keys in shared memory (of the
+// first kKeys positions; what lies past them is read again in each pass).
 constexpr int kSelThreads = 1024;
+constexpr int kKeys = 40960;
+constexpr int kLookUps = 8;
 constexpr int kMoveChunk = 256;  // positions per chunk (= threads of a move CTA)
 
 struct EvictArgs {
@@ -216,23 +329,42 @@ __device__ __forceinline__ uint32_t evict_key(const EvictArgs &a, const int32_t 
 }
 
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) {
+    extern __shared__ uint32_t keys[];
     __shared__ int hist[kBins];
     __shared__ int part[33];
     __shared__ int s_bin, s_above;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int b = blockIdx.y, h = blockIdx.x, tid = threadIdx.x;
     const EvictPlan e = evict_plan(a, b);
     const int32_t *pages = a.pages + (int64_t)b * a.max_pages;
     if (h == 0 && tid == 0) a.new_lengths[b] = e.kept;
     const int64_t bh = (int64_t)b * a.p.H + h;
     if (e.need == e.old) return;  // everything stays
+    const int cached = min(e.old, kKeys);
+    for (int t0 = tid; t0 < cached; t0 += kLookUps * kSelThreads) {
+        int32_t ts[kLookUps];
+        float m[kLookUps];
+#pragma unroll
+        for (int j = 0; j < kLookUps; ++j) {
+            const int t = t0 + j * kSelThreads;
+            ts[j] = t < cached ? a.p.token_slot(pages, t) : -1;
+        }
+#pragma unroll
+        for (int j = 0; j < kLookUps; ++j) m[j] = ts[j] >= 0 ? a.p.mass[a.p.slot(ts[j], h)] : 0.f;
+#pragma unroll
+        for (int j = 0; j < kLookUps; ++j)
+            if (t0 + j * kSelThreads < cached) keys[t0 + j * kSelThreads] = ts[j] >= 0 ? float_key(m[j]) : 0u;
+    }
+    auto key_at = [&](int t) { return t < cached ? keys[t] : evict_key(a, pages, h, t); };
     uint32_t prefix = 0;
     int need = e.need;
     if (need > 0) {
         for (int d = 0; d < kDigits; ++d) {
             for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
             __syncthreads();
+#pragma unroll 4
             for (int t = tid; t < e.old; t += kSelThreads) {
-                const uint32_t key = evict_key(a, pages, h, t);
+                const uint32_t key = key_at(t);
                 if (digit_in(key, prefix, d)) atomicAdd(&hist[(key >> digit_shift(d)) & digit_mask(d)], 1);
             }
             __syncthreads();
@@ -243,6 +375,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) 
         }
     } else {
         prefix = 0xFFFFFFFFu;  // no float has this key
+        __syncthreads();
     }
     if (tid == 0) {
         a.thr[bh] = prefix;
@@ -254,9 +387,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) 
     const int nch = (e.n + kMoveChunk - 1) / kMoveChunk;
     for (int c = warp; c < nch; c += kSelThreads / 32) {
         int gt = 0, eq = 0;
+#pragma unroll
         for (int i = 0; i < kMoveChunk; i += 32) {
             const int t = c * kMoveChunk + i + lane;
-            const uint32_t key = t < e.old ? evict_key(a, pages, h, t) : 0u;
+            const uint32_t key = t < e.old ? key_at(t) : 0u;
             gt += __popc(__ballot_sync(0xffffffffu, t < e.old && key > prefix));
             eq += __popc(__ballot_sync(0xffffffffu, t < e.old && key == prefix));
         }
@@ -278,66 +412,67 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) 
     }
 }
 
+template <int G>
 __global__ void __launch_bounds__(kMoveChunk) evict_move_kernel(EvictArgs a) {
     __shared__ int part[33];
-    __shared__ int64_t s_src[kMoveChunk], s_dst[kMoveChunk];
+    __shared__ int64_t s_src[kMoveChunk], s_dst[kMoveChunk];  // the chunk's kept entries
     const int b = blockIdx.z, h = blockIdx.y, c = blockIdx.x, tid = threadIdx.x;
     const EvictPlan e = evict_plan(a, b);
     const int t = c * kMoveChunk + tid;
-    if (c * kMoveChunk >= e.n) return;
-    const int32_t *pages = a.pages + (int64_t)b * a.max_pages;
+    if (c * kMoveChunk >= e.n) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
     const int64_t bh = (int64_t)b * a.p.H + h;
-    int32_t ts = -1;
-    if (t < e.n) ts = a.p.token_slot(pages, t);
-    int at = -1;  // place among the kept
-    if (e.need == e.old) {
-        if (t < e.n) at = t;
-    } else {
+    const int32_t ts = t < e.n ? a.p.token_slot(a.pages + (int64_t)b * a.max_pages, t) : -1;
+    const int64_t src = ts >= 0 ? a.p.slot(ts, h) : -1;
+    const float mass = src >= 0 ? a.p.mass[src] : 0.f;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // select's results; nothing was written before
+    const bool old = t < e.old;
+    bool keep = t < e.n;
+    int base = c * kMoveChunk, rank = tid, total = min(kMoveChunk, e.n - c * kMoveChunk);
+    if (e.need != e.old) {
         const uint32_t thr = a.thr[bh];
         const int ties = a.ties[bh];
         const int2 before = a.before[bh * a.nch + c];
-        const bool old = t < e.old;
-        const uint32_t key = old && ts >= 0 ? float_key(a.p.mass[a.p.slot(ts, h)]) : 0u;
-        int total;
+        const uint32_t key = old && src >= 0 ? float_key(mass) : 0u;
         const int eq = before.y + block_exclusive((int)(old && key == thr), part, &total);
         __syncthreads();
-        const bool keep = t < e.n && (!old || key > thr || (key == thr && eq < ties));
-        const int rank = block_exclusive((int)keep, part, &total);
+        keep = t < e.n && (!old || key > thr || (key == thr && eq < ties));
+        rank = block_exclusive((int)keep, part, &total);
         // kept before the chunk: keys above the threshold, the first ties, and
         // (in the last chunks) entries past `old`
-        const int past = max(0, c * kMoveChunk - e.old);
-        if (keep) at = before.x + min(before.y, ties) + past + rank;
+        base = before.x + min(before.y, ties) + max(0, c * kMoveChunk - e.old);
     }
-    int64_t src = -1, dst = -1;
-    if (at >= 0) {
-        const int32_t td = a.p.token_slot(a.dst_pages + (int64_t)b * a.dst_max_pages, at);
-        if (ts < 0 || td < 0) {
+    if (keep) {
+        const int32_t td = a.p.token_slot(a.dst_pages + (int64_t)b * a.dst_max_pages, base + rank);
+        int64_t dst = -1;
+        if (src < 0 || td < 0) {
             atomicOr(&g_pool_error, 4u);
         } else {
-            src = a.p.slot(ts, h);
             dst = a.p.slot(td, h);
+            a.p.kz[dst] = a.p.kz[src];
+            a.p.vz[dst] = a.p.vz[src];
+            a.p.mass[dst] = mass;
         }
-    }
-    s_src[tid] = src;
-    s_dst[tid] = dst;
-    if (src >= 0) {
-        a.p.kz[dst] = a.p.kz[src];
-        a.p.vz[dst] = a.p.vz[src];
-        a.p.mass[dst] = a.p.mass[src];
+        s_src[rank] = src;
+        s_dst[rank] = dst;
     }
     __syncthreads();
-    // code records (G 16-byte pieces of K and of V) and scales, neighbouring
+    // code records, G 16-byte pieces of K and of V, and scales: neighbouring
     // threads on neighbouring pieces of an entry
-    const int G = a.p.G;
     uint4 *kc = reinterpret_cast<uint4 *>(a.p.kc), *vc = reinterpret_cast<uint4 *>(a.p.vc);
-    for (int i = tid; i < kMoveChunk * G; i += kMoveChunk) {
+#pragma unroll 2
+    for (int i = tid; i < total * G; i += kMoveChunk) {
         const int s = i / G, g = i - s * G;
-        const int64_t from = s_src[s], to = s_dst[s];
-        if (from >= 0) {
-            kc[to * G + g] = kc[from * G + g];
-            vc[to * G + g] = vc[from * G + g];
-            a.p.ks[to * G + g] = a.p.ks[from * G + g];
-            a.p.vs[to * G + g] = a.p.vs[from * G + g];
+        const int64_t from = s_src[s] * G + g, to = s_dst[s] * G + g;
+        if (to >= 0) {
+            const uint4 x = kc[from], y = vc[from];
+            const uint16_t u = a.p.ks[from], v = a.p.vs[from];
+            kc[to] = x;
+            vc[to] = y;
+            a.p.ks[to] = u;
+            a.p.vs[to] = v;
         }
     }
 }
@@ -346,23 +481,41 @@ int64_t evict_chunks(int64_t positions) { return cdiv(positions, kMoveChunk); }
 
 }  // namespace
 
+// The kernels' G, from the pool's head_dim.
+#define SPECTRA_POOL_GROUPS(G_, CALL)    \
+    switch (G_) {                        \
+        case 1: CALL(1); break;          \
+        case 2: CALL(2); break;          \
+        case 3: CALL(3); break;          \
+        case 4: CALL(4); break;          \
+        case 5: CALL(5); break;          \
+        case 6: CALL(6); break;          \
+        case 7: CALL(7); break;          \
+        default: CALL(8); break;         \
+    }
+
 spectra_status launch_pool_append(const spectra_kv_pool &pool, const uint16_t *k, const uint16_t *v,
                                   int n_tok, int64_t k_stride, int64_t v_stride, const int32_t *slots,
                                   cudaStream_t s) {
     const PoolView p = PoolView::of(pool);
-    const int64_t items = (int64_t)n_tok * 2 * p.H;
-    const int64_t warps = cdiv(items, 32 / (4 * p.G));
-    pool_append_kernel<<<(unsigned)cdiv(warps * 32, 256), 256, 0, s>>>(p, k, v, k_stride, v_stride, slots, items);
+    const uint32_t n = (uint32_t)n_tok * (uint32_t)p.H;
+    const dim3 grid((unsigned)cdiv((int64_t)n * 4, 256), 2);
+#define SPECTRA_CALL(G) pool_append_kernel<G><<<grid, 256, 0, s>>>(p, k, v, k_stride, v_stride, slots, n)
+    SPECTRA_POOL_GROUPS(p.G, SPECTRA_CALL)
+#undef SPECTRA_CALL
     return cudaGetLastError() == cudaSuccess ? SPECTRA_OK : SPECTRA_ERR_CUDA;
 }
 
-spectra_status launch_pool_read(const spectra_kv_pool &pool, const int32_t *slots, int n, void *k_out,
+spectra_status launch_pool_read(const spectra_kv_pool &pool, const int32_t *slots, int n_tok, void *k_out,
                                 void *v_out, bool bf16, cudaStream_t s) {
     const PoolView p = PoolView::of(pool);
-    const int64_t threads = (int64_t)n * p.H * 4 * p.G;
-    const unsigned grid = (unsigned)cdiv(threads, 256);
-    if (bf16) pool_read_kernel<true><<<grid, 256, 0, s>>>(p, slots, threads, k_out, v_out);
-    else pool_read_kernel<false><<<grid, 256, 0, s>>>(p, slots, threads, k_out, v_out);
+    const uint32_t n = (uint32_t)n_tok * (uint32_t)p.H;
+    const dim3 grid((unsigned)cdiv((int64_t)n * 4, 256), 2);
+#define SPECTRA_CALL(G)                                                                         \
+    if (bf16) pool_read_kernel<G, true><<<grid, 256, 0, s>>>(p, slots, n, k_out, v_out);        \
+    else pool_read_kernel<G, false><<<grid, 256, 0, s>>>(p, slots, n, k_out, v_out)
+    SPECTRA_POOL_GROUPS(p.G, SPECTRA_CALL)
+#undef SPECTRA_CALL
     return cudaGetLastError() == cudaSuccess ? SPECTRA_OK : SPECTRA_ERR_CUDA;
 }
 
@@ -374,7 +527,7 @@ size_t evict_workspace_bytes(int n_seq, int n_heads, int64_t positions) {
 spectra_status launch_evict(const spectra_kv_pool &pool, const int32_t *pages, int max_pages,
                             const int32_t *lengths, int n_seq, const int32_t *dst_pages,
                             int dst_max_pages, int budget, int recent, int32_t *new_lengths, void *ws,
-                            cudaStream_t s) {
+                            cudaStream_t s, const DeviceInfo &dev) {
     EvictArgs a;
     a.p = PoolView::of(pool);
     a.pages = pages;
@@ -390,10 +543,26 @@ spectra_status launch_evict(const spectra_kv_pool &pool, const int32_t *pages, i
     a.before = static_cast<int2 *>(ws);
     a.thr = reinterpret_cast<uint32_t *>(a.before + bh * a.nch);
     a.ties = reinterpret_cast<int *>(a.thr + bh);
-    evict_select_kernel<<<dim3((unsigned)a.p.H, (unsigned)n_seq), kSelThreads, 0, s>>>(a);
+    const int64_t longest = (int64_t)max_pages << a.p.lp;
+    const size_t smem = (size_t)(longest < kKeys ? longest : kKeys) * 4;
+    static std::atomic<uint64_t> ready{0};
+    if (allow_smem((const void *)evict_select_kernel, kKeys * 4, dev, &ready) != cudaSuccess) return SPECTRA_ERR_CUDA;
+    evict_select_kernel<<<dim3((unsigned)a.p.H, (unsigned)n_seq), kSelThreads, smem, s>>>(a);
     if (cudaGetLastError() != cudaSuccess) return SPECTRA_ERR_CUDA;
-    evict_move_kernel<<<dim3((unsigned)a.nch, (unsigned)a.p.H, (unsigned)n_seq), kMoveChunk, 0, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? SPECTRA_OK : SPECTRA_ERR_CUDA;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.nch, (unsigned)a.p.H, (unsigned)n_seq);
+    cfg.blockDim = dim3(kMoveChunk, 1, 1);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cudaError_t err;
+#define SPECTRA_CALL(G) err = cudaLaunchKernelEx(&cfg, evict_move_kernel<G>, a)
+    SPECTRA_POOL_GROUPS(a.p.G, SPECTRA_CALL)
+#undef SPECTRA_CALL
+    return err == cudaSuccess ? SPECTRA_OK : SPECTRA_ERR_CUDA;
 }
 
 spectra_status pool_device_error(unsigned int *bits, cudaStream_t s) {

@@ -591,7 +591,8 @@ spectra_status launch_sample(const float *logits, int rows, int vocab, int64_t s
     int ranks = 1;
     while (ranks < 8 && (int64_t)rows * ranks * 2 <= dev.sm_count && vocab >= 2 * ranks * 4096) ranks *= 2;
     a.per_cta = (int)(cdiv(vocab, (int64_t)ranks * kSegment) * kSegment);
-    cudaError_t e = cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
+    static std::atomic<uint64_t> ready{0};
+    cudaError_t e = allow_smem((const void *)sample_kernel, (int)sizeof(Smem), dev, &ready);
     if (e != cudaSuccess) return SPECTRA_ERR_CUDA;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
