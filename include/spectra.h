@@ -662,7 +662,9 @@ typedef struct {
  * touch nothing: a page id outside the pool hides its positions, a length
  * outside [0, max_pages*page_size] counts as 0, and a sequence whose rows lie
  * outside [0, n_rows) or number more than max_q has its rows left as they
- * were.  Deterministic, asynchronous, allocates nothing, graph-capturable
+ * were.  Sequences may share pages.  Deterministic (but for the mass of an
+ * entry that several sequences of a call share, whose sums are added in any
+ * order), asynchronous, allocates nothing, graph-capturable
  * (lengths, pages and q_start are read on the device).  n_seq == 0 or n_rows
  * == 0 returns SPECTRA_OK without touching CUDA.
  * Errors: INVALID_ARG (update_mass without a mass buffer among them), SHAPE,

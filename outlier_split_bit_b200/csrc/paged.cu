@@ -216,16 +216,8 @@ __device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
 // unit_position(r): rows 2t, 2t+1, 2t+8, 2t+9 are t, t+4, t+8, t+12.
 __device__ __forceinline__ int unit_position(int r) { return (r & 8) | ((r & 1) << 2) | ((r & 7) >> 1); }
 
-// Where a unit's data is read from: the pool, or a stage in shared memory (read
-// once each: left to itself the compiler reads some of it again).
-struct Global {
-    const unsigned char *at;
-    __device__ __forceinline__ Global operator+(uint32_t bytes) const { return {at + bytes}; }
-    __device__ __forceinline__ uint4 get16() const { return *reinterpret_cast<const uint4 *>(at); }
-    __device__ __forceinline__ uint2 get8() const { return *reinterpret_cast<const uint2 *>(at); }
-    __device__ __forceinline__ uint32_t get4() const { return *reinterpret_cast<const uint32_t *>(at); }
-    __device__ __forceinline__ uint32_t get2() const { return *reinterpret_cast<const uint16_t *>(at); }
-};
+// A place in shared memory, read once: left to itself the compiler reads some
+// of a stage's data again.
 struct Shared {
     uint32_t at;
     __device__ __forceinline__ Shared operator+(uint32_t bytes) const { return {at + bytes}; }
@@ -286,14 +278,14 @@ __device__ __forceinline__ float half_of(uint32_t w, int which) {
 }
 
 // A unit's 16 slots lie together in each of the pool's six arrays; a warp
-// copies them into its stage in shared memory (16 bytes a lane and copy,
-// asynchronous), at these places.
-template <int G>
+// copies them (or K's three) into its stage in shared memory, 16 bytes a lane
+// and copy, asynchronously, at these places.
+template <int G, bool V>
 struct Stage {
     static constexpr int kCodes = 256 * G, kScales = 32 * G, kZeros = 64;  // bytes per unit
-    static constexpr int kc = 0, vc = kc + kCodes, ks = vc + kCodes, vs = ks + kScales, kz = vs + kScales,
-                         vz = kz + kZeros, kBytes = vz + kZeros;
-    static constexpr int kSmall = 4 * G + 8;  // 16-byte pieces of the scales and zero words
+    static constexpr int kc = 0, vc = kc + kCodes, ks = vc + (V ? kCodes : 0), vs = ks + kScales,
+                         kz = vs + (V ? kScales : 0), vz = kz + kZeros, kBytes = vz + (V ? kZeros : 0);
+    static constexpr int kSmall = (V ? 2 : 1) * (2 * G + 4);  // 16-byte pieces of the scales and zero words
     static constexpr int kPer = (kSmall + 31) / 32;
 };
 
@@ -302,9 +294,9 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
 }
 
 // What a lane copies of every unit.
-template <int G>
+template <int G, bool V>
 struct Copier {
-    using S = Stage<G>;
+    using S = Stage<G, V>;
     const char *kc, *vc, *small[S::kPer];
     uint32_t stride[S::kPer], to[S::kPer];
     __device__ __forceinline__ Copier(const PoolView &p, int lane) {
@@ -312,26 +304,29 @@ struct Copier {
         vc = reinterpret_cast<const char *>(p.vc) + 16 * lane;
 #pragma unroll
         for (int j = 0; j < S::kPer; ++j) {
-            int m = lane + 32 * j;
+            int m = min(lane + 32 * j, S::kSmall - 1);  // lanes past the last piece copy it again
+            const char *from;
+            uint32_t at;
             if (m < 2 * G) {
-                small[j] = reinterpret_cast<const char *>(p.ks);
+                from = reinterpret_cast<const char *>(p.ks);
                 stride[j] = S::kScales;
-                to[j] = S::ks + 16 * m;
-            } else if ((m -= 2 * G) < 2 * G) {
-                small[j] = reinterpret_cast<const char *>(p.vs);
+                at = S::ks;
+            } else if (V && (m -= 2 * G) < 2 * G) {
+                from = reinterpret_cast<const char *>(p.vs);
                 stride[j] = S::kScales;
-                to[j] = S::vs + 16 * m;
+                at = S::vs;
             } else if ((m -= 2 * G) < 4) {
-                small[j] = reinterpret_cast<const char *>(p.kz);
+                from = reinterpret_cast<const char *>(p.kz);
                 stride[j] = S::kZeros;
-                to[j] = S::kz + 16 * m;
+                at = S::kz;
             } else {
-                m = (m - 4) & 3;  // lanes past the last piece copy one of these again
-                small[j] = reinterpret_cast<const char *>(p.vz);
+                m -= 4;
+                from = reinterpret_cast<const char *>(p.vz);
                 stride[j] = S::kZeros;
-                to[j] = S::vz + 16 * m;
+                at = S::vz;
             }
-            small[j] += 16 * m;
+            small[j] = from + 16 * m;
+            to[j] = at + 16 * m;
         }
     }
     __device__ __forceinline__ void copy(uint32_t dst, uint32_t unit, int lane) const {
@@ -340,7 +335,7 @@ struct Copier {
         for (int c = 0; c < 16 * G; c += 32)
             if (c + 32 <= 16 * G || lane < 16 * G - c) {
                 copy16(dst + S::kc + 16 * (c + lane), k + 16 * c);
-                copy16(dst + S::vc + 16 * (c + lane), v + 16 * c);
+                if (V) copy16(dst + S::vc + 16 * (c + lane), v + 16 * c);
             }
 #pragma unroll
         for (int j = 0; j < S::kPer; ++j) copy16(dst + to[j], small[j] + (uint64_t)unit * stride[j]);
@@ -504,6 +499,63 @@ __device__ __forceinline__ uint32_t unit_of(const PoolView &p, int32_t page, int
     return (((uint32_t)page * (uint32_t)p.H + (uint32_t)h) << (p.lp - 4)) + ((uint32_t)(t0 & ((1 << p.lp) - 1)) >> 4);
 }
 
+constexpr int kStages = 3;
+
+// A warp's way through its units of one item: unit i is positions t0 + i *
+// kTile .. + 15.  Copies run kStages - 1 units ahead, a group each.  The
+// bookkeeping is done 32 units at a time: lane i finds unit f + i's place in
+// the pool; the top bit marks a unit whose scores need more than their factor
+// (hidden positions, a page outside the pool, a cap, a bias).
+template <int G, bool V>
+struct UnitRing {
+    using S = Stage<G, V>;
+    const PoolView &p;
+    const Copier<G, V> &copier;
+    const int32_t *pages;
+    uint32_t first;  // the ring's address
+    int h, t0, n_units, pos_lo, pos_hi, window, lane;
+    bool mark_all;
+    uint32_t units = 0, marks = 0, at = 0, done = 0;  // marks: bit i is that of the unit fetched i steps ago
+
+    __device__ __forceinline__ void look_up(int f) {
+        const int t = t0 + (f + lane) * kTile;
+        if (f + lane < n_units) {
+            units = unit_of(p, pages[t >> p.lp], t, h);
+            if (units == kNoUnit) units = kSpecial;  // unit 0 instead, hidden whole
+            if (mark_all || t + kUnit - 1 > pos_lo || (window > 0 && t <= pos_hi - window)) units |= kSpecial;
+        }
+    }
+    __device__ __forceinline__ void fetch(int f, uint32_t dst) {
+        uint32_t unit = 0;
+        if (f < n_units) {
+            if ((f & 31) == 0) look_up(f);
+            unit = __shfl_sync(0xffffffffu, units, f);
+            copier.copy(dst, unit & ~kSpecial, lane);
+        }
+        marks = __funnelshift_l(unit, marks, 1);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    __device__ __forceinline__ void start() {
+#pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) fetch(i, first + i * S::kBytes);
+        at = first;
+        done = first + (kStages - 1) * S::kBytes;
+    }
+    // Unit i's stage, once every lane's copies of it have landed.
+    __device__ __forceinline__ Shared next(int i) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        __syncwarp();  // and nobody reads the last unit's stage any more
+        fetch(i + kStages - 1, done);
+        done = at;
+        at = at == first + (kStages - 1) * S::kBytes ? first : at + S::kBytes;
+        return {done};
+    }
+    __device__ __forceinline__ bool marked() const { return marks & (1u << (kStages - 1)); }
+    __device__ __forceinline__ bool gone(int i) const {
+        return (uint32_t)pages[(t0 + i * kTile) >> p.lp] >= (uint32_t)p.n_pages;
+    }
+};
+
 // This CTA's run of the tile list and where it starts: sequence b, `off` tiles
 // into it.
 struct Run {
@@ -511,6 +563,12 @@ struct Run {
     int64_t off;
     int b, runs;
 };
+
+// a / b, with the short division where it will do.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if ((uint64_t)(a | b) >> 32 == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+    return a / b;
+}
 
 // per_seq(b): tiles of sequence b in the list.
 template <class F>
@@ -529,8 +587,8 @@ __device__ __forceinline__ Run find_run(const F &per_seq, int n_seq, int run, in
         r.b = 0;
         return r;
     }
-    r.cur = run * r.total / r.runs;
-    r.end = (run + 1) * r.total / r.runs;
+    r.cur = quotient(run * r.total, r.runs);
+    r.end = quotient((run + 1) * r.total, r.runs);
     if (before <= r.cur && r.cur < before + own) {
         for (int b = b0;; ++b) {
             const int64_t n = per_seq(b);
@@ -549,7 +607,9 @@ __device__ __forceinline__ Run find_run(const F &per_seq, int n_seq, int run, in
 }
 
 // The run that holds tile t of the list.
-__device__ __forceinline__ int run_of(int64_t t, const Run &r) { return (int)(((t + 1) * r.runs - 1) / r.total); }
+__device__ __forceinline__ int run_of(int64_t t, const Run &r) {
+    return (int)quotient((t + 1) * r.runs - 1, r.total);
+}
 
 // Four channels of an output row: the weighted sum over the sum of weights.
 template <bool EXACT>
@@ -570,12 +630,11 @@ constexpr int min_ctas() {
     return G * NT <= 4 ? 4 : (G * NT <= 8 ? 3 : 2);
 }
 
-constexpr int kStages = 3;
 // Shared memory: the warps' stages, which the exchange of the warps' sums
 // takes over at an item's end; then the queries' operands of several n-tiles.
 template <int G>
 constexpr int ring_bytes() {
-    constexpr int ring = kWarps * kStages * Stage<G>::kBytes, xch = kWarps * 8 * (32 * G + 4) * 4;
+    constexpr int ring = kWarps * kStages * Stage<G, true>::kBytes, xch = kWarps * 8 * (32 * G + 4) * 4;
     return ring > xch ? ring : xch;
 }
 
@@ -590,9 +649,9 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
     __shared__ int64_t s_part[33], s_found[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const PoolView &p = a.p;
-    const Copier<G> copier(p, lane);
+    const Copier<G, true> copier(p, lane);
     const LaneOffsets<G> lo(lane);
-    using S = Stage<G>;
+    using S = Stage<G, true>;
     const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(smem) + warp * kStages * S::kBytes;
     const Score score(a);
     const bool shaped = score.capped || a.slopes;  // scores are more than a multiple of the products
@@ -615,13 +674,21 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
             run.off = 0;
             continue;
         }
-        const int item = (int)(run.off / tiles.count);
+        const int item = (int)quotient(run.off, tiles.count);
         const int ta = (int)(run.off - (int64_t)item * tiles.count);
         const int tb = (int)min((int64_t)tiles.count, ta + (run.end - run.cur));
         const int h = item / n_ct, c0 = (item - h * n_ct) * C;
         const int cols = min(C, ncols - c0);
         const int pos_lo = s.n - s.m + c0 / a.grp, pos_hi = s.n - s.m + (c0 + cols - 1) / a.grp;
         const int vis_lo = a.window > 0 ? max(0, pos_lo - a.window + 1) : 0;  // the first position any column sees
+        // this warp's units: tiles first + ta .. first + tb - 1 that any column sees
+        const int32_t *pages = a.pages + (int64_t)b * a.max_pages;
+        const int u_end = min((tiles.first + tb) * kTile, min(s.n, pos_hi + 1));
+        int t0 = (tiles.first + ta) * kTile + warp * kUnit;
+        while (t0 + kUnit <= vis_lo) t0 += kTile;
+        const int n_units = t0 < u_end ? (u_end - t0 + kTile - 1) / kTile : 0;
+        UnitRing<G, true> ring{p, copier, pages, ring_at, h, t0, n_units, pos_lo, pos_hi, a.window, lane, shaped};
+        ring.start();  // the first units are on their way while the queries are prepared
         // queries: column g of every n-tile (zeros past the last column); mul
         // is what this lane's columns' products are multiplied with
         uint4 qf[G];
@@ -663,47 +730,8 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
                 for (int i = 0; i < 8; ++i) o[nt][gr][i >> 2][i & 3] = 0.f;
         }
 
-        // this warp's units: tiles first + ta .. first + tb - 1 that any column sees
-        const int32_t *pages = a.pages + (int64_t)b * a.max_pages;
-        const int u_end = min((tiles.first + tb) * kTile, min(s.n, pos_hi + 1));
-        int t0 = (tiles.first + ta) * kTile + warp * kUnit;
-        while (t0 + kUnit <= vis_lo) t0 += kTile;
-        const int n_units = t0 < u_end ? (u_end - t0 + kTile - 1) / kTile : 0;
-        // Bookkeeping 32 units at a time: lane i finds unit f + i's place in the
-        // pool; the top bit marks a unit whose scores need more than their
-        // factor (hidden positions, a page outside the pool, a cap, a bias).
-        uint32_t units = 0;
-        auto look_up = [&](int f) {
-            const int t = t0 + (f + lane) * kTile;
-            if (f + lane < n_units) {
-                units = unit_of(p, pages[t >> p.lp], t, h);
-                if (units == kNoUnit) units = kSpecial;  // unit 0 instead, hidden whole
-                if (shaped || t + kUnit - 1 > pos_lo || (a.window > 0 && t <= pos_hi - a.window)) units |= kSpecial;
-            }
-        };
-        // the ring: units kStages - 1 ahead, one group of copies each; marks: bit
-        // i is the mark of the unit fetched i steps ago
-        uint32_t marks = 0;
-        auto fetch = [&](int f, uint32_t dst) {
-            uint32_t unit = 0;
-            if (f < n_units) {
-                if ((f & 31) == 0) look_up(f);
-                unit = __shfl_sync(0xffffffffu, units, f);
-                copier.copy(dst, unit & ~kSpecial, lane);
-            }
-            marks = __funnelshift_l(unit, marks, 1);
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        };
-#pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) fetch(i, ring_at + i * S::kBytes);
-        uint32_t at = ring_at, done = ring_at + (kStages - 1) * S::kBytes;
         for (int i = 0; i < n_units; ++i) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-            __syncwarp();  // every lane's copies of this unit have landed, and nobody reads the last one's stage
-            fetch(i + kStages - 1, done);
-            const Shared here = {at};
-            done = at;
-            at = at == ring_at + (kStages - 1) * S::kBytes ? ring_at : at + S::kBytes;
+            const Shared here = ring.next(i);
             {
                 float x[NT][4];
                 KUnit<G> ku;
@@ -737,9 +765,9 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) x[nt][i] *= mul[nt][i & 1];
-                if (marks & (1u << (kStages - 1))) {
+                if (ring.marked()) {
                     const int t = t0 + i * kTile;
-                    const bool gone = (uint32_t)pages[t >> p.lp] >= (uint32_t)p.n_pages;
+                    const bool gone = ring.gone(i);
                     vu.cut_off(gone ? 0 : s.n - t, lane);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
@@ -975,22 +1003,28 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedArgs a)
 }
 
 // The accumulated weights, a second pass over K alone with the rows' lse: a
-// warp per unit, 8 columns at a time; a position belongs to one warp, so its
-// sum has one order and needs no atomics.
+// warp per unit, 8 columns at a time.  A position's sum over the columns is
+// formed in one warp, in order; it is added to the mass atomically, for the
+// pages that several sequences share.
 template <int G>
-__global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 2) paged_mass_kernel(const PagedArgs a) {
+__global__ void __launch_bounds__(kThreads, G <= 4 ? 5 : 3) paged_mass_kernel(const PagedArgs a) {
     constexpr int D = 32 * G;
+    extern __shared__ __align__(16) unsigned char smem[];
     __shared__ int64_t s_part[33], s_found[2];
+    using S = Stage<G, false>;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const PoolView &p = a.p;
+    const Copier<G, false> copier(p, lane);
     const LaneOffsets<G> lo(lane);
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(smem) + warp * kStages * S::kBytes;
     const Score score(a);
+    const bool shaped = score.capped || a.slopes;
     auto per_seq = [&](int b) -> int64_t {
         const Sequence s = sequence_of(a, b);
         return s.m == 0 || s.n == 0 ? 0 : (int64_t)p.H * tiles_of(a, s).count;
     };
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     Run run = find_run(per_seq, a.n_seq, blockIdx.x, gridDim.x, s_part, s_found);
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the rows' lse
     int b = run.b;
     while (run.cur < run.end) {
         const Sequence s = sequence_of(a, b);
@@ -1000,27 +1034,30 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 2) paged_mass_kernel(co
             run.off = 0;
             continue;
         }
-        const int h = (int)(run.off / tiles.count);
+        const int h = (int)quotient(run.off, tiles.count);
         const int ta = (int)(run.off - (int64_t)h * tiles.count);
         const int tb = (int)min((int64_t)tiles.count, ta + (run.end - run.cur));
         const int32_t *pages = a.pages + (int64_t)b * a.max_pages;
         const int ncols = s.m * a.grp;
         for (int c0 = 0; c0 < ncols; c0 += 8) {
             const int cols = min(8, ncols - c0);
-            int pos[2];
-            float slope[2], lse2[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int c = c0 + min(2 * t4 + e, cols - 1);
-                const int i = h * a.grp + c % a.grp;
-                pos[e] = s.n - s.m + c / a.grp;
-                slope[e] = a.slopes ? a.slopes[i] * kLog2e : 0.f;
-                // a column past the last, or one that saw nothing: weight 0
-                const float v = a.lse[(int64_t)(s.row0 + c / a.grp) * a.Hq + i] * kLog2e;
-                lse2[e] = 2 * t4 + e < cols && v > -INFINITY ? v : INFINITY;
-            }
             const int pos_lo = s.n - s.m + c0 / a.grp, pos_hi = s.n - s.m + (c0 + cols - 1) / a.grp;
             const int vis_lo = a.window > 0 ? max(0, pos_lo - a.window + 1) : 0;
+            const int u_end = min((tiles.first + tb) * kTile, min(s.n, pos_hi + 1));
+            int t0 = (tiles.first + ta) * kTile + warp * kUnit;
+            while (t0 + kUnit <= vis_lo) t0 += kTile;
+            const int n_units = t0 < u_end ? (u_end - t0 + kTile - 1) / kTile : 0;
+            UnitRing<G, false> ring{p, copier, pages, ring_at, h, t0, n_units, pos_lo, pos_hi, a.window, lane, shaped};
+            __syncwarp();  // every lane has read the ring's last unit of the columns before
+            ring.start();
+            float lse2[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                // a column past the last, or one that saw nothing: weight 0
+                const int c = c0 + min(2 * t4 + e, cols - 1);
+                const float v = a.lse[(int64_t)(s.row0 + c / a.grp) * a.Hq + h * a.grp + c % a.grp] * kLog2e;
+                lse2[e] = 2 * t4 + e < cols && v != -INFINITY ? v : INFINITY;
+            }
             uint4 qf[G];
             const int cg = c0 + g;
             float back, mul[2];
@@ -1028,19 +1065,11 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 2) paged_mass_kernel(co
                                        : nullptr, t4, qf, back);
 #pragma unroll
             for (int e = 0; e < 2; ++e) mul[e] = score.mul * __shfl_sync(0xffffffffu, back, 4 * (2 * t4 + e));
-            const int u_end = min((tiles.first + tb) * kTile, min(s.n, pos_hi + 1));
-            for (int t0 = (tiles.first + ta) * kTile + warp * kUnit; t0 < u_end; t0 += kTile) {
-                if (t0 + kUnit <= vis_lo) continue;
-                const uint32_t unit = unit_of(p, pages[t0 >> p.lp], t0, h);
-                if (unit == kNoUnit) continue;
+            for (int i = 0; i < n_units; ++i) {
+                const Shared here = ring.next(i);
+                const int t = t0 + i * kTile;
                 KUnit<G> ku;
-                ku.load(Global{reinterpret_cast<const unsigned char *>(p.kc) + (uint64_t)unit * Stage<G>::kCodes + lo.kc},
-                        Global{reinterpret_cast<const unsigned char *>(p.ks) + (uint64_t)unit * Stage<G>::kScales + lo.ks},
-                        Global{reinterpret_cast<const unsigned char *>(p.kz) + (uint64_t)unit * Stage<G>::kZeros + lo.kz});
-                float *mass = p.mass + (uint64_t)unit * kUnit;
-                float old[2];
-#pragma unroll
-                for (int r = 0; r < 2; ++r) old[r] = mass[unit_position(g + 8 * r)];
+                ku.load(here + S::kc + lo.kc, here + S::ks + lo.ks, here + S::kz + lo.kz);
                 float x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int gr = 0; gr < G; ++gr) {
@@ -1056,22 +1085,41 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 2) paged_mass_kernel(co
                     x[3] = fmaf(d[3], s1, x[3]);
                 }
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int u = unit_position(g + 8 * r), t = t0 + u;
-                    float w = 0.f;
+                for (int j = 0; j < 4; ++j) x[j] *= mul[j & 1];
+                bool skip = false;
+                if (ring.marked()) {
+                    skip = ring.gone(i);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int gap = pos[e] - t;
-                        float v = x[2 * r + e] * mul[e];
-                        if (score.capped) v = score.cap_of(v);
-                        if (a.slopes) v = fmaf(-slope[e], (float)gap, v);
-                        if (gap >= 0 && (a.window <= 0 || gap < a.window)) w += ex2(v - lse2[e]);
+                        const int c = c0 + min(2 * t4 + e, cols - 1);
+                        const float slope = a.slopes ? a.slopes[h * a.grp + c % a.grp] * kLog2e : 0.f;
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const int gap = s.n - s.m + c / a.grp - t - unit_position(g + 8 * r);
+                            float v = x[2 * r + e];
+                            if (score.capped) v = score.cap_of(v);
+                            if (a.slopes) v = fmaf(-slope, (float)gap, v);
+                            if (gap < 0 || (a.window > 0 && gap >= a.window)) v = -INFINITY;
+                            x[2 * r + e] = v;
+                        }
                     }
-                    w += __shfl_xor_sync(0xffffffffu, w, 1);
-                    w += __shfl_xor_sync(0xffffffffu, w, 2);
-                    if (t4 == 0 && t < s.n) mass[u] = old[r] + w;
+                }
+                float w[2];
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    w[r] = ex2(x[2 * r] - lse2[0]) + ex2(x[2 * r + 1] - lse2[1]);
+                    w[r] += __shfl_xor_sync(0xffffffffu, w[r], 1);
+                    w[r] += __shfl_xor_sync(0xffffffffu, w[r], 2);
+                }
+                // lanes t4 = 0 and 1 add the rows g and g + 8 (an entry past the
+                // sequence is left alone: its weight is 0, its mass may be anything)
+                const int u = unit_position(g) + 8 * t4;
+                if (t4 < 2 && t + u < s.n && !skip) {
+                    const uint32_t unit = unit_of(p, pages[t >> p.lp], t, h);
+                    atomicAdd(p.mass + (uint64_t)unit * kUnit + u, t4 ? w[1] : w[0]);
                 }
             }
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
         }
         run.cur += tb - ta;
         run.off += tb - ta;
@@ -1137,7 +1185,9 @@ cudaError_t run_attention(const PagedArgs &a, const DeviceInfo &dev, bool mass, 
     if (e != cudaSuccess) return e;
     e = launch(paged_join_kernel<G, NT, EXACT>, dim3(grid, (unsigned)(cols < C ? cols : C)), 0, true, s, a);
     if (e != cudaSuccess || !mass) return e;
-    return launch(paged_mass_kernel<G>, dim3(runs(heads, G <= 4 ? 4 : 2)), 0, true, s, a);
+    constexpr int mass_smem = kWarps * kStages * Stage<G, false>::kBytes;
+    static_assert(mass_smem <= 40 * 1024, "fits without asking for more");
+    return launch(paged_mass_kernel<G>, dim3(runs(heads, G <= 4 ? 5 : 3)), mass_smem, true, s, a);
 }
 
 template <int G, bool EXACT>
