@@ -541,18 +541,19 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _on(dev: torch.device, stream, call):
-    """call(stream handle) with dev as the current device, and with `stream`
-    (when one is given) as the stream that allocations belong to."""
-    if stream is None and torch.cuda.current_device() == dev.index:
-        return call(_raw_stream(dev.index))
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _elsewhere(dev: torch.device, stream, call, *args, **kwargs):
+    """call(*args, **kwargs) with dev as the current device and `stream` (when one
+    is given) as the current stream, which allocations then belong to."""
     with torch.cuda.device(dev):
         if stream is None:
-            return call(_raw_stream(dev.index))
+            return call(*args, **kwargs)
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(int(stream), device=dev)
         with torch.cuda.stream(stream):
-            return call(stream.cuda_stream)
+            return call(*args, **kwargs)
 
 
 class KVPool:
@@ -630,29 +631,30 @@ class KVPool:
         """Quantise k and v (BF16 [n_tok, n_heads, head_dim], the tokens any
         stride apart) into the token slots page * page_size + r (int32 [n_tok],
         distinct; negative: skipped)."""
+        if stream is not None or _current_device() != self.device.index:
+            return _elsewhere(self.device, stream, self.append, k, v, slots)
         n = k.shape[0]
         kp, ks = self._tokens(k, "k")
         vp, vs = self._tokens(v, "v")
         if v.shape[0] != n:
             raise ValueError("k and v hold different numbers of tokens")
         sp = _arg(slots, "slots", torch.int32, (n,), self.device)
-        _on(self.device, stream, lambda s: _check(
-            _lib.load().spectra_kv_pool_append(self._ref, kp, vp, n, ks, vs, sp, s), "spectra_kv_pool_append"))
+        _check(_lib.load().spectra_kv_pool_append(self._ref, kp, vp, n, ks, vs, sp, _raw_stream(self.device.index)),
+               "spectra_kv_pool_append")
 
     def read(self, slots: torch.Tensor, *, out_dtype=torch.bfloat16, stream=None):
         """K and V of the token slots (int32 [n]; negative: zeros), dequantised:
         two tensors [n, n_heads, head_dim]."""
+        dev = self.device
+        if stream is not None or _current_device() != dev.index:
+            return _elsewhere(dev, stream, self.read, slots, out_dtype=out_dtype)
         n = slots.shape[0]
-        sp = _arg(slots, "slots", torch.int32, (n,), self.device)
-
-        def call(s):
-            k = torch.empty((n, self.n_heads, self.head_dim), dtype=out_dtype, device=self.device)
-            v = torch.empty_like(k)
-            _check(_lib.load().spectra_kv_pool_read(self._ref, sp, n, k.data_ptr(), v.data_ptr(), _DT[out_dtype], s),
-                   "spectra_kv_pool_read")
-            return k, v
-
-        return _on(self.device, stream, call)
+        sp = _arg(slots, "slots", torch.int32, (n,), dev)
+        k = torch.empty(n, self.n_heads, self.head_dim, dtype=out_dtype, device=dev)
+        v = torch.empty_like(k)
+        _check(_lib.load().spectra_kv_pool_read(self._ref, sp, n, k.data_ptr(), v.data_ptr(), _DT[out_dtype],
+                                                _raw_stream(dev.index)), "spectra_kv_pool_read")
+        return k, v
 
 
 # A spectra_paged_query as bytes (native alignment, as the C struct).
@@ -678,13 +680,16 @@ def spectra_attention_paged(pool: KVPool, pages: torch.Tensor, lengths: torch.Te
     adds the weights to the pool's mass.  Rows outside every sequence are not
     written."""
     dev = pool.device
+    if stream is not None or _current_device() != dev.index:
+        return _elsewhere(dev, stream, spectra_attention_paged, pool, pages, lengths, q, q_start, max_q=max_q,
+                          scale=scale, softcap=softcap, slopes=slopes, window=window, out=out, out_dtype=out_dtype,
+                          want_lse=want_lse, update_mass=update_mass, workspace=workspace)
     n_seq, max_pages = pages.shape
     n_rows, hq, d = q.shape
     if d != pool.head_dim:
         raise ValueError(f"q has head_dim {d}, the pool {pool.head_dim}")
     if max_q is None:
         max_q = 1 if q_start is None else max(n_rows, 1)
-    heads = (n_rows, hq)
     shape = (n_rows, hq, d)
     at_pages = _arg(pages, "pages", torch.int32, (n_seq, max_pages), dev)
     at_lengths = _arg(lengths, "lengths", torch.int32, (n_seq,), dev)
@@ -692,32 +697,26 @@ def spectra_attention_paged(pool: KVPool, pages: torch.Tensor, lengths: torch.Te
     at_q = _arg(q, "q", torch.bfloat16, shape, dev)
     at_slopes = 0 if slopes is None else _arg(slopes, "slopes", torch.float32, (hq,), dev)
     if out is not None:
-        out_dtype = out.dtype
-        _arg(out, "out", out_dtype, shape, dev)
-
-    def call(s):
-        lib = _lib.load()
-        if out is not None:
-            o = out
-        elif out_dtype is torch.bfloat16:
-            o = torch.empty_like(q)
-        else:
-            o = torch.empty(shape, dtype=out_dtype, device=dev)
-        lse = torch.empty(heads, dtype=torch.float32, device=dev) if want_lse else None
-        ws = workspace
-        if ws is None:
-            need = pool._ws.get(heads)
-            if need is None:
-                need = pool._ws[heads] = lib.spectra_attention_paged_workspace_size(pool._ref, n_rows, hq)
-            ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        x = _PAGED_QUERY(at_pages, at_lengths, at_start, n_seq, max_pages, n_rows, max_q, hq, window,
-                         d ** -0.5 if scale is None else scale, softcap, at_q, at_slopes, o.data_ptr(),
-                         _DT[out_dtype], 1 if update_mass else 0, lse.data_ptr() if want_lse else 0)
-        _check(lib.spectra_attention_paged(pool._ref, x, ws.data_ptr(), ws.numel() * ws.element_size(), s),
-               "spectra_attention_paged")
-        return (o, lse) if want_lse else o
-
-    return _on(dev, stream, call)
+        _arg(out, "out", out.dtype, shape, dev)
+    elif out_dtype is torch.bfloat16:
+        out = torch.empty_like(q)
+    else:
+        out = torch.empty(n_rows, hq, d, dtype=out_dtype, device=dev)
+    lse = torch.empty(n_rows, hq, dtype=torch.float32, device=dev) if want_lse else None
+    lib = _lib.load()
+    if workspace is None:
+        need = pool._ws.get((n_rows, hq))
+        if need is None:
+            need = pool._ws[n_rows, hq] = lib.spectra_attention_paged_workspace_size(pool._ref, n_rows, hq)
+        workspace, room = torch.empty(need or 16, dtype=torch.uint8, device=dev), need
+    else:
+        room = workspace.numel() * workspace.element_size()
+    x = _PAGED_QUERY(at_pages, at_lengths, at_start, n_seq, max_pages, n_rows, max_q, hq, window,
+                     d ** -0.5 if scale is None else scale, softcap, at_q, at_slopes, out.data_ptr(),
+                     _DT[out.dtype], 1 if update_mass else 0, lse.data_ptr() if want_lse else 0)
+    _check(lib.spectra_attention_paged(pool._ref, x, workspace.data_ptr(), room, _raw_stream(dev.index)),
+           "spectra_attention_paged")
+    return (out, lse) if want_lse else out
 
 
 def spectra_kv_evict(pool: KVPool, pages: torch.Tensor, lengths: torch.Tensor, dst_pages: torch.Tensor,
@@ -728,24 +727,26 @@ def spectra_kv_evict(pool: KVPool, pages: torch.Tensor, lengths: torch.Tensor, d
     fresh pages dst_pages (int32 [n_seq, >= ceil(budget / page_size)]).
     Returns the new lengths (int32 [n_seq], which may not be `lengths`)."""
     dev = pool.device
+    if stream is not None or _current_device() != dev.index:
+        return _elsewhere(dev, stream, spectra_kv_evict, pool, pages, lengths, dst_pages, budget, recent, new_lengths,
+                          workspace=workspace)
     n_seq, max_pages = pages.shape
     dst_max = dst_pages.shape[1]
-    args = (_arg(pages, "pages", torch.int32, (n_seq, max_pages), dev), max_pages,
-            _arg(lengths, "lengths", torch.int32, (n_seq,), dev), n_seq,
-            _arg(dst_pages, "dst_pages", torch.int32, (n_seq, dst_max), dev), dst_max, budget, recent)
-
-    def call(s):
-        n, ws = new_lengths, workspace
-        if n is None:
-            n = torch.empty(n_seq, dtype=torch.int32, device=dev)
-        if ws is None:
-            need = _lib.load().spectra_kv_evict_workspace_size(pool._ref, n_seq, max_pages)
-            ws = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-        _check(_lib.load().spectra_kv_evict(pool._ref, *args, _arg(n, "new_lengths", torch.int32, (n_seq,), dev),
-                                   ws.data_ptr(), ws.numel() * ws.element_size(), s), "spectra_kv_evict")
-        return n
-
-    return _on(dev, stream, call)
+    at_pages = _arg(pages, "pages", torch.int32, (n_seq, max_pages), dev)
+    at_lengths = _arg(lengths, "lengths", torch.int32, (n_seq,), dev)
+    at_dst = _arg(dst_pages, "dst_pages", torch.int32, (n_seq, dst_max), dev)
+    lib = _lib.load()
+    if new_lengths is None:
+        new_lengths = torch.empty_like(lengths)
+    at_new = _arg(new_lengths, "new_lengths", torch.int32, (n_seq,), dev)
+    if workspace is None:
+        room = lib.spectra_kv_evict_workspace_size(pool._ref, n_seq, max_pages)
+        workspace = torch.empty(room or 16, dtype=torch.uint8, device=dev)
+    else:
+        room = workspace.numel() * workspace.element_size()
+    _check(lib.spectra_kv_evict(pool._ref, at_pages, max_pages, at_lengths, n_seq, at_dst, dst_max, budget, recent,
+                                at_new, workspace.data_ptr(), room, _raw_stream(dev.index)), "spectra_kv_evict")
+    return new_lengths
 
 
 # ---------------------------------------------------------------- token choice
@@ -757,24 +758,25 @@ def spectra_sample(logits: torch.Tensor, u: torch.Tensor, *, temperature: torch.
     apart, or [vocab]) with the uniform numbers u (float [rows]); temperature,
     top_p, min_p (float) and top_k (int32) are [rows] or None.  Returns (ids
     int32 [rows], log of the chosen tokens' probabilities float [rows])."""
+    dev = logits.device
     if logits.dim() == 1:
         logits = logits.unsqueeze(0)
     rows, vocab = logits.shape
-    dev = logits.device
     if logits.dtype is not torch.float32 or not logits.is_cuda or (rows > 0 and logits.stride(1) != 1):
         raise ValueError(f"logits: float32 rows on a CUDA device are wanted, got {logits.dtype} "
                          f"{list(logits.shape)} with strides {logits.stride()} on {dev}")
-    stride = logits.stride(0) if rows > 1 else vocab
-    f32 = torch.float32
-    args = (_arg(u, "u", f32, (rows,), dev), _opt(temperature, "temperature", f32, (rows,), dev),
-            _opt(top_k, "top_k", torch.int32, (rows,), dev), _opt(top_p, "top_p", f32, (rows,), dev),
-            _opt(min_p, "min_p", f32, (rows,), dev))
-
-    def call(s):
-        ids = torch.empty(rows, dtype=torch.int32, device=dev)
-        logp = torch.empty(rows, dtype=f32, device=dev)
-        _check(_lib.load().spectra_sample(logits.data_ptr(), rows, vocab, stride, *args, ids.data_ptr(), logp.data_ptr(),
-                                 s), "spectra_sample")
-        return ids, logp
-
-    return _on(dev, stream, call)
+    if stream is not None or _current_device() != dev.index:
+        return _elsewhere(dev, stream, spectra_sample, logits, u, temperature=temperature, top_k=top_k, top_p=top_p,
+                          min_p=min_p)
+    f32, one = torch.float32, (rows,)
+    at_u = _arg(u, "u", f32, one, dev)
+    at_t = None if temperature is None else _arg(temperature, "temperature", f32, one, dev)
+    at_k = None if top_k is None else _arg(top_k, "top_k", torch.int32, one, dev)
+    at_p = None if top_p is None else _arg(top_p, "top_p", f32, one, dev)
+    at_m = None if min_p is None else _arg(min_p, "min_p", f32, one, dev)
+    logp = torch.empty_like(u)
+    ids = torch.empty(rows, dtype=torch.int32, device=dev)
+    _check(_lib.load().spectra_sample(logits.data_ptr(), rows, vocab, logits.stride(0) if rows > 1 else vocab, at_u,
+                                      at_t, at_k, at_p, at_m, ids.data_ptr(), logp.data_ptr(),
+                                      _raw_stream(dev.index)), "spectra_sample")
+    return ids, logp
