@@ -23,14 +23,13 @@
 //     values under 2^-28 of the largest lose any).  The product sums are exact
 //     up to FP32 accumulation, and each group's is multiplied by its scale in
 //     FP32;
-//   weighted sum, BF16 output: A = 16 channels x 16 positions of V, dequantised
-//     to FP16 (c - z) * s with one rounding, B = the weights in FP16, scaled so
-//     that they lie under 2^15: both roundings are 2^-12 at most, a sixteenth
-//     of the output's own.  A V beyond FP16's range turns the output
-//     non-finite, which is reported;
-//   weighted sum, FP32 output: A = the exact BF16 integers c - z, B = weight
-//     times V's scale, one per position and group, in three BF16 pieces (24
-//     bits), each a product of its own.
+//   weighted sum: A = 16 channels x 16 positions of V, dequantised to FP16 (c -
+//     z) * s with one rounding, B = the weights in FP16, scaled so that they lie
+//     under 2^15.  For a BF16 output that is enough: both roundings are 2^-11 at
+//     most, an eighth of the output's own.  For an FP32 output what the two
+//     roundings left goes in as well, as two more products (V's remainder is
+//     exact; of the weights 2^-22 is lost).  A V beyond FP16's range turns the
+//     output non-finite, which is reported.
 // The scores' accumulator layout (positions in rows) is transposed into the
 // weights' operand layout inside the warp (movmatrix on the two halves of the
 // FP32 bits).  Which lane holds which channel or position is free as long as
@@ -63,9 +62,11 @@ __device__ unsigned int g_paged_error;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kUnit = 16;                // positions of a warp's step
-constexpr int kTile = kUnit * kWarps;    // positions of a CTA's step
-constexpr int kMaxCtas = 148 * 5;        // runs: one wave of the smallest variant's CTAs
-constexpr int kMinTiles = 2;             // tiles of a run, at least (fewer pieces to join)
+// Positions of a CTA's step (a tile of the list), U units per warp.
+template <int U>
+constexpr int kTile = kUnit * kWarps * U;
+constexpr int kMaxCtas = 148 * 4;        // runs, at most: a wave
+constexpr int kMinPositions = 128;       // of a run, at least (fewer pieces to join)
 constexpr float kRefBelow = 7.f;         // the reference lies 7 under the maximum (base 2) when it is set
 constexpr float kRefRoom = 15.f;         // and moves when a score is 15 over it
 constexpr float kLog2e = 1.4426950408889634f;
@@ -115,28 +116,21 @@ __device__ __forceinline__ Sequence sequence_of(const PagedArgs &a, int b) {
 struct Tiles {
     int first, count;
 };
+template <int U>
 __device__ __forceinline__ Tiles tiles_of(const PagedArgs &a, const Sequence &s) {
     const int64_t lo = a.window > 0 ? (int64_t)s.n - s.m - a.window + 1 : 0;
     Tiles t;
-    t.first = lo > 0 ? (int)(lo / kTile) : 0;
-    t.count = max(1, (s.n + kTile - 1) / kTile - t.first);
+    t.first = lo > 0 ? (int)(lo / kTile<U>) : 0;
+    t.count = max(1, (s.n + kTile<U> - 1) / kTile<U> - t.first);
     return t;
 }
 
-template <bool BF16>
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    if constexpr (BF16)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                     "{%0,%1,%2,%3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                     "{%0,%1,%2,%3};"
-                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// The same from zero (FP16).
+// The same from zero.
 __device__ __forceinline__ void mma_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
         : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
@@ -200,17 +194,6 @@ struct ZeroPair {
         x[3] = __hfma2(as_half2(masked_or<0x00F000F0u>(w8, 0x64006400u)), sixteenth, b);
     }
 };
-
-// Nibble j of both halfwords as the BF16 pair 128 + c, 128 + c'; and the
-// difference of two such pairs.
-__device__ __forceinline__ uint32_t code_pair(uint32_t w, int j) {
-    return masked_or<0x000F000Fu>(w >> (4 * j), 0x43004300u);
-}
-__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
-    const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&a),
-                                     *reinterpret_cast<const __nv_bfloat162 *>(&b));
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
 
 // Row r of a unit's 16 (as the tensor core counts them) is its position
 // unit_position(r): rows 2t, 2t+1, 2t+8, 2t+9 are t, t+4, t+8, t+12.
@@ -414,29 +397,33 @@ struct VUnit {
                 for (int k = 0; k < W; ++k) s[i][k] = 0u;
     }
     // The A operands of group gr, channels (4g, 4g + 1) and (4g + 2, 4g + 3):
-    // EXACT the BF16 integers c - z, otherwise the FP16 values (c - z) * s.
+    // (c - z) * s rounded to FP16, and (EXACT) in l0, l1 what that left, which is
+    // exact: the product has 15 bits at most and its last one is 2^-24 or more.
     template <bool EXACT>
-    __device__ __forceinline__ void operands(int gr, uint32_t (&a0)[4], uint32_t (&a1)[4]) const {
+    __device__ __forceinline__ void operands(int gr, uint32_t (&a0)[4], uint32_t (&a1)[4], uint32_t (&l0)[4],
+                                             uint32_t (&l1)[4]) const {
         const uint32_t pick = gr & 1 ? 0x7632u : 0x5410u;
-        uint32_t x[2][4];
+        uint32_t x[2][4], rest[2][4];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const uint32_t c = __byte_perm(w[2 * r][gr / 2], w[2 * r + 1][gr / 2], pick);
             const uint32_t zp = __byte_perm(z[2 * r], z[2 * r + 1], gr < 4 ? 0x5410u : 0x7632u);
-            if constexpr (EXACT) {
-                const uint32_t zz = code_pair(zp, gr & 3);
+            __half2 v[4];
+            ZeroPair(zp >> (gr & 2 ? 8 : 0), gr & 1).codes(c, v);
+            const __half2 sc = as_half2(__byte_perm(s[2 * r][gr / 2], s[2 * r + 1][gr / 2], pick));
 #pragma unroll
-                for (int j = 0; j < 4; ++j) x[r][j] = sub_bf16x2(code_pair(c, j), zz);
-            } else {
-                __half2 v[4];
-                ZeroPair(zp >> (gr & 2 ? 8 : 0), gr & 1).codes(c, v);
-                const __half2 sc = as_half2(__byte_perm(s[2 * r][gr / 2], s[2 * r + 1][gr / 2], pick));
-#pragma unroll
-                for (int j = 0; j < 4; ++j) x[r][j] = as_bits(__hmul2(v[j], sc));
+            for (int j = 0; j < 4; ++j) {
+                const __half2 y = __hmul2(v[j], sc);
+                x[r][j] = as_bits(y);
+                if constexpr (EXACT) rest[r][j] = as_bits(__hfma2(v[j], sc, __hneg2(y)));
             }
         }
         a0[0] = x[0][0]; a0[1] = x[0][1]; a0[2] = x[1][0]; a0[3] = x[1][1];
         a1[0] = x[0][2]; a1[1] = x[0][3]; a1[2] = x[1][2]; a1[3] = x[1][3];
+        if constexpr (EXACT) {
+            l0[0] = rest[0][0]; l0[1] = rest[0][1]; l0[2] = rest[1][0]; l0[3] = rest[1][1];
+            l1[0] = rest[0][2]; l1[1] = rest[0][3]; l1[2] = rest[1][2]; l1[3] = rest[1][3];
+        }
     }
 };
 
@@ -501,58 +488,69 @@ __device__ __forceinline__ uint32_t unit_of(const PoolView &p, int32_t page, int
 
 constexpr int kStages = 3;
 
-// A warp's way through its units of one item: unit i is positions t0 + i *
-// kTile .. + 15.  Copies run kStages - 1 units ahead, a group each.  The
-// bookkeeping is done 32 units at a time: lane i finds unit f + i's place in
-// the pool; the top bit marks a unit whose scores need more than their factor
-// (hidden positions, a page outside the pool, a cap, a bias).
-template <int G, bool V>
+// A warp's way through its units of one item, U at a step: unit j of step i is
+// the positions t0 + i * kTile<U> + 16 j .. + 15.  Copies run kStages - 1 steps
+// ahead, a group each.  The bookkeeping is done 32 units at a time: a lane finds
+// one unit's place in the pool; the top bit marks a unit whose scores need more
+// than their factor (hidden positions, a page outside the pool, a cap, a bias).
+template <int G, bool V, int U>
 struct UnitRing {
     using S = Stage<G, V>;
     const PoolView &p;
     const Copier<G, V> &copier;
     const int32_t *pages;
     uint32_t first;  // the ring's address
-    int h, t0, n_units, pos_lo, pos_hi, window, lane;
+    int h, t0, t_end, pos_lo, pos_hi, window, lane;
     bool mark_all;
-    uint32_t units = 0, marks = 0, at = 0, done = 0;  // marks: bit i is that of the unit fetched i steps ago
+    int steps;
+    uint32_t units = 0, marks = 0, at = 0, done = 0;  // marks: bit i is that of the unit fetched i ago
 
+    __device__ __forceinline__ int position(int f) const { return t0 + f / U * kTile<U> + f % U * kUnit; }
     __device__ __forceinline__ void look_up(int f) {
-        const int t = t0 + (f + lane) * kTile;
-        if (f + lane < n_units) {
-            units = unit_of(p, pages[t >> p.lp], t, h);
-            if (units == kNoUnit) units = kSpecial;  // unit 0 instead, hidden whole
-            if (mark_all || t + kUnit - 1 > pos_lo || (window > 0 && t <= pos_hi - window)) units |= kSpecial;
+        const int t = position(f + lane);
+        units = kSpecial;  // unit 0 in the place of one that is not there, hidden whole
+        if (t < t_end) {
+            const uint32_t unit = unit_of(p, pages[t >> p.lp], t, h);
+            if (unit != kNoUnit) {
+                units = unit;
+                if (mark_all || t + kUnit - 1 > pos_lo || (window > 0 && t <= pos_hi - window)) units |= kSpecial;
+            }
         }
     }
-    __device__ __forceinline__ void fetch(int f, uint32_t dst) {
-        uint32_t unit = 0;
-        if (f < n_units) {
-            if ((f & 31) == 0) look_up(f);
-            unit = __shfl_sync(0xffffffffu, units, f);
-            copier.copy(dst, unit & ~kSpecial, lane);
+    __device__ __forceinline__ void fetch(int step, uint32_t dst) {
+        if (step < steps) {
+            if ((step * U & 31) == 0) look_up(step * U);
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const uint32_t unit = __shfl_sync(0xffffffffu, units, step * U + j);
+                copier.copy(dst + j * S::kBytes, unit & ~kSpecial, lane);
+                marks = __funnelshift_l(unit, marks, 1);
+            }
+        } else {
+            marks <<= U;
         }
-        marks = __funnelshift_l(unit, marks, 1);
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
     __device__ __forceinline__ void start() {
+        steps = t0 < t_end ? (t_end - t0 + kTile<U> - 1) / kTile<U> : 0;
 #pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) fetch(i, first + i * S::kBytes);
+        for (int i = 0; i < kStages - 1; ++i) fetch(i, first + i * U * S::kBytes);
         at = first;
-        done = first + (kStages - 1) * S::kBytes;
+        done = first + (kStages - 1) * U * S::kBytes;
     }
-    // Unit i's stage, once every lane's copies of it have landed.
+    // Step i's stage, once every lane's copies of it have landed.
     __device__ __forceinline__ Shared next(int i) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-        __syncwarp();  // and nobody reads the last unit's stage any more
+        __syncwarp();  // and nobody reads the last step's stage any more
         fetch(i + kStages - 1, done);
         done = at;
-        at = at == first + (kStages - 1) * S::kBytes ? first : at + S::kBytes;
+        at = at == first + (kStages - 1) * U * S::kBytes ? first : at + U * S::kBytes;
         return {done};
     }
-    __device__ __forceinline__ bool marked() const { return marks & (1u << (kStages - 1)); }
-    __device__ __forceinline__ bool gone(int i) const {
-        return (uint32_t)pages[(t0 + i * kTile) >> p.lp] >= (uint32_t)p.n_pages;
+    __device__ __forceinline__ bool marked() const { return marks & (((1u << U) - 1) << ((kStages - 1) * U)); }
+    // Whether the unit at position t is not there.
+    __device__ __forceinline__ bool gone(int t) const {
+        return t >= t_end || (uint32_t)pages[t >> p.lp] >= (uint32_t)p.n_pages;
     }
 };
 
@@ -572,7 +570,7 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 
 // per_seq(b): tiles of sequence b in the list.
 template <class F>
-__device__ __forceinline__ Run find_run(const F &per_seq, int n_seq, int run, int max_runs, int64_t *part,
+__device__ __forceinline__ Run find_run(const F &per_seq, int n_seq, int run, int max_runs, int min_tiles, int64_t *part,
                                         int64_t *found) {
     const int tid = threadIdx.x, per = (n_seq + kThreads - 1) / kThreads;
     const int b0 = min(n_seq, tid * per), b1 = min(n_seq, b0 + per);
@@ -580,7 +578,7 @@ __device__ __forceinline__ Run find_run(const F &per_seq, int n_seq, int run, in
     for (int b = b0; b < b1; ++b) own += per_seq(b);
     Run r;
     int64_t before = block_exclusive(own, part, &r.total);
-    const int64_t want = (r.total + kMinTiles - 1) / kMinTiles;
+    const int64_t want = (r.total + min_tiles - 1) / min_tiles;
     r.runs = (int)(want < max_runs ? want : max_runs);
     if (run >= r.runs) {
         r.cur = r.end = r.off = 0;
@@ -621,38 +619,46 @@ __device__ __forceinline__ void store_out(const PagedArgs &a, int64_t at, float4
     } else {
         *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(a.out) + at) =
             make_uint2(bf16_pair(v.x, v.y), bf16_pair(v.z, v.w));
-        if (!(isfinite(v.x) && isfinite(v.y) && isfinite(v.z) && isfinite(v.w))) atomicOr(&g_paged_error, 2u);
     }
+    if (!(isfinite(v.x) && isfinite(v.y) && isfinite(v.z) && isfinite(v.w))) atomicOr(&g_paged_error, 2u);
 }
 
+// Units of a step: two where the accumulators leave the registers for it (the
+// loop's own work is done once for both, and their instructions interleave).
+template <int G, int NT>
+constexpr int units_per_step() {
+    return G * NT <= 4 ? 2 : 1;
+}
 template <int G, int NT>
 constexpr int min_ctas() {
-    return G * NT <= 4 ? 4 : (G * NT <= 8 ? 3 : 2);
+    return G * NT <= 8 ? 3 : 2;
 }
 
 // Shared memory: the warps' stages, which the exchange of the warps' sums
 // takes over at an item's end; then the queries' operands of several n-tiles.
-template <int G>
+template <int G, int U>
 constexpr int ring_bytes() {
-    constexpr int ring = kWarps * kStages * Stage<G, true>::kBytes, xch = kWarps * 8 * (32 * G + 4) * 4;
+    constexpr int ring = kWarps * kStages * U * Stage<G, true>::kBytes, xch = kWarps * 8 * (32 * G + 4) * 4;
     return ring > xch ? ring : xch;
 }
 
 template <int G, int NT, bool EXACT>
 __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_kernel(const PagedArgs a) {
+    constexpr int U = units_per_step<G, NT>();
     constexpr int D = 32 * G, C = 8 * NT, kRow = D + 4;  // kRow: a padded column of the exchange buffer
     extern __shared__ __align__(16) unsigned char smem[];
     float *xch = reinterpret_cast<float *>(smem);                      // [kWarps][8][kRow]
-    uint4 *qs = reinterpret_cast<uint4 *>(smem + ring_bytes<G>());     // NT > 1: [NT][G][32]
+    uint4 *qs = reinterpret_cast<uint4 *>(smem + ring_bytes<G, U>());  // NT > 1: [NT][G][32]
     __shared__ float2 s_ml[kWarps][C];
     __shared__ float s_back[C];
+    __shared__ float2 s_col[kWarps][C];  // a column's position and slope (each warp its own copy)
     __shared__ int64_t s_part[33], s_found[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     const PoolView &p = a.p;
     const Copier<G, true> copier(p, lane);
     const LaneOffsets<G> lo(lane);
     using S = Stage<G, true>;
-    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(smem) + warp * kStages * S::kBytes;
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(smem) + warp * kStages * U * S::kBytes;
     const Score score(a);
     const bool shaped = score.capped || a.slopes;  // scores are more than a multiple of the products
 
@@ -660,14 +666,14 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     auto per_seq = [&](int b) -> int64_t {
         const Sequence s = sequence_of(a, b);
-        return s.m == 0 ? 0 : (int64_t)p.H * ((s.m * a.grp + C - 1) / C) * tiles_of(a, s).count;
+        return s.m == 0 ? 0 : (int64_t)p.H * ((s.m * a.grp + C - 1) / C) * tiles_of<U>(a, s).count;
     };
-    Run run = find_run(per_seq, a.n_seq, blockIdx.x, gridDim.x, s_part, s_found);
+    Run run = find_run(per_seq, a.n_seq, blockIdx.x, gridDim.x, kMinPositions / kTile<U>, s_part, s_found);
     int4 cut = make_int4(-1, 0, 0, 0);
     int b = run.b;
     while (run.cur < run.end) {
         const Sequence s = sequence_of(a, b);
-        const Tiles tiles = tiles_of(a, s);
+        const Tiles tiles = tiles_of<U>(a, s);
         const int ncols = s.m * a.grp, n_ct = (ncols + C - 1) / C;
         if (s.m == 0 || run.off >= (int64_t)p.H * n_ct * tiles.count) {
             ++b;
@@ -683,12 +689,17 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
         const int vis_lo = a.window > 0 ? max(0, pos_lo - a.window + 1) : 0;  // the first position any column sees
         // this warp's units: tiles first + ta .. first + tb - 1 that any column sees
         const int32_t *pages = a.pages + (int64_t)b * a.max_pages;
-        const int u_end = min((tiles.first + tb) * kTile, min(s.n, pos_hi + 1));
-        int t0 = (tiles.first + ta) * kTile + warp * kUnit;
-        while (t0 + kUnit <= vis_lo) t0 += kTile;
-        const int n_units = t0 < u_end ? (u_end - t0 + kTile - 1) / kTile : 0;
-        UnitRing<G, true> ring{p, copier, pages, ring_at, h, t0, n_units, pos_lo, pos_hi, a.window, lane, shaped};
+        const int t_end = min((tiles.first + tb) * kTile<U>, min(s.n, pos_hi + 1));
+        int t0 = (tiles.first + ta) * kTile<U> + warp * (U * kUnit);
+        while (t0 + U * kUnit <= vis_lo) t0 += kTile<U>;
+        UnitRing<G, true, U> ring{p, copier, pages, ring_at, h, t0, t_end, pos_lo, pos_hi, a.window, lane, shaped};
         ring.start();  // the first units are on their way while the queries are prepared
+        if (lane < C) {
+            const int c = c0 + min(lane, cols - 1);
+            s_col[warp][lane] = make_float2(__int_as_float(s.n - s.m + c / a.grp),
+                                            a.slopes ? a.slopes[h * a.grp + c % a.grp] * kLog2e : 0.f);
+        }
+        __syncwarp();
         // queries: column g of every n-tile (zeros past the last column); mul
         // is what this lane's columns' products are multiplied with
         uint4 qf[G];
@@ -730,16 +741,18 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
                 for (int i = 0; i < 8; ++i) o[nt][gr][i >> 2][i & 3] = 0.f;
         }
 
-        for (int i = 0; i < n_units; ++i) {
+        for (int i = 0; i < ring.steps; ++i) {
             const Shared here = ring.next(i);
-            {
-                float x[NT][4];
+            float x[U][NT][4];
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const Shared at = here + j * S::kBytes;
                 KUnit<G> ku;
-                ku.load(here + S::kc + lo.kc, here + S::ks + lo.ks, here + S::kz + lo.kz);
+                ku.load(at + S::kc + lo.kc, at + S::ks + lo.ks, at + S::kz + lo.kz);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[nt][i] = 0.f;
+                    for (int e = 0; e < 4; ++e) x[j][nt][e] = 0.f;
 #pragma unroll
                 for (int gr = 0; gr < G; ++gr) {
                     uint32_t a0[4], a1[4];
@@ -752,130 +765,112 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
                         else q4 = qs[(nt * G + gr) * 32 + lane];
                         float d[4];
                         mma_first(d, a0, q4.x, q4.y);
-                        mma<false>(d, a1, q4.z, q4.w);
-                        x[nt][0] = fmaf(d[0], s0, x[nt][0]);
-                        x[nt][1] = fmaf(d[1], s0, x[nt][1]);
-                        x[nt][2] = fmaf(d[2], s1, x[nt][2]);
-                        x[nt][3] = fmaf(d[3], s1, x[nt][3]);
+                        mma(d, a1, q4.z, q4.w);
+                        x[j][nt][0] = fmaf(d[0], s0, x[j][nt][0]);
+                        x[j][nt][1] = fmaf(d[1], s0, x[j][nt][1]);
+                        x[j][nt][2] = fmaf(d[2], s1, x[j][nt][2]);
+                        x[j][nt][3] = fmaf(d[3], s1, x[j][nt][3]);
                     }
                 }
-                VUnit<G> vu;
-                vu.load(here + S::vc + lo.vc, here + S::vs + lo.vs, here + S::vz + lo.vz);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[nt][i] *= mul[nt][i & 1];
-                if (ring.marked()) {
-                    const int t = t0 + i * kTile;
-                    const bool gone = ring.gone(i);
-                    vu.cut_off(gone ? 0 : s.n - t, lane);
+                    for (int e = 0; e < 4; ++e) x[j][nt][e] *= mul[nt][e & 1];
+            }
+            const bool marked = ring.marked();
+            if (marked) {
+#pragma unroll
+                for (int j = 0; j < U; ++j) {
+                    const int t = t0 + i * kTile<U> + j * kUnit;
+                    const bool gone = ring.gone(t);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const int c = c0 + min(8 * nt + 2 * t4 + e, cols - 1);
-                            const float slope = a.slopes ? a.slopes[h * a.grp + c % a.grp] * kLog2e : 0.f;
+                            const float2 col = s_col[warp][8 * nt + 2 * t4 + e];
 #pragma unroll
                             for (int r = 0; r < 2; ++r) {
-                                const int gap = s.n - s.m + c / a.grp - t - unit_position(g + 8 * r);
-                                float v = x[nt][2 * r + e];
+                                const int gap = __float_as_int(col.x) - t - unit_position(g) - 8 * r;
+                                float v = x[j][nt][2 * r + e];
                                 if (score.capped) v = score.cap_of(v);
-                                if (a.slopes) v = fmaf(-slope, (float)gap, v);
+                                v = fmaf(-col.y, (float)gap, v);
                                 if (gone || gap < 0 || (a.window > 0 && gap >= a.window)) v = -INFINITY;
-                                x[nt][2 * r + e] = v;
+                                x[j][nt][2 * r + e] = v;
                             }
                         }
                 }
-                bool up = false;
+            }
+            bool up = false;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) up |= fmaxf(x[nt][e], x[nt][2 + e]) > limit[nt][e];
-                if (__any_sync(0xffffffffu, up)) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float m = fmaxf(x[nt][e], x[nt][2 + e]);
-#pragma unroll
-                            for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-                            // a column that saw nothing yet keeps its zeros
-                            const bool first = limit[nt][e] == -INFINITY;
-                            const float to = m == -INFINITY ? ref[nt][e]
-                                                            : (first ? m - kRefBelow : fmaxf(m - kRefBelow, ref[nt][e]));
-                            const float f = first ? 1.f : ex2(ref[nt][e] - to);
-                            if (m > -INFINITY) limit[nt][e] = to + kRefRoom;
-                            ref[nt][e] = to;
-                            sum[nt][e] *= f;
-#pragma unroll
-                            for (int gr = 0; gr < G; ++gr) {
-                                o[nt][gr][0][e] *= f;
-                                o[nt][gr][0][2 + e] *= f;
-                                o[nt][gr][1][e] *= f;
-                                o[nt][gr][1][2 + e] *= f;
-                            }
-                        }
+                for (int e = 0; e < 2; ++e) {
+                    float m = fmaxf(x[0][nt][e], x[0][nt][2 + e]);
+                    if (U > 1) m = fmaxf(m, fmaxf(x[U - 1][nt][e], x[U - 1][nt][2 + e]));
+                    up |= m > limit[nt][e];
                 }
+            if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        x[nt][i] = ex2(x[nt][i] - ref[nt][i & 1]);
-                        sum[nt][i & 1] += x[nt][i];
-                    }
-                if constexpr (EXACT) {
-                    // weights, transposed: f[nt][i] is column 8 nt + g at position t4 + 4 i
-                    float f[NT][4];
+                    for (int e = 0; e < 2; ++e) {
+                        float m = fmaxf(x[0][nt][e], x[0][nt][2 + e]);
+                        if (U > 1) m = fmaxf(m, fmaxf(x[U - 1][nt][e], x[U - 1][nt][2 + e]));
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                        for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+                        // a column that saw nothing yet keeps its zeros
+                        const bool first = limit[nt][e] == -INFINITY;
+                        const float to = m == -INFINITY ? ref[nt][e]
+                                                        : (first ? m - kRefBelow : fmaxf(m - kRefBelow, ref[nt][e]));
+                        const float f = first ? 1.f : ex2(ref[nt][e] - to);
+                        if (m > -INFINITY) limit[nt][e] = to + kRefRoom;
+                        ref[nt][e] = to;
+                        sum[nt][e] *= f;
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const uint32_t u0 = __float_as_uint(x[nt][2 * r]), u1 = __float_as_uint(x[nt][2 * r + 1]);
-                            const uint32_t hi = transpose8x8(__byte_perm(u0, u1, 0x7632));
-                            const uint32_t lo = transpose8x8(__byte_perm(u0, u1, 0x5410));
-                            f[nt][2 * r] = __uint_as_float(__byte_perm(lo, hi, 0x5410));
-                            f[nt][2 * r + 1] = __uint_as_float(__byte_perm(lo, hi, 0x7632));
-                        }
-#pragma unroll
-                    for (int gr = 0; gr < G; ++gr) {
-                        uint32_t a0[4], a1[4];
-                        vu.template operands<true>(gr, a0, a1);
-                        float s4[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) s4[i] = half_of(vu.s[i][gr / 2], gr & 1);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            float rest[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) rest[i] = f[nt][i] * s4[i];
-#pragma unroll
-                            for (int piece = 0; piece < 3; ++piece) {
-                                uint32_t b[2];
-#pragma unroll
-                                for (int r = 0; r < 2; ++r) {
-                                    b[r] = bf16_pair(rest[2 * r], rest[2 * r + 1]);
-                                    rest[2 * r] -= __uint_as_float(b[r] << 16);
-                                    rest[2 * r + 1] -= __uint_as_float(b[r] & 0xFFFF0000u);
-                                }
-                                mma<true>(o[nt][gr][0], a0, b[0], b[1]);
-                                mma<true>(o[nt][gr][1], a1, b[0], b[1]);
-                            }
+                        for (int gr = 0; gr < G; ++gr) {
+                            o[nt][gr][0][e] *= f;
+                            o[nt][gr][0][2 + e] *= f;
+                            o[nt][gr][1][e] *= f;
+                            o[nt][gr][1][2 + e] *= f;
                         }
                     }
-                } else {
-                    uint32_t b[NT][2];
+            }
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+            for (int j = 0; j < U; ++j) {
+                const Shared at = here + j * S::kBytes;
+                VUnit<G> vu;
+                vu.load(at + S::vc + lo.vc, at + S::vs + lo.vs, at + S::vz + lo.vz);
+                if (marked) {
+                    const int t = t0 + i * kTile<U> + j * kUnit;
+                    vu.cut_off(ring.gone(t) ? 0 : s.n - t, lane);
+                }
+                // the weights as B operands: b, and (EXACT) what its rounding left
+                uint32_t b[NT][2], rest[NT][2];
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) b[nt][r] = transpose8x8(f16_pair(x[nt][2 * r], x[nt][2 * r + 1]));
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int gr = 0; gr < G; ++gr) {
-                        uint32_t a0[4], a1[4];
-                        vu.template operands<false>(gr, a0, a1);
+                    for (int r = 0; r < 2; ++r) {
+                        const float w0 = ex2(x[j][nt][2 * r] - ref[nt][0]), w1 = ex2(x[j][nt][2 * r + 1] - ref[nt][1]);
+                        sum[nt][0] += w0;
+                        sum[nt][1] += w1;
+                        const uint32_t h2 = f16_pair(w0, w1);
+                        b[nt][r] = transpose8x8(h2);
+                        if constexpr (EXACT)
+                            rest[nt][r] = transpose8x8(f16_pair(w0 - half_of(h2, 0), w1 - half_of(h2, 1)));
+                    }
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            mma<false>(o[nt][gr][0], a0, b[nt][0], b[nt][1]);
-                            mma<false>(o[nt][gr][1], a1, b[nt][0], b[nt][1]);
+                for (int gr = 0; gr < G; ++gr) {
+                    uint32_t a0[4], a1[4], l0[4], l1[4];
+                    vu.template operands<EXACT>(gr, a0, a1, l0, l1);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        mma(o[nt][gr][0], a0, b[nt][0], b[nt][1]);
+                        mma(o[nt][gr][1], a1, b[nt][0], b[nt][1]);
+                        if constexpr (EXACT) {
+                            mma(o[nt][gr][0], a0, rest[nt][0], rest[nt][1]);
+                            mma(o[nt][gr][1], a1, rest[nt][0], rest[nt][1]);
+                            mma(o[nt][gr][0], l0, b[nt][0], b[nt][1]);
+                            mma(o[nt][gr][1], l1, b[nt][0], b[nt][1]);
                         }
                     }
                 }
@@ -1007,8 +1002,8 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedArgs a)
 // formed in one warp, in order; it is added to the mass atomically, for the
 // pages that several sequences share.
 template <int G>
-__global__ void __launch_bounds__(kThreads, G <= 4 ? 5 : 3) paged_mass_kernel(const PagedArgs a) {
-    constexpr int D = 32 * G;
+__global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 3) paged_mass_kernel(const PagedArgs a) {
+    constexpr int D = 32 * G, U = units_per_step<G, 1>();
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ int64_t s_part[33], s_found[2];
     using S = Stage<G, false>;
@@ -1016,19 +1011,19 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 5 : 3) paged_mass_kernel(co
     const PoolView &p = a.p;
     const Copier<G, false> copier(p, lane);
     const LaneOffsets<G> lo(lane);
-    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(smem) + warp * kStages * S::kBytes;
+    const uint32_t ring_at = (uint32_t)__cvta_generic_to_shared(smem) + warp * kStages * U * S::kBytes;
     const Score score(a);
     const bool shaped = score.capped || a.slopes;
     auto per_seq = [&](int b) -> int64_t {
         const Sequence s = sequence_of(a, b);
-        return s.m == 0 || s.n == 0 ? 0 : (int64_t)p.H * tiles_of(a, s).count;
+        return s.m == 0 || s.n == 0 ? 0 : (int64_t)p.H * tiles_of<U>(a, s).count;
     };
-    Run run = find_run(per_seq, a.n_seq, blockIdx.x, gridDim.x, s_part, s_found);
+    Run run = find_run(per_seq, a.n_seq, blockIdx.x, gridDim.x, kMinPositions / kTile<U>, s_part, s_found);
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the rows' lse
     int b = run.b;
     while (run.cur < run.end) {
         const Sequence s = sequence_of(a, b);
-        const Tiles tiles = tiles_of(a, s);
+        const Tiles tiles = tiles_of<U>(a, s);
         if (s.m == 0 || s.n == 0 || run.off >= (int64_t)p.H * tiles.count) {
             ++b;
             run.off = 0;
@@ -1043,11 +1038,10 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 5 : 3) paged_mass_kernel(co
             const int cols = min(8, ncols - c0);
             const int pos_lo = s.n - s.m + c0 / a.grp, pos_hi = s.n - s.m + (c0 + cols - 1) / a.grp;
             const int vis_lo = a.window > 0 ? max(0, pos_lo - a.window + 1) : 0;
-            const int u_end = min((tiles.first + tb) * kTile, min(s.n, pos_hi + 1));
-            int t0 = (tiles.first + ta) * kTile + warp * kUnit;
-            while (t0 + kUnit <= vis_lo) t0 += kTile;
-            const int n_units = t0 < u_end ? (u_end - t0 + kTile - 1) / kTile : 0;
-            UnitRing<G, false> ring{p, copier, pages, ring_at, h, t0, n_units, pos_lo, pos_hi, a.window, lane, shaped};
+            const int t_end = min((tiles.first + tb) * kTile<U>, min(s.n, pos_hi + 1));
+            int t0 = (tiles.first + ta) * kTile<U> + warp * (U * kUnit);
+            while (t0 + U * kUnit <= vis_lo) t0 += kTile<U>;
+            UnitRing<G, false, U> ring{p, copier, pages, ring_at, h, t0, t_end, pos_lo, pos_hi, a.window, lane, shaped};
             __syncwarp();  // every lane has read the ring's last unit of the columns before
             ring.start();
             float lse2[2];
@@ -1065,58 +1059,63 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 5 : 3) paged_mass_kernel(co
                                        : nullptr, t4, qf, back);
 #pragma unroll
             for (int e = 0; e < 2; ++e) mul[e] = score.mul * __shfl_sync(0xffffffffu, back, 4 * (2 * t4 + e));
-            for (int i = 0; i < n_units; ++i) {
+            for (int i = 0; i < ring.steps; ++i) {
                 const Shared here = ring.next(i);
-                const int t = t0 + i * kTile;
-                KUnit<G> ku;
-                ku.load(here + S::kc + lo.kc, here + S::ks + lo.ks, here + S::kz + lo.kz);
-                float x[4] = {0.f, 0.f, 0.f, 0.f};
+                const bool marked = ring.marked();
 #pragma unroll
-                for (int gr = 0; gr < G; ++gr) {
-                    uint32_t a0[4], a1[4];
-                    ku.operands(gr, a0, a1);
-                    const float s0 = half_of(ku.s[0][gr / 2], gr & 1), s1 = half_of(ku.s[1][gr / 2], gr & 1);
-                    float d[4];
-                    mma_first(d, a0, qf[gr].x, qf[gr].y);
-                    mma<false>(d, a1, qf[gr].z, qf[gr].w);
-                    x[0] = fmaf(d[0], s0, x[0]);
-                    x[1] = fmaf(d[1], s0, x[1]);
-                    x[2] = fmaf(d[2], s1, x[2]);
-                    x[3] = fmaf(d[3], s1, x[3]);
-                }
+                for (int j = 0; j < U; ++j) {
+                    const Shared at = here + j * S::kBytes;
+                    const int t = t0 + i * kTile<U> + j * kUnit;
+                    KUnit<G> ku;
+                    ku.load(at + S::kc + lo.kc, at + S::ks + lo.ks, at + S::kz + lo.kz);
+                    float x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] *= mul[j & 1];
-                bool skip = false;
-                if (ring.marked()) {
-                    skip = ring.gone(i);
+                    for (int gr = 0; gr < G; ++gr) {
+                        uint32_t a0[4], a1[4];
+                        ku.operands(gr, a0, a1);
+                        const float s0 = half_of(ku.s[0][gr / 2], gr & 1), s1 = half_of(ku.s[1][gr / 2], gr & 1);
+                        float d[4];
+                        mma_first(d, a0, qf[gr].x, qf[gr].y);
+                        mma(d, a1, qf[gr].z, qf[gr].w);
+                        x[0] = fmaf(d[0], s0, x[0]);
+                        x[1] = fmaf(d[1], s0, x[1]);
+                        x[2] = fmaf(d[2], s1, x[2]);
+                        x[3] = fmaf(d[3], s1, x[3]);
+                    }
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int c = c0 + min(2 * t4 + e, cols - 1);
-                        const float slope = a.slopes ? a.slopes[h * a.grp + c % a.grp] * kLog2e : 0.f;
+                    for (int e = 0; e < 4; ++e) x[e] *= mul[e & 1];
+                    bool gone = false;
+                    if (marked) {
+                        gone = ring.gone(t);
 #pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            const int gap = s.n - s.m + c / a.grp - t - unit_position(g + 8 * r);
-                            float v = x[2 * r + e];
-                            if (score.capped) v = score.cap_of(v);
-                            if (a.slopes) v = fmaf(-slope, (float)gap, v);
-                            if (gap < 0 || (a.window > 0 && gap >= a.window)) v = -INFINITY;
-                            x[2 * r + e] = v;
+                        for (int e = 0; e < 2; ++e) {
+                            const int c = c0 + min(2 * t4 + e, cols - 1);
+                            const float slope = a.slopes ? a.slopes[h * a.grp + c % a.grp] * kLog2e : 0.f;
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                const int gap = s.n - s.m + c / a.grp - t - unit_position(g) - 8 * r;
+                                float v = x[2 * r + e];
+                                if (score.capped) v = score.cap_of(v);
+                                if (a.slopes) v = fmaf(-slope, (float)gap, v);
+                                if (gap < 0 || (a.window > 0 && gap >= a.window)) v = -INFINITY;
+                                x[2 * r + e] = v;
+                            }
                         }
                     }
-                }
-                float w[2];
+                    float w[2];
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    w[r] = ex2(x[2 * r] - lse2[0]) + ex2(x[2 * r + 1] - lse2[1]);
-                    w[r] += __shfl_xor_sync(0xffffffffu, w[r], 1);
-                    w[r] += __shfl_xor_sync(0xffffffffu, w[r], 2);
-                }
-                // lanes t4 = 0 and 1 add the rows g and g + 8 (an entry past the
-                // sequence is left alone: its weight is 0, its mass may be anything)
-                const int u = unit_position(g) + 8 * t4;
-                if (t4 < 2 && t + u < s.n && !skip) {
-                    const uint32_t unit = unit_of(p, pages[t >> p.lp], t, h);
-                    atomicAdd(p.mass + (uint64_t)unit * kUnit + u, t4 ? w[1] : w[0]);
+                    for (int r = 0; r < 2; ++r) {
+                        w[r] = ex2(x[2 * r] - lse2[0]) + ex2(x[2 * r + 1] - lse2[1]);
+                        w[r] += __shfl_xor_sync(0xffffffffu, w[r], 1);
+                        w[r] += __shfl_xor_sync(0xffffffffu, w[r], 2);
+                    }
+                    // lanes t4 = 0 and 1 add the rows g and g + 8 (an entry past the
+                    // sequence is left alone: its weight is 0, its mass may be anything)
+                    const int u = unit_position(g) + 8 * t4;
+                    if (t4 < 2 && t + u < s.n && !gone) {
+                        const uint32_t unit = unit_of(p, pages[t >> p.lp], t, h);
+                        atomicAdd(p.mass + (uint64_t)unit * kUnit + u, t4 ? w[1] : w[0]);
+                    }
                 }
             }
             asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -1166,28 +1165,27 @@ cudaError_t launch(void (*kernel)(A...), dim3 grid, size_t smem, bool dependent,
 template <int G, int NT, bool EXACT>
 cudaError_t run_attention(const PagedArgs &a, const DeviceInfo &dev, bool mass, cudaStream_t s) {
     constexpr int C = 8 * NT;
-    const size_t smem = ring_bytes<G>() + (NT > 1 ? NT * G * 512 : 0);
+    const size_t smem = ring_bytes<G, units_per_step<G, NT>()>() + (NT > 1 ? NT * G * 512 : 0);
     static std::atomic<uint64_t> ready{0};
     cudaError_t e = allow_smem((const void *)paged_attention_kernel<G, NT, EXACT>, (int)smem, dev, &ready);
     if (e != cudaSuccess) return e;
     // runs: one wave, and no more than the tables' width allows tiles for
     const int64_t cols = (int64_t)a.max_q * a.grp, n_ct = (cols + C - 1) / C;
-    const int64_t tiles = (((int64_t)a.max_pages << a.p.lp) + kTile - 1) / kTile;
-    const int64_t heads = (int64_t)a.n_seq * a.p.H;
-    auto runs = [&](int64_t items, int per_sm) {
+    const int64_t positions = (int64_t)a.max_pages << a.p.lp, heads = (int64_t)a.n_seq * a.p.H;
+    auto runs = [&](int64_t items, int per_sm, int U) {
         const int64_t most = (int64_t)dev.sm_count * per_sm < kMaxCtas ? (int64_t)dev.sm_count * per_sm : kMaxCtas;
-        if (items >= most * kMinTiles || tiles >= most * kMinTiles) return (unsigned)most;
-        const int64_t want = (items * tiles + kMinTiles - 1) / kMinTiles;
-        return (unsigned)(want < most ? want : most);
+        const int64_t each = cdiv(cdiv(positions, kUnit * kWarps * U) * kUnit * kWarps * U, kMinPositions);
+        if (items >= most || each >= most) return (unsigned)most;
+        return (unsigned)(items * each < most ? items * each : most);
     };
-    const unsigned grid = runs(heads * n_ct, min_ctas<G, NT>());
+    const unsigned grid = runs(heads * n_ct, min_ctas<G, NT>(), units_per_step<G, NT>());
     e = launch(paged_attention_kernel<G, NT, EXACT>, dim3(grid), smem, false, s, a);
     if (e != cudaSuccess) return e;
     e = launch(paged_join_kernel<G, NT, EXACT>, dim3(grid, (unsigned)(cols < C ? cols : C)), 0, true, s, a);
     if (e != cudaSuccess || !mass) return e;
-    constexpr int mass_smem = kWarps * kStages * Stage<G, false>::kBytes;
-    static_assert(mass_smem <= 40 * 1024, "fits without asking for more");
-    return launch(paged_mass_kernel<G>, dim3(runs(heads, G <= 4 ? 5 : 3)), mass_smem, true, s, a);
+    constexpr int mass_smem = kWarps * kStages * units_per_step<G, 1>() * Stage<G, false>::kBytes;
+    static_assert(mass_smem <= 46 * 1024, "fits without asking for more");
+    return launch(paged_mass_kernel<G>, dim3(runs(heads, G <= 4 ? 4 : 3, units_per_step<G, 1>())), mass_smem, true, s, a);
 }
 
 template <int G, bool EXACT>

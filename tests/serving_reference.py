@@ -86,14 +86,17 @@ def attention(pool, pages, lengths, q, q_start, scale, softcap=0.0, slopes=None,
     are `ds`.  Weights then lie within a factor exp(2 ds) of the true ones
     (their own rounding: 2^-20).  Their sum, T positive FP32 terms in any order,
     is off by (T - 1) * 2^-24 of itself, and so are the weights, and lse by as
-    much.  The weights are multiplied by V's scales and
-    enter the tensor core as BF16 pieces, 2^-16 of them lost at most, and the
+    much.  V's values and the weights enter the tensor core in two FP16
+    pieces each: V's are exact, of a weight 2^-22 is lost, and so is the product
+    of the two second pieces, 2^-22 too; 2^-16 covers these.  A weight under
+    FP16's normal range (2^-14, where the largest one is 2^7 or more) is off by
+    half of the last place there, 2^-25, which is 2^-32 of the largest weight and
+    so of the sum; this counts where all larger weights meet a zero value.  The
     sum of T positions costs (T/16 + 64) roundings of 2^-23.
 
-    `half` (BF16 output): V's values are rounded to FP16 (half a step: 2^-11 of
-    each; a value under FP16's normal range has a subnormal scale and is
-    exact), and so are the weights, 2^-11 of each down to 2^-14 and 2^-25 below,
-    where the largest weight is 2^7 or more: 2^-32 of the sum."""
+    `half` (BF16 output): one piece each.  V's values are rounded to FP16 (half a
+    step: 2^-11 of each; a value under FP16's normal range has a subnormal scale
+    and is exact), and so are the weights, 2^-11 of each."""
     rows, Hq, D = q.shape
     grp = Hq // pool.H
     out = np.zeros((rows, Hq, D))
@@ -141,9 +144,9 @@ def attention(pool, pages, lengths, q, q_start, scale, softcap=0.0, slopes=None,
                     sums = seen.sum() * 2.0 ** -24
                     f = np.expm1(2 * ds) + 2.0 ** -20 + sums
                     tol_o[r0 + j, i] = (f + 2.0 ** -16 + (seen.sum() / 16 + 64) * 2.0 ** -23) * (p @ np.abs(v)) + 1e-30
+                    tol_o[r0 + j, i] += 2.0 ** -32 * np.abs(v[seen]).sum(0)
                     if half:
                         tol_o[r0 + j, i] += (2.0 ** -10 + 2.0 ** -22) * (p @ np.abs(v))
-                        tol_o[r0 + j, i] += 2.0 ** -32 * np.abs(v[seen]).sum(0)
                     tol_l[r0 + j, i] = ds + sums + 2.0 ** -20 + 2.0 ** -22 * abs(lse[r0 + j, i])
                     tol_m[at] += (f + 2.0 ** -20) * p + 1e-37
     return out, lse, add, tol_o, tol_l, tol_m
