@@ -67,8 +67,12 @@ template <int U>
 constexpr int kTile = kUnit * kWarps * U;
 constexpr int kMaxCtas = 148 * 4;        // runs, at most: a wave
 constexpr int kMinPositions = 128;       // of a run, at least (fewer pieces to join)
-constexpr float kRefBelow = 7.f;         // the reference lies 7 under the maximum (base 2) when it is set
-constexpr float kRefRoom = 15.f;         // and moves when a score is 15 over it
+// The reference lies kRefBelow under the maximum (base 2) when it is set, and
+// moves when a score is kRefRoom over it.  The second values are for weights
+// that are multiplied with V's scales: a weight of 1 at most times any FP16
+// number is one again.
+constexpr float kRefBelow = 7.f, kRefBelowLow = -8.f;
+constexpr float kRefRoom = 15.f, kRefRoomLow = 0.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -167,6 +171,19 @@ __device__ __forceinline__ uint32_t masked_or(uint32_t w, uint32_t magic) {
     asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(w), "n"(MASK), "r"(magic));
     return y;
 }
+
+// The codes of word w as they stand: nibble j of both halfwords is the FP16
+// subnormal c * 2^-24 (j = 0, 2) or 16 c * 2^-24 (j = 1, 3).  Products and sums
+// with them are as exact as with any other number; what is multiplied with the
+// odd ones is divided by 16, and 2^24 and the zero point are seen to later.
+__device__ __forceinline__ void raw_codes(uint32_t w, uint32_t (&x)[4]) {
+    const uint32_t w8 = w >> 8;
+    x[0] = w & 0x000F000Fu;
+    x[1] = w & 0x00F000F0u;
+    x[2] = w8 & 0x000F000Fu;
+    x[3] = w8 & 0x00F000F0u;
+}
+constexpr float kRaw = 16777216.f;  // 2^24
 
 // A group's zero points of two rows (or one, twice), as the FP16 pairs that
 // take 1024 + c and (1024 + 16c) / 16 to c - z.  zp: the rows' zero halfwords
@@ -358,7 +375,20 @@ struct KUnit {
             z[r] = (kz + r * 8 * 4).get4();
         }
     }
-    // The A operands of group gr, k-steps 0 and 1.
+    // The A operands of group gr from the codes as they stand, k-steps 0 and 1;
+    // and row r's zero points of groups gr (even) and gr + 1, z * 2^-24 and
+    // 16 z * 2^-24.
+    __device__ __forceinline__ void raw_operands(int gr, uint32_t (&a0)[4], uint32_t (&a1)[4]) const {
+        uint32_t x[2][4];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) raw_codes(w[r][gr], x[r]);
+        a0[0] = x[0][0]; a0[1] = x[1][0]; a0[2] = x[0][1]; a0[3] = x[1][1];
+        a1[0] = x[0][2]; a1[1] = x[1][2]; a1[2] = x[0][3]; a1[3] = x[1][3];
+    }
+    __device__ __forceinline__ uint32_t raw_zeros(int r, int gr) const {
+        return (__byte_perm(z[r], 0, gr < 4 ? 0x1010 : 0x3232) >> (gr & 2 ? 8 : 0)) & 0x00F0000Fu;
+    }
+    // The A operands of group gr less the zero points, k-steps 0 and 1.
     __device__ __forceinline__ void operands(int gr, uint32_t (&a0)[4], uint32_t (&a1)[4]) const {
         __half2 x[2][4];
 #pragma unroll
@@ -396,6 +426,25 @@ struct VUnit {
 #pragma unroll
                 for (int k = 0; k < W; ++k) s[i][k] = 0u;
     }
+    // The A operands of group gr from the codes as they stand, channels (4g, 4g +
+    // 1) and (4g + 2, 4g + 3); and minus the zero points in the same form (the
+    // same for both).
+    __device__ __forceinline__ void raw_operands(int gr, uint32_t (&a0)[4], uint32_t (&a1)[4], uint32_t (&az)[4]) const {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            uint32_t x[4];
+            raw_codes(__byte_perm(w[2 * r][gr / 2], w[2 * r + 1][gr / 2], gr & 1 ? 0x7632u : 0x5410u), x);
+            a0[2 * r] = x[0]; a0[2 * r + 1] = x[1];
+            a1[2 * r] = x[2]; a1[2 * r + 1] = x[3];
+            const uint32_t zp = __byte_perm(z[2 * r], z[2 * r + 1], gr < 4 ? 0x5410u : 0x7632u) >> (gr & 2 ? 8 : 0);
+            az[2 * r] = masked_or<0x000F000Fu>(gr & 1 ? zp >> 4 : zp, 0x80008000u);
+            az[2 * r + 1] = masked_or<0x00F000F0u>(gr & 1 ? zp : zp << 4, 0x80008000u);
+        }
+    }
+    // The scales of group gr at two of the lane's four positions.
+    __device__ __forceinline__ __half2 scale_pair(int gr, int r) const {
+        return as_half2(__byte_perm(s[2 * r][gr / 2], s[2 * r + 1][gr / 2], gr & 1 ? 0x7632u : 0x5410u));
+    }
     // The A operands of group gr, channels (4g, 4g + 1) and (4g + 2, 4g + 3):
     // (c - z) * s rounded to FP16, and (EXACT) in l0, l1 what that left, which is
     // exact: the product has 15 bits at most and its last one is 2^-24 or more.
@@ -432,8 +481,12 @@ struct VUnit {
 // the order in which ZeroPair::codes takes a word's nibbles.  `back` undoes the
 // row's power of two.  Rows lie on groups of 4 lanes; all lanes of the warp call
 // it (q is null for a column without a query).
-template <int G>
-__device__ __forceinline__ void query_operands(const uint16_t *q, int t, uint4 (&f)[G], float &back) {
+// RAW, for codes as they stand: q1, q3, q5, q7 divided by 16; and in `zero` minus
+// the group's sum of the query, as the zero points' form wants it (an odd
+// group's divided by 16).
+template <int G, bool RAW>
+__device__ __forceinline__ void query_operands(const uint16_t *q, int t, uint4 (&f)[G], float &back,
+                                               float (&zero)[RAW ? G : 1]) {
     uint32_t top = 0;
 #pragma unroll
     for (int gr = 0; gr < G; ++gr) {
@@ -456,7 +509,17 @@ __device__ __forceinline__ void query_operands(const uint16_t *q, int t, uint4 (
             v[2 * i] = __uint_as_float(w[i] << 16) * up;
             v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u) * up;
         }
-        f[gr] = make_uint4(f16_pair(v[0], v[4]), f16_pair(v[1], v[5]), f16_pair(v[2], v[6]), f16_pair(v[3], v[7]));
+        constexpr float odd = RAW ? 0.0625f : 1.f;
+        f[gr] = make_uint4(f16_pair(v[0], v[4]), f16_pair(v[1] * odd, v[5] * odd), f16_pair(v[2], v[6]),
+                           f16_pair(v[3] * odd, v[7] * odd));
+        if constexpr (RAW) {
+            const float even = half_of(f[gr].x, 0) + half_of(f[gr].x, 1) + half_of(f[gr].z, 0) + half_of(f[gr].z, 1);
+            const float odds = half_of(f[gr].y, 0) + half_of(f[gr].y, 1) + half_of(f[gr].w, 0) + half_of(f[gr].w, 1);
+            float sum = -fmaf(16.f, odds, even);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            zero[gr] = gr & 1 ? sum * 0.0625f : sum;
+        }
     }
 }
 
@@ -645,6 +708,9 @@ constexpr int ring_bytes() {
 template <int G, int NT, bool EXACT>
 __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_kernel(const PagedArgs a) {
     constexpr int U = units_per_step<G, NT>();
+    // codes as they stand: of K, and of V (whose zero points take a product of
+    // their own, dearer for many columns than subtracting them once)
+    constexpr bool kRawK = NT == 1, kRawV = NT == 1 && !EXACT;
     constexpr int D = 32 * G, C = 8 * NT, kRow = D + 4;  // kRow: a padded column of the exchange buffer
     extern __shared__ __align__(16) unsigned char smem[];
     float *xch = reinterpret_cast<float *>(smem);                      // [kWarps][8][kRow]
@@ -692,8 +758,16 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
         const int t_end = min((tiles.first + tb) * kTile<U>, min(s.n, pos_hi + 1));
         int t0 = (tiles.first + ta) * kTile<U> + warp * (U * kUnit);
         while (t0 + U * kUnit <= vis_lo) t0 += kTile<U>;
+        uint4 qf[G];
+        float mul[NT][2], qz[kRawK ? G : 1][2];
+        float ref[NT][2], limit[NT][2], sum[NT][2], o[NT][G][2][4];
+        // Once; again, with lower weights, where a weight times V's scale passed
+        // FP16's range (a scale over 2: values of 30 and more).
+#pragma unroll 1
+        for (int low = 0;; ++low) {
         UnitRing<G, true, U> ring{p, copier, pages, ring_at, h, t0, t_end, pos_lo, pos_hi, a.window, lane, shaped};
         ring.start();  // the first units are on their way while the queries are prepared
+        if (low == 0) {
         if (lane < C) {
             const int c = c0 + min(lane, cols - 1);
             s_col[warp][lane] = make_float2(__int_as_float(s.n - s.m + c / a.grp),
@@ -702,22 +776,24 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
         __syncwarp();
         // queries: column g of every n-tile (zeros past the last column); mul
         // is what this lane's columns' products are multiplied with
-        uint4 qf[G];
-        float mul[NT][2];
         auto query_row = [&](int nt) -> const uint16_t * {
             const int c = c0 + 8 * nt + g;
             return 8 * nt + g < cols
                        ? a.q + ((int64_t)(s.row0 + c / a.grp) * a.Hq + h * a.grp + c % a.grp) * D : nullptr;
         };
         if constexpr (NT == 1) {
-            float back;
-            query_operands<G>(query_row(0), t4, qf, back);
+            float back, zero[G];
+            query_operands<G, true>(query_row(0), t4, qf, back, zero);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) mul[0][e] = score.mul * __shfl_sync(0xffffffffu, back, 4 * (2 * t4 + e));
+            for (int e = 0; e < 2; ++e) {
+                mul[0][e] = score.mul * __shfl_sync(0xffffffffu, back, 4 * (2 * t4 + e));
+#pragma unroll
+                for (int gr = 0; gr < G; ++gr) qz[gr][e] = __shfl_sync(0xffffffffu, zero[gr], 4 * (2 * t4 + e));
+            }
         } else {
             for (int nt = warp; nt < NT; nt += kWarps) {
-                float back;
-                query_operands<G>(query_row(nt), t4, qf, back);
+                float back, none[1];
+                query_operands<G, false>(query_row(nt), t4, qf, back, none);
 #pragma unroll
                 for (int gr = 0; gr < G; ++gr) qs[(nt * G + gr) * 32 + lane] = qf[gr];
                 if (t4 == 0) s_back[8 * nt + g] = back;
@@ -728,8 +804,8 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
 #pragma unroll
                 for (int e = 0; e < 2; ++e) mul[nt][e] = score.mul * s_back[8 * nt + 2 * t4 + e];
         }
+        }
         // ref: what weights are relative to; limit: the score that moves it
-        float ref[NT][2], limit[NT][2], sum[NT][2], o[NT][G][2][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             ref[nt][0] = ref[nt][1] = 0.f;
@@ -756,7 +832,8 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
 #pragma unroll
                 for (int gr = 0; gr < G; ++gr) {
                     uint32_t a0[4], a1[4];
-                    ku.operands(gr, a0, a1);
+                    if constexpr (kRawK) ku.raw_operands(gr, a0, a1);
+                    else ku.operands(gr, a0, a1);
                     const float s0 = half_of(ku.s[0][gr / 2], gr & 1), s1 = half_of(ku.s[1][gr / 2], gr & 1);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
@@ -766,6 +843,13 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
                         float d[4];
                         mma_first(d, a0, q4.x, q4.y);
                         mma(d, a1, q4.z, q4.w);
+                        if constexpr (kRawK) {
+                            const float z0 = half_of(ku.raw_zeros(0, gr), gr & 1), z1 = half_of(ku.raw_zeros(1, gr), gr & 1);
+                            d[0] = fmaf(z0, qz[gr][0], d[0]);
+                            d[1] = fmaf(z0, qz[gr][1], d[1]);
+                            d[2] = fmaf(z1, qz[gr][0], d[2]);
+                            d[3] = fmaf(z1, qz[gr][1], d[3]);
+                        }
                         x[j][nt][0] = fmaf(d[0], s0, x[j][nt][0]);
                         x[j][nt][1] = fmaf(d[1], s0, x[j][nt][1]);
                         x[j][nt][2] = fmaf(d[2], s1, x[j][nt][2]);
@@ -775,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[j][nt][e] *= mul[nt][e & 1];
+                    for (int e = 0; e < 4; ++e) x[j][nt][e] = (kRawK ? x[j][nt][e] * kRaw : x[j][nt][e]) * mul[nt][e & 1];
             }
             const bool marked = ring.marked();
             if (marked) {
@@ -820,10 +904,10 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
                         for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
                         // a column that saw nothing yet keeps its zeros
                         const bool first = limit[nt][e] == -INFINITY;
-                        const float to = m == -INFINITY ? ref[nt][e]
-                                                        : (first ? m - kRefBelow : fmaxf(m - kRefBelow, ref[nt][e]));
+                        const float under = m - (low ? kRefBelowLow : kRefBelow);
+                        const float to = m == -INFINITY ? ref[nt][e] : (first ? under : fmaxf(under, ref[nt][e]));
                         const float f = first ? 1.f : ex2(ref[nt][e] - to);
-                        if (m > -INFINITY) limit[nt][e] = to + kRefRoom;
+                        if (m > -INFINITY) limit[nt][e] = to + (low ? kRefRoomLow : kRefRoom);
                         ref[nt][e] = to;
                         sum[nt][e] *= f;
 #pragma unroll
@@ -861,6 +945,16 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
 #pragma unroll
                 for (int gr = 0; gr < G; ++gr) {
                     uint32_t a0[4], a1[4], l0[4], l1[4];
+                    if constexpr (kRawV) {
+                        vu.raw_operands(gr, a0, a1, l0);
+                        const uint32_t b0 = as_bits(__hmul2(as_half2(b[0][0]), vu.scale_pair(gr, 0)));
+                        const uint32_t b1 = as_bits(__hmul2(as_half2(b[0][1]), vu.scale_pair(gr, 1)));
+                        mma(o[0][gr][0], a0, b0, b1);
+                        mma(o[0][gr][1], a1, b0, b1);
+                        mma(o[0][gr][0], l0, b0, b1);
+                        mma(o[0][gr][1], l0, b0, b1);
+                        continue;
+                    }
                     vu.template operands<EXACT>(gr, a0, a1, l0, l1);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
@@ -876,8 +970,22 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
                 }
             }
         }
-        // the exchange buffer takes the ring's place
         asm volatile("cp.async.wait_group 0;" ::: "memory");
+        if constexpr (kRawV) {
+            float odd = 0.f;  // NaN if a sum is not finite
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) odd = fmaf(o[0][gr][e >> 2][e & 3], 0.f, odd);
+            if (low == 0 && __any_sync(0xffffffffu, odd != 0.f)) continue;
+#pragma unroll
+            for (int gr = 0; gr < G; ++gr)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[0][gr][e >> 2][e & 3] *= e & 2 ? kRaw * 0.0625f : kRaw;  // rows g + 8: odd codes
+        }
+        break;
+        }
+        // the exchange buffer takes the ring's place
         __syncthreads();
 
         // join the four warps; a whole item is written out, a piece of one kept
@@ -1054,11 +1162,15 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 3) paged_mass_kernel(co
             }
             uint4 qf[G];
             const int cg = c0 + g;
-            float back, mul[2];
-            query_operands<G>(g < cols ? a.q + ((int64_t)(s.row0 + cg / a.grp) * a.Hq + h * a.grp + cg % a.grp) * D
-                                       : nullptr, t4, qf, back);
+            float back, mul[2], zero[G], qz[G][2];
+            query_operands<G, true>(g < cols ? a.q + ((int64_t)(s.row0 + cg / a.grp) * a.Hq + h * a.grp + cg % a.grp) * D
+                                       : nullptr, t4, qf, back, zero);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) mul[e] = score.mul * __shfl_sync(0xffffffffu, back, 4 * (2 * t4 + e));
+            for (int e = 0; e < 2; ++e) {
+                mul[e] = score.mul * __shfl_sync(0xffffffffu, back, 4 * (2 * t4 + e));
+#pragma unroll
+                for (int gr = 0; gr < G; ++gr) qz[gr][e] = __shfl_sync(0xffffffffu, zero[gr], 4 * (2 * t4 + e));
+            }
             for (int i = 0; i < ring.steps; ++i) {
                 const Shared here = ring.next(i);
                 const bool marked = ring.marked();
@@ -1072,18 +1184,23 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 3) paged_mass_kernel(co
 #pragma unroll
                     for (int gr = 0; gr < G; ++gr) {
                         uint32_t a0[4], a1[4];
-                        ku.operands(gr, a0, a1);
+                        ku.raw_operands(gr, a0, a1);
                         const float s0 = half_of(ku.s[0][gr / 2], gr & 1), s1 = half_of(ku.s[1][gr / 2], gr & 1);
+                        const float z0 = half_of(ku.raw_zeros(0, gr), gr & 1), z1 = half_of(ku.raw_zeros(1, gr), gr & 1);
                         float d[4];
                         mma_first(d, a0, qf[gr].x, qf[gr].y);
                         mma(d, a1, qf[gr].z, qf[gr].w);
+                        d[0] = fmaf(z0, qz[gr][0], d[0]);
+                        d[1] = fmaf(z0, qz[gr][1], d[1]);
+                        d[2] = fmaf(z1, qz[gr][0], d[2]);
+                        d[3] = fmaf(z1, qz[gr][1], d[3]);
                         x[0] = fmaf(d[0], s0, x[0]);
                         x[1] = fmaf(d[1], s0, x[1]);
                         x[2] = fmaf(d[2], s1, x[2]);
                         x[3] = fmaf(d[3], s1, x[3]);
                     }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[e] *= mul[e & 1];
+                    for (int e = 0; e < 4; ++e) x[e] = x[e] * kRaw * mul[e & 1];
                     bool gone = false;
                     if (marked) {
                         gone = ring.gone(t);

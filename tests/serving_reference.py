@@ -94,9 +94,13 @@ def attention(pool, pages, lengths, q, q_start, scale, softcap=0.0, slopes=None,
     so of the sum; this counts where all larger weights meet a zero value.  The
     sum of T positions costs (T/16 + 64) roundings of 2^-23.
 
-    `half` (BF16 output): one piece each.  V's values are rounded to FP16 (half a
-    step: 2^-11 of each; a value under FP16's normal range has a subnormal scale
-    and is exact), and so are the weights, 2^-11 of each."""
+    `half` (BF16 output): one piece each, with two FP16 roundings: of the weight
+    and of V's value, or of the weight and of its product with V's scale, which
+    is then multiplied with the exact c - z.  Half a step each, 2^-11.  (A value
+    under the normal range has a subnormal scale and is exact.)  A product under
+    the normal range is off by 2^-25, where the largest weight is 2^7 or more,
+    or 2^-8 or more with scales over 1.9 (a product over FP16's range would
+    show): 2^-32 or 2^-17 of the sum, times |c - z| <= 15."""
     rows, Hq, D = q.shape
     grp = Hq // pool.H
     out = np.zeros((rows, Hq, D))
@@ -147,6 +151,8 @@ def attention(pool, pages, lengths, q, q_start, scale, softcap=0.0, slopes=None,
                     tol_o[r0 + j, i] += 2.0 ** -32 * np.abs(v[seen]).sum(0)
                     if half:
                         tol_o[r0 + j, i] += (2.0 ** -10 + 2.0 ** -22) * (p @ np.abs(v))
+                        steep = pool.scales["v"][at].view(np.float16).max() > 1.9
+                        tol_o[r0 + j, i] += 15 * seen.sum() * 2.0 ** (-17 if steep else -32)
                     tol_l[r0 + j, i] = ds + sums + 2.0 ** -20 + 2.0 ** -22 * abs(lse[r0 + j, i])
                     tol_m[at] += (f + 2.0 ** -20) * p + 1e-37
     return out, lse, add, tol_o, tol_l, tol_m

@@ -262,10 +262,47 @@ def test_chunks(Hq, H, D, P, lengths, m, out_dtype):
 
 
 @pytest.mark.parametrize("value_scale,q_scale", [(1e-6, 1.0), (3e3, 1e-3), (1.0, 30.0), (100.0, 100.0)])
-def test_magnitudes(value_scale, q_scale):
+@pytest.mark.parametrize("Hq,out_dtype", [(4, torch.float32), (4, torch.bfloat16), (12, torch.bfloat16)],
+                         ids=["fp32", "bf16", "bf16-wide"])
+def test_magnitudes(value_scale, q_scale, Hq, out_dtype):
     """Subnormal FP16 scales, large values, scores far apart."""
-    check_attention(np.random.default_rng(9), [77, 300], [1, 4], 4, 2, 64, 16, out_dtype=torch.float32,
+    check_attention(np.random.default_rng(9), [77, 300], [1, 4], Hq, 2, 64, 16, out_dtype=out_dtype,
                     value_scale=value_scale, q_scale=q_scale)
+
+
+def test_queries_of_every_magnitude():
+    """Rows from subnormal to huge, zeros, and elements 2^40 apart in one row."""
+    rng = np.random.default_rng(19)
+    p, pages, _ = filled(rng, [90], 1, 128, 16)
+    g = device_pool(p)
+    x = rng.standard_normal((8, 1, 128)) * np.exp2(np.array([-130, -60, -20, 0, 20, 60, 100, 0]))[:, None, None]
+    x[7] *= np.exp2(rng.integers(-40, 1, (1, 128)))
+    q = torch.from_numpy(x).to(torch.bfloat16)
+    q[3, 0, ::2] = 0.0
+    scale = 2.0 ** -60
+    for r in range(8):
+        big = float(q[r].abs().max())
+        k = float(np.float32(0.1 / big)) if big > 0 and 0.1 / big < 1e38 else scale
+        out, lse = sp.spectra_attention_paged(g, i32(pages), i32([90]), q[r:r + 1].to(DEV), scale=k, want_lse=True,
+                                              out_dtype=torch.float32)
+        want, wl_, _, to, tl, _ = ref.attention(p, pages, [90], q[r:r + 1].double().numpy(), [0, 1], k)
+        assert (np.abs(out.double().cpu().numpy() - want) <= to + 2.0 ** -23 * np.abs(want)).all(), r
+        assert (np.abs(lse.double().cpu().numpy() - wl_) <= tl).all(), r
+    sp.spectra_device_status()
+
+
+def test_values_past_fp16_are_reported():
+    """An FP32 output of V's entries over 65504 is refused after the fact."""
+    g = sp.KVPool(1, 64, 16, 1)
+    x = torch.full((3, 1, 64), 3e5, device=DEV).bfloat16()
+    x[:, :, ::2] = -3e5
+    g.append(x, x, i32([0, 1, 2]))
+    q = torch.zeros((1, 2, 64), device=DEV).bfloat16()
+    sp.spectra_device_status()
+    sp.spectra_attention_paged(g, i32([[0]]), i32([3]), q, out_dtype=torch.float32)
+    with pytest.raises(sp.SpectraError) as e:
+        sp.spectra_device_status()
+    assert e.value.status == 5
 
 
 def test_many_sequences_ragged():
