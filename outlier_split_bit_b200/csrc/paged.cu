@@ -115,8 +115,13 @@ __device__ __forceinline__ Sequence sequence_of(const PagedArgs &a, int b) {
     return s;
 }
 
-// Tiles of a sequence: from the one with the first visible position, at
-// least one (an item without positions still writes its zeros).
+// Tiles of one item of a sequence in the list: from the one with the first
+// visible position, and before them as many as make 256 positions, which stand
+// for the time an item takes whatever its length.  (Without them the runs of
+// short items came last: 48 sequences of 1 to 6000 positions took 68 us; with
+// 128, 256, 384 and 768 positions 60, 51, 51 and 55 us.)
+template <int U>
+constexpr int kItemCost = 256 / kTile<U>;
 struct Tiles {
     int first, count;
 };
@@ -125,7 +130,7 @@ __device__ __forceinline__ Tiles tiles_of(const PagedArgs &a, const Sequence &s)
     const int64_t lo = a.window > 0 ? (int64_t)s.n - s.m - a.window + 1 : 0;
     Tiles t;
     t.first = lo > 0 ? (int)(lo / kTile<U>) : 0;
-    t.count = max(1, (s.n + kTile<U> - 1) / kTile<U> - t.first);
+    t.count = max(0, (s.n + kTile<U> - 1) / kTile<U> - t.first) + kItemCost<U>;
     return t;
 }
 
@@ -755,8 +760,8 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
         const int vis_lo = a.window > 0 ? max(0, pos_lo - a.window + 1) : 0;  // the first position any column sees
         // this warp's units: tiles first + ta .. first + tb - 1 that any column sees
         const int32_t *pages = a.pages + (int64_t)b * a.max_pages;
-        const int t_end = min((tiles.first + tb) * kTile<U>, min(s.n, pos_hi + 1));
-        int t0 = (tiles.first + ta) * kTile<U> + warp * (U * kUnit);
+        const int t_end = min((tiles.first + tb - kItemCost<U>) * kTile<U>, min(s.n, pos_hi + 1));
+        int t0 = (tiles.first + max(0, ta - kItemCost<U>)) * kTile<U> + warp * (U * kUnit);
         while (t0 + U * kUnit <= vis_lo) t0 += kTile<U>;
         uint4 qf[G];
         float mul[NT][2], qz[kRawK ? G : 1][2];
@@ -1146,8 +1151,8 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 3) paged_mass_kernel(co
             const int cols = min(8, ncols - c0);
             const int pos_lo = s.n - s.m + c0 / a.grp, pos_hi = s.n - s.m + (c0 + cols - 1) / a.grp;
             const int vis_lo = a.window > 0 ? max(0, pos_lo - a.window + 1) : 0;
-            const int t_end = min((tiles.first + tb) * kTile<U>, min(s.n, pos_hi + 1));
-            int t0 = (tiles.first + ta) * kTile<U> + warp * (U * kUnit);
+            const int t_end = min((tiles.first + tb - kItemCost<U>) * kTile<U>, min(s.n, pos_hi + 1));
+            int t0 = (tiles.first + max(0, ta - kItemCost<U>)) * kTile<U> + warp * (U * kUnit);
             while (t0 + U * kUnit <= vis_lo) t0 += kTile<U>;
             UnitRing<G, false, U> ring{p, copier, pages, ring_at, h, t0, t_end, pos_lo, pos_hi, a.window, lane, shaped};
             __syncwarp();  // every lane has read the ring's last unit of the columns before
@@ -1291,7 +1296,7 @@ cudaError_t run_attention(const PagedArgs &a, const DeviceInfo &dev, bool mass, 
     const int64_t positions = (int64_t)a.max_pages << a.p.lp, heads = (int64_t)a.n_seq * a.p.H;
     auto runs = [&](int64_t items, int per_sm, int U) {
         const int64_t most = (int64_t)dev.sm_count * per_sm < kMaxCtas ? (int64_t)dev.sm_count * per_sm : kMaxCtas;
-        const int64_t each = cdiv(cdiv(positions, kUnit * kWarps * U) * kUnit * kWarps * U, kMinPositions);
+        const int64_t each = cdiv((cdiv(positions, kUnit * kWarps * U) + 256 / (kUnit * kWarps * U)) * kUnit * kWarps * U, kMinPositions);
         if (items >= most || each >= most) return (unsigned)most;
         return (unsigned)(items * each < most ? items * each : most);
     };
