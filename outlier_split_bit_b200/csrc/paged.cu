@@ -963,13 +963,24 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
                     vu.template operands<EXACT>(gr, a0, a1, l0, l1);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        mma(o[nt][gr][0], a0, b[nt][0], b[nt][1]);
-                        mma(o[nt][gr][1], a1, b[nt][0], b[nt][1]);
                         if constexpr (EXACT) {
-                            mma(o[nt][gr][0], a0, rest[nt][0], rest[nt][1]);
-                            mma(o[nt][gr][1], a1, rest[nt][0], rest[nt][1]);
-                            mma(o[nt][gr][0], l0, b[nt][0], b[nt][1]);
-                            mma(o[nt][gr][1], l1, b[nt][0], b[nt][1]);
+                            // summed apart and added in FP32: the tensor core cuts
+                            // its sums off, which would add up over a long context
+                            float d0[4], d1[4];
+                            mma_first(d0, l0, b[nt][0], b[nt][1]);
+                            mma_first(d1, l1, b[nt][0], b[nt][1]);
+                            mma(d0, a0, rest[nt][0], rest[nt][1]);
+                            mma(d1, a1, rest[nt][0], rest[nt][1]);
+                            mma(d0, a0, b[nt][0], b[nt][1]);
+                            mma(d1, a1, b[nt][0], b[nt][1]);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                o[nt][gr][0][e] += d0[e];
+                                o[nt][gr][1][e] += d1[e];
+                            }
+                        } else {
+                            mma(o[nt][gr][0], a0, b[nt][0], b[nt][1]);
+                            mma(o[nt][gr][1], a1, b[nt][0], b[nt][1]);
                         }
                     }
                 }

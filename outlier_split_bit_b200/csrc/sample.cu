@@ -44,6 +44,7 @@ constexpr int kMaxVocab = 1 << 19;
 constexpr int kSegment = 512;                     // tokens of a warp's running sum
 constexpr int kMaxSegments = kMaxVocab / kSegment;
 constexpr int kList = 512;                        // tokens that are ranked against one another, all pairs
+constexpr int kKept = 1 << 15;                    // tokens of a CTA that stay in shared memory
 constexpr float kReach = 31.5f;                   // exp(-31.5) < 2^-45
 constexpr int kTable = 32;
 
@@ -78,7 +79,7 @@ struct Smem {
     float queue[kThreads / 32][64];
     u64 part[33];
     u64 found_above, total, cta_mass;
-    int found_bin, n_list, cta_ties, pick;
+    int found_bin, n_list[2], cta_ties, pick;  // n_list: of this gathering and the next, in turn
     float cta_max;
     uint32_t thr;
     int ties;
@@ -190,7 +191,7 @@ __device__ bool cluster_find(cg::cluster_group &cl, Smem &s, u64 need, bool ceil
             s.found_above = before + (second ? v0 : 0);
         }
     }
-    cl.sync();
+    __syncthreads();  // (what others still read here is written after the cluster's next barrier)
     *bin = s.found_bin;
     *above = s.found_above;
     __syncthreads();
@@ -217,12 +218,12 @@ __device__ __forceinline__ void for_each(const float *x, int i0, int i1, const F
     for (; i + (kBatch - 1) * kThreads < i1; i += kBatch * kThreads, at += kBatch * kThreads) {
         float v[kBatch];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) v[j] = __ldg(at + j * kThreads);
+        for (int j = 0; j < kBatch; ++j) v[j] = at[j * kThreads];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) f(v[j], i + j * kThreads);
     }
 #pragma unroll 1
-    for (; i < i1; i += kThreads, at += kThreads) f(__ldg(at), i);
+    for (; i < i1; i += kThreads, at += kThreads) f(*at, i);
 }
 
 __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_constant__ SampleArgs a) {
@@ -232,22 +233,26 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
     const int ranks = (int)cl.num_blocks(), rank = (int)cl.block_rank();
     const int row = blockIdx.x / ranks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int i0 = min(a.vocab, rank * a.per_cta), i1 = min(a.vocab, i0 + a.per_cta);
-    const float *x = a.x + (int64_t)row * a.stride;
+    const float *row_x = a.x + (int64_t)row * a.stride, *x = row_x;
     const float temp = a.temperature ? a.temperature[row] : 1.f;
 
     // the largest logit, and whether one is NaN
     float mx = -INFINITY;
     bool nan = false;
-    for_each(x, i0, i1, [&](float v, int) {
+    const bool kept = a.per_cta <= kKept;
+    float *mine_x = reinterpret_cast<float *>(raw + sizeof(Smem));
+    for_each(x, i0, i1, [&](float v, int i) {
         nan |= !(v == v);
         mx = fmaxf(mx, v);
+        if (kept) mine_x[i - i0] = v;
     });
+    if (kept) x = mine_x - i0;  // read from there after the next barrier
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     if (nan) atomicOr(&g_sample_error, 1u);
     if (tid < kTable) s.table[tid] = exp2((double)tid / kTable);
     if (tid == 0) {
         s.pick = a.vocab;
-        s.n_list = 0;
+        s.n_list[0] = s.n_list[1] = 0;
     }
     if (lane == 0) s.part[warp] = float_key(mx);
     __syncthreads();
@@ -298,20 +303,27 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
     uint32_t thr = 0;  // the smallest kept key,
     int ties = a.vocab;  // and how many of its tokens stay (the first ones)
     // Gathers the tokens for which take(v) into rank 0's list, as far as there
-    // is room; their number is left in its n_list.
-    auto gather = [&](auto take) {
+    // is room, and returns their number.  (The next gathering's counter is
+    // cleared here; a barrier of the cluster lies between the two.)
+    int gathering = 0;
+    auto gather = [&](auto take) -> int {
         Smem *to = cl.map_shared_rank(&s, 0);
+        int *count = &to->n_list[gathering & 1];
         for_each(x, i0, i1, [&](float v, int i) {
             if (take(v)) {
-                const int at = atomicAdd(&to->n_list, 1);
+                const int at = atomicAdd(count, 1);
                 if (at < kList) to->comp[at] = ((u64)float_key(v) << 32) | (0xFFFFFFFFu - (uint32_t)i);
             }
         });
         cl.sync();
-        if (to->n_list > kList) return;
-        if (rank == 0)
-            for (int e = tid; e < s.n_list; e += kThreads) s.q[e] = w.fixed(key_float((uint32_t)(s.comp[e] >> 32)), 0.0);
+        const int n = *count;
+        ++gathering;
+        if (rank == 0) {
+            if (tid == 0) s.n_list[gathering & 1] = 0;
+            if (n <= kList && tid < n) s.q[tid] = w.fixed(key_float((uint32_t)(s.comp[tid] >> 32)), 0.0);
+        }
         __syncthreads();
+        return n;
     };
     // Finds the threshold within step `bin`: the `need`-th token of it, or the
     // token at which its weight reaches `need`.  tie_w, tie_n: the weight and
@@ -319,8 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
     auto resolve = [&](int bin, u64 need, bool by_weight, u64 tie_w) {
         const uint32_t from = thr;
         auto member = [&](float v) { return step_of(v) == bin && (from == 0 || float_key(v) > from); };
-        gather(member);
-        const int n = cl.map_shared_rank(&s, 0)->n_list;
+        const int n = gather(member);
         if (n <= kList) {
             if (rank == 0) {
                 if (tid == 0) {
@@ -358,13 +369,9 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
             cl.sync();
             const Smem *o = cl.map_shared_rank(&s, 0);
             thr = o->thr;
-            ties = o->ties;
-            if (rank == 0 && tid == 0) s.n_list = 0;
-            cl.sync();
+            ties = o->ties;  // (written again, if at all, two barriers later)
             return;
         }
-        cl.sync();
-        if (rank == 0 && tid == 0) s.n_list = 0;
         uint32_t prefix = 0;
         for (int d = 0; d < kDigits; ++d) {
             clear_bins(s);
@@ -393,7 +400,56 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
     u = u == u ? fminf(fmaxf(u, 0.f), 0.99999994f) : 0.f;
     auto choose = [&](int i, u64 total) {
         a.ids[row] = i;
-        if (a.logp) a.logp[row] = (float)(w.exponent(x[i]) - log((double)total / (double)(1ll << kFix)));
+        if (a.logp) a.logp[row] = (float)(w.exponent(row_x[i]) - log((double)total / (double)(1ll << kFix)));
+    };
+    // what lies at or under `least_v` has no weight or fails min-p (with room
+    // for the rounding of the bound)
+    float least_v = -INFINITY;
+    if (mx < INFINITY) {
+        float reach = kReach + 1.f;
+        if (least > 0.0) reach = fminf(reach, (float)(-log(least)) + 1e-3f);
+        least_v = mx - reach * temp - 1e-6f * fabsf(mx);
+    }
+    // The end of a row whose kept tokens are all in rank 0's list of n (and no
+    // better ones outside it): rank 0 keeps the `most` best of them, then those
+    // before which, in order of value, less than `need` lies (0: top-p of the
+    // list's own whole), then min-p's, and chooses.
+    auto finish = [&](int n, int most, u64 need) {
+        const u64 mine = tid < n ? s.comp[tid] : 0;
+        u64 before = 0, own = 0;
+        if (tid < n) {
+            int place = 0;
+            for (int j = 0; j < n; ++j)
+                if (s.comp[j] > mine) {
+                    ++place;
+                    before += s.q[j];
+                }
+            if (place < most) own = s.q[tid];
+        }
+        u64 whole;
+        block_exclusive(own, s.part, &whole);
+        if (need == 0) {
+            need = whole;
+            if (p < 1.f) {
+                bool rest = false;
+                need = p > 0.f ? fraction_of(p, whole, &rest) : 0;
+                need += rest;
+                if (need == 0) need = 1;
+            }
+        }
+        if (own && !(before < need && w.weight(key_float((uint32_t)(mine >> 32))) >= least)) own = 0;
+        __syncthreads();
+        if (tid < n) s.q[tid] = own;
+        u64 left;
+        block_exclusive(own, s.part, &left);
+        bool rest;
+        const u64 target = fraction_of(u, left, &rest);
+        if (own) {
+            u64 run = 0;
+            for (int j = 0; j < n; ++j)
+                if ((uint32_t)s.comp[j] > (uint32_t)mine) run += s.q[j];  // ~index
+            if (run <= target && target < run + own) choose((int)(0xFFFFFFFFu - (uint32_t)mine), left);
+        }
     };
     if (k > 0 && k < a.vocab) {
         clear_bins(s);
@@ -404,48 +460,12 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
         int bin;
         u64 above, total, unused;
         if (cluster_find(cl, s, (u64)k, false, 0.f, &bin, &above, &total, &unused)) {
-            // how many tokens the step holds
+            // how many tokens the step holds (the bins are cleared after the next barrier)
             u64 members = 0;
             for (int r = 0; r < ranks; ++r) members += cl.map_shared_rank(&s, r)->lo[bin];
-            cl.sync();
             if (above + members <= kList) {
-                gather([&](float v) { return step_of(v) <= bin; });
-                if (rank != 0) return;  // (nobody reads another CTA's memory any more)
-                // rank and weight before each, in order of value
-                const int n = s.n_list;
-                const u64 mine = tid < n ? s.comp[tid] : 0;
-                u64 before = 0, own = 0;
-                if (tid < n) {
-                    int place = 0;
-                    for (int j = 0; j < n; ++j)
-                        if (s.comp[j] > mine) {
-                            ++place;
-                            before += s.q[j];
-                        }
-                    if (place < k) own = s.q[tid];
-                }
-                u64 whole;
-                block_exclusive(own, s.part, &whole);
-                u64 need = whole;
-                if (p < 1.f) {
-                    bool rest = false;
-                    need = p > 0.f ? fraction_of(p, whole, &rest) : 0;
-                    need += rest;
-                    if (need == 0) need = 1;
-                }
-                if (own && !(before < need && w.weight(key_float((uint32_t)(mine >> 32))) >= least)) own = 0;
-                __syncthreads();
-                if (tid < n) s.q[tid] = own;
-                u64 left;
-                block_exclusive(own, s.part, &left);
-                bool rest;
-                const u64 target = fraction_of(u, left, &rest);
-                if (own) {
-                    u64 run = 0;
-                    for (int j = 0; j < n; ++j)
-                        if ((uint32_t)s.comp[j] > (uint32_t)mine) run += s.q[j];  // ~index
-                    if (run <= target && target < run + own) choose((int)(0xFFFFFFFFu - (uint32_t)mine), left);
-                }
+                const int n = gather([&](float v) { return step_of(v) <= bin; });
+                if (rank == 0) finish(n, k, 0);  // (nobody reads another CTA's memory any more)
                 return;
             }
             resolve(bin, (u64)k - above, false, 0);
@@ -463,21 +483,30 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
         int bin;
         u64 above, total, need;
         cluster_find(cl, s, 0, true, p, &bin, &above, &total, &need);
+        if (least > 0.0 && thr == 0) {
+            // min-p may leave few: what passes it and lies over the threshold's
+            // step or in it holds all that stays, and all that is better
+            const int n = gather([&](float v) { return v > least_v && step_of(v) <= bin; });
+            if (n <= kList) {
+                if (rank == 0) finish(n, kList, need);
+                return;
+            }
+            cl.sync();  // (the count was read; the list starts anew)
+        }
         resolve(bin, need - above, true, tie_w);
+    } else if (least > 0.0 && thr == 0) {
+        const int n = gather([&](float v) { return v > least_v; });
+        if (n <= kList) {
+            if (rank == 0) finish(n, kList, 0);
+            return;
+        }
     }
 
     // the kept weight of each segment in index order, thr's ties counted apart
     const int segs = (i1 - i0 + kSegment - 1) / kSegment;
     const u64 tie_q = thr > kKeyNegInf ? w.fixed(key_float(thr), least) : 0;
     const float thr_v = thr > kKeyNegInf ? key_float(thr) : -INFINITY;
-    // what lies at or under `cut` is not kept or has no weight: the threshold,
-    // the reach, and (with room for the rounding of these) min-p's bound
-    float cut = thr_v;
-    if (mx < INFINITY) {
-        float reach = kReach + 1.f;
-        if (least > 0.0) reach = fminf(reach, (float)(-log(least)) + 1e-3f);
-        cut = fmaxf(cut, mx - reach * temp - 1e-6f * fabsf(mx));
-    }
+    const float cut = fmaxf(thr_v, least_v);  // what lies at or under it is not kept, but for thr's ties
     auto over = [&](float v) { return v > cut; };
     if (tid == 0) {
         s.cta_mass = 0;
@@ -493,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
             float v[kBatch];
             const int i = i0 + g * kSegment + j + lane;
 #pragma unroll
-            for (int c = 0; c < kBatch; ++c) v[c] = i + 32 * c < i1 ? __ldg(x + i + 32 * c) : __int_as_float(0x7FC00000);
+            for (int c = 0; c < kBatch; ++c) v[c] = i + 32 * c < i1 ? x[i + 32 * c] : __int_as_float(0x7FC00000);
 #pragma unroll
             for (int c = 0; c < kBatch; ++c) {
                 const bool keep = over(v[c]);
@@ -592,7 +621,7 @@ spectra_status launch_sample(const float *logits, int rows, int vocab, int64_t s
     while (ranks < 8 && (int64_t)rows * ranks * 2 <= dev.sm_count && vocab >= 2 * ranks * 4096) ranks *= 2;
     a.per_cta = (int)(cdiv(vocab, (int64_t)ranks * kSegment) * kSegment);
     static std::atomic<uint64_t> ready{0};
-    cudaError_t e = allow_smem((const void *)sample_kernel, (int)sizeof(Smem), dev, &ready);
+    cudaError_t e = allow_smem((const void *)sample_kernel, (int)(sizeof(Smem) + kKept * 4), dev, &ready);
     if (e != cudaSuccess) return SPECTRA_ERR_CUDA;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -601,7 +630,7 @@ spectra_status launch_sample(const float *logits, int rows, int vocab, int64_t s
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)rows * ranks, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = sizeof(Smem);
+    cfg.dynamicSmemBytes = sizeof(Smem) + (a.per_cta <= kKept ? (size_t)a.per_cta * 4 : 0);
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
