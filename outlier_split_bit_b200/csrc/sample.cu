@@ -44,9 +44,9 @@ constexpr int kMaxVocab = 1 << 19;
 constexpr int kSegment = 512;                     // tokens of a warp's running sum
 constexpr int kMaxSegments = kMaxVocab / kSegment;
 constexpr int kList = 512;                        // tokens that are ranked against one another, all pairs
-constexpr int kKept = 1 << 15;                    // tokens of a CTA that stay in shared memory
 constexpr float kReach = 31.5f;                   // exp(-31.5) < 2^-45
 constexpr int kTable = 32;
+constexpr int kMaxRanks = 8;
 
 // Constants of the exponential, in the kernel's parameters (as operands they
 // cost no instruction there).
@@ -147,11 +147,19 @@ __device__ bool cluster_find(cg::cluster_group &cl, Smem &s, u64 need, bool ceil
     cl.sync();
     u64 own = 0;
     for (int i = tid; i < n; i += kThreads) {
-        u64 v = 0;
-        for (int r = 0; r < ranks; ++r) {
-            const Smem *o = cl.map_shared_rank(&s, r);
-            v += (u64)o->lo[rank * n + i] + ((u64)o->hi[rank * n + i] << 32);
+        uint32_t lo[kMaxRanks], hi[kMaxRanks];  // all loads in flight at once
+#pragma unroll
+        for (int r = 0; r < kMaxRanks; ++r) {
+            lo[r] = hi[r] = 0;
+            if (r < ranks) {
+                const Smem *o = cl.map_shared_rank(&s, r);
+                lo[r] = o->lo[rank * n + i];
+                hi[r] = o->hi[rank * n + i];
+            }
         }
+        u64 v = 0;
+#pragma unroll
+        for (int r = 0; r < kMaxRanks; ++r) v += (u64)lo[r] + ((u64)hi[r] << 32);
         s.merged[i] = v;
         own += v;
     }
@@ -159,8 +167,11 @@ __device__ bool cluster_find(cg::cluster_group &cl, Smem &s, u64 need, bool ceil
     block_exclusive(own, s.part, &sum);
     if (tid == 0) s.total = sum;
     cl.sync();
-    u64 all = 0;
-    for (int r = 0; r < ranks; ++r) all += cl.map_shared_rank(&s, r)->total;
+    u64 totals[kMaxRanks], all = 0;
+#pragma unroll
+    for (int r = 0; r < kMaxRanks; ++r) totals[r] = r < ranks ? cl.map_shared_rank(&s, r)->total : 0;
+#pragma unroll
+    for (int r = 0; r < kMaxRanks; ++r) all += totals[r];
     *total = all;
     if (ceil_of_p) {
         // a token stays while the sum before it is under p of the whole: the
@@ -175,11 +186,12 @@ __device__ bool cluster_find(cg::cluster_group &cl, Smem &s, u64 need, bool ceil
     if (ok) {
         u64 run = 0;
         int at = 0;
-        for (; at < ranks - 1; ++at) {
-            const u64 v = cl.map_shared_rank(&s, at)->total;
-            if (need <= run + v) break;
-            run += v;
-        }
+#pragma unroll
+        for (int r = 0; r < kMaxRanks - 1; ++r)
+            if (at == r && r < ranks - 1 && need > run + totals[r]) {
+                run += totals[r];
+                ++at;
+            }
         const Smem *o = cl.map_shared_rank(&s, at);
         // n <= 2 * kThreads bins of that share, two neighbours per thread
         const u64 v0 = 2 * tid < n ? o->merged[2 * tid] : 0, v1 = 2 * tid + 1 < n ? o->merged[2 * tid + 1] : 0;
@@ -218,12 +230,12 @@ __device__ __forceinline__ void for_each(const float *x, int i0, int i1, const F
     for (; i + (kBatch - 1) * kThreads < i1; i += kBatch * kThreads, at += kBatch * kThreads) {
         float v[kBatch];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) v[j] = at[j * kThreads];
+        for (int j = 0; j < kBatch; ++j) v[j] = __ldg(at + j * kThreads);
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) f(v[j], i + j * kThreads);
     }
 #pragma unroll 1
-    for (; i < i1; i += kThreads, at += kThreads) f(*at, i);
+    for (; i < i1; i += kThreads, at += kThreads) f(__ldg(at), i);
 }
 
 __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_constant__ SampleArgs a) {
@@ -233,20 +245,16 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
     const int ranks = (int)cl.num_blocks(), rank = (int)cl.block_rank();
     const int row = blockIdx.x / ranks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int i0 = min(a.vocab, rank * a.per_cta), i1 = min(a.vocab, i0 + a.per_cta);
-    const float *row_x = a.x + (int64_t)row * a.stride, *x = row_x;
+    const float *x = a.x + (int64_t)row * a.stride;
     const float temp = a.temperature ? a.temperature[row] : 1.f;
 
     // the largest logit, and whether one is NaN
     float mx = -INFINITY;
     bool nan = false;
-    const bool kept = a.per_cta <= kKept;
-    float *mine_x = reinterpret_cast<float *>(raw + sizeof(Smem));
-    for_each(x, i0, i1, [&](float v, int i) {
+    for_each(x, i0, i1, [&](float v, int) {
         nan |= !(v == v);
         mx = fmaxf(mx, v);
-        if (kept) mine_x[i - i0] = v;
     });
-    if (kept) x = mine_x - i0;  // read from there after the next barrier
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     if (nan) atomicOr(&g_sample_error, 1u);
     if (tid < kTable) s.table[tid] = exp2((double)tid / kTable);
@@ -263,7 +271,9 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
     }
     cl.sync();
     mx = -INFINITY;
-    for (int r = 0; r < ranks; ++r) mx = fmaxf(mx, cl.map_shared_rank(&s, r)->cta_max);
+#pragma unroll
+    for (int r = 0; r < kMaxRanks; ++r)
+        if (r < ranks) mx = fmaxf(mx, cl.map_shared_rank(&s, r)->cta_max);
     if (mx == -INFINITY) {
         if (rank == 0 && tid == 0) {
             a.ids[row] = -1;
@@ -344,12 +354,11 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
                     const u64 mine = s.comp[tid], own = by_weight ? s.q[tid] : 1;
                     u64 before = 0;
                     int same = 1;
+#pragma unroll 8
                     for (int j = 0; j < n; ++j) {
-                        const u64 c = s.comp[j];
-                        if (c > mine) {
-                            before += by_weight ? s.q[j] : 1;
-                            same += (uint32_t)(c >> 32) == (uint32_t)(mine >> 32);
-                        }
+                        const u64 c = s.comp[j], q = by_weight ? s.q[j] : 1;
+                        before += c > mine ? q : 0;
+                        same += c > mine && (uint32_t)(c >> 32) == (uint32_t)(mine >> 32);
                     }
                     listed = own;
                     if (before < need && need <= before + own) {
@@ -400,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
     u = u == u ? fminf(fmaxf(u, 0.f), 0.99999994f) : 0.f;
     auto choose = [&](int i, u64 total) {
         a.ids[row] = i;
-        if (a.logp) a.logp[row] = (float)(w.exponent(row_x[i]) - log((double)total / (double)(1ll << kFix)));
+        if (a.logp) a.logp[row] = (float)(w.exponent(x[i]) - log((double)total / (double)(1ll << kFix)));
     };
     // what lies at or under `least_v` has no weight or fails min-p (with room
     // for the rounding of the bound)
@@ -419,11 +428,13 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
         u64 before = 0, own = 0;
         if (tid < n) {
             int place = 0;
-            for (int j = 0; j < n; ++j)
-                if (s.comp[j] > mine) {
-                    ++place;
-                    before += s.q[j];
-                }
+#pragma unroll 8
+            for (int j = 0; j < n; ++j) {
+                const u64 q = s.q[j];
+                const bool better = s.comp[j] > mine;
+                place += better;
+                before += better ? q : 0;
+            }
             if (place < most) own = s.q[tid];
         }
         u64 whole;
@@ -446,8 +457,11 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
         const u64 target = fraction_of(u, left, &rest);
         if (own) {
             u64 run = 0;
-            for (int j = 0; j < n; ++j)
-                if ((uint32_t)s.comp[j] > (uint32_t)mine) run += s.q[j];  // ~index
+#pragma unroll 8
+            for (int j = 0; j < n; ++j) {
+                const u64 q = s.q[j];
+                run += (uint32_t)s.comp[j] > (uint32_t)mine ? q : 0;  // ~index
+            }
             if (run <= target && target < run + own) choose((int)(0xFFFFFFFFu - (uint32_t)mine), left);
         }
     };
@@ -462,7 +476,9 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
         if (cluster_find(cl, s, (u64)k, false, 0.f, &bin, &above, &total, &unused)) {
             // how many tokens the step holds (the bins are cleared after the next barrier)
             u64 members = 0;
-            for (int r = 0; r < ranks; ++r) members += cl.map_shared_rank(&s, r)->lo[bin];
+#pragma unroll
+            for (int r = 0; r < kMaxRanks; ++r)
+                if (r < ranks) members += cl.map_shared_rank(&s, r)->lo[bin];
             if (above + members <= kList) {
                 const int n = gather([&](float v) { return step_of(v) <= bin; });
                 if (rank == 0) finish(n, k, 0);  // (nobody reads another CTA's memory any more)
@@ -483,9 +499,10 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
         int bin;
         u64 above, total, need;
         cluster_find(cl, s, 0, true, p, &bin, &above, &total, &need);
-        if (least > 0.0 && thr == 0) {
-            // min-p may leave few: what passes it and lies over the threshold's
-            // step or in it holds all that stays, and all that is better
+        if (thr == 0 && (double)total <= 2.0 * kList * (double)(1ll << kFix) * least) {
+            // min-p is likely to leave few (total / least at most, and those that
+            // pass it weigh more than that): what passes it and lies over the
+            // threshold's step or in it holds all that stays, and all that is better
             const int n = gather([&](float v) { return v > least_v && step_of(v) <= bin; });
             if (n <= kList) {
                 if (rank == 0) finish(n, kList, need);
@@ -522,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
             float v[kBatch];
             const int i = i0 + g * kSegment + j + lane;
 #pragma unroll
-            for (int c = 0; c < kBatch; ++c) v[c] = i + 32 * c < i1 ? x[i + 32 * c] : __int_as_float(0x7FC00000);
+            for (int c = 0; c < kBatch; ++c) v[c] = i + 32 * c < i1 ? __ldg(x + i + 32 * c) : __int_as_float(0x7FC00000);
 #pragma unroll
             for (int c = 0; c < kBatch; ++c) {
                 const bool keep = over(v[c]);
@@ -618,10 +635,10 @@ spectra_status launch_sample(const float *logits, int rows, int vocab, int64_t s
     a.vocab = vocab;
     // as many CTAs a row as keep one wave, each with 4096 tokens or more
     int ranks = 1;
-    while (ranks < 8 && (int64_t)rows * ranks * 2 <= dev.sm_count && vocab >= 2 * ranks * 4096) ranks *= 2;
+    while (ranks < kMaxRanks && (int64_t)rows * ranks * 2 <= dev.sm_count && vocab >= 2 * ranks * 4096) ranks *= 2;
     a.per_cta = (int)(cdiv(vocab, (int64_t)ranks * kSegment) * kSegment);
     static std::atomic<uint64_t> ready{0};
-    cudaError_t e = allow_smem((const void *)sample_kernel, (int)(sizeof(Smem) + kKept * 4), dev, &ready);
+    cudaError_t e = allow_smem((const void *)sample_kernel, (int)sizeof(Smem), dev, &ready);
     if (e != cudaSuccess) return SPECTRA_ERR_CUDA;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -630,7 +647,7 @@ spectra_status launch_sample(const float *logits, int rows, int vocab, int64_t s
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)rows * ranks, 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = sizeof(Smem) + (a.per_cta <= kKept ? (size_t)a.per_cta * 4 : 0);
+    cfg.dynamicSmemBytes = sizeof(Smem);
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
