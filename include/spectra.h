@@ -455,8 +455,9 @@ SPECTRA_API spectra_status spectra_embed_rows(const spectra_layer *table, const 
  * SPECTRA_ERR_INTERNAL if a wait gave up, else SPECTRA_ERR_INVALID_ARG if the
  * gather saw a bad id, a paged operator a value out of bounds or the sampler
  * an empty row, else SPECTRA_ERR_NONFINITE from a KV append or the sampler,
- * else SPECTRA_ERR_RANGE from a KV append (a scale overflowing FP16) or from
- * the tensor-core matmul (an FP16 operand out of range), else SPECTRA_OK.
+ * else SPECTRA_ERR_RANGE from a KV append (a scale overflowing FP16), from the
+ * tensor-core matmul (an FP16 operand out of range) or from the paged attention
+ * (a non-finite output), else SPECTRA_OK.
  * Synchronous on `stream`.
  */
 SPECTRA_API spectra_status spectra_device_status(void *stream);
@@ -625,7 +626,7 @@ typedef struct {
     const int32_t *q_start;  /* device [n_seq + 1], nondecreasing: sequence b's new tokens are
                                 the rows q_start[b] .. q_start[b+1]-1; NULL: row b alone */
     int32_t n_seq;
-    int32_t max_pages;       /* page ids per row of pages */
+    int32_t max_pages;       /* page ids per row of pages; times page_size at most 2^30 */
     int32_t n_rows;          /* rows of q */
     int32_t max_q;           /* at least every sequence's number of rows */
     int32_t n_q_heads;       /* a multiple of the pool's n_heads, at most 64 times it */
@@ -634,7 +635,8 @@ typedef struct {
     float softcap;           /* 0: none */
     const uint16_t *q;       /* device, BF16 bits [n_rows][n_q_heads][head_dim] */
     const float *slopes;     /* device [n_q_heads], or NULL */
-    void *out;               /* device [n_rows][n_q_heads][head_dim] of out_dtype */
+    void *out;               /* device [n_rows][n_q_heads][head_dim] of out_dtype; must not
+                                overlap q */
     spectra_dtype out_dtype;
     int32_t update_mass;     /* nonzero: add the weights to the pool's mass */
     float *lse;              /* device [n_rows][n_q_heads], or NULL */
@@ -656,9 +658,14 @@ typedef struct {
  * they count the entries that are left.
  *   workspace  device, 16-byte aligned, >= the stated size; its contents need
  *              not be kept, and calls that run in stream order may share it
- * FP32 scores, softmax and sums; the products of the 4-bit codes with q and
- * with the weights run on the tensor cores with FP32 accumulation.  Out of
- * bounds values are reported by spectra_device_status as INVALID_ARG and
+ * FP32 scores, softmax and sums; the products run on the tensor cores with
+ * FP32 accumulation, K's with the exact codes.  For a BF16 output V's values
+ * and the weights (or the weights and their products with V's scales) are
+ * rounded to FP16 on the way, 2^-11 each, an eighth of the output's own
+ * rounding; an FP32 output has no such rounding.  A non-finite output (from a
+ * non-finite q, or from V's entries beyond 65504 in magnitude, which FP16 does
+ * not hold) is reported by spectra_device_status as RANGE.  Out of bounds
+ * values are reported by spectra_device_status as INVALID_ARG and
  * touch nothing: a page id outside the pool hides its positions, a length
  * outside [0, max_pages*page_size] counts as 0, and a sequence whose rows lie
  * outside [0, n_rows) or number more than max_q has its rows left as they
@@ -685,7 +692,8 @@ SPECTRA_API spectra_status spectra_attention_paged(const spectra_kv_pool *pool,
  * older; a NaN counts as the smallest).  The kept entries (K, V and mass)
  * move, in their order, to positions 0 .. keep-1 of fresh pages; the old
  * pages are left as they are, for the caller to free.
- *   pages, lengths, max_pages, n_seq   as spectra_paged_query
+ *   pages, lengths, max_pages, n_seq   as spectra_paged_query (dst_max_pages
+ *                and max_pages times page_size at most 2^30)
  *   dst_pages    device [n_seq][dst_max_pages] page ids, dst_max_pages *
  *                page_size >= budget; no page named here may be another
  *                sequence's, or named in the used part of pages

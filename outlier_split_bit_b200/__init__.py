@@ -535,6 +535,14 @@ def _opt(t, name, dtype, shape, dev):
     return None if t is None else _arg(t, name, dtype, shape, dev)
 
 
+def _room(workspace: torch.Tensor, dev) -> int:
+    """Bytes of a caller's workspace, which must lie on dev in one piece."""
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: a contiguous tensor on {dev} is wanted, got one on {workspace.device} with "
+                         f"strides {workspace.stride()}")
+    return workspace.numel() * workspace.element_size()
+
+
 # The current stream's handle without a Stream object around it, which costs
 # more than a launch; the public call where this torch has no such entry.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
@@ -650,6 +658,8 @@ class KVPool:
             return _elsewhere(dev, stream, self.read, slots, out_dtype=out_dtype)
         n = slots.shape[0]
         sp = _arg(slots, "slots", torch.int32, (n,), dev)
+        if out_dtype not in _DT:
+            raise ValueError(f"out_dtype: float32 or bfloat16 is wanted, got {out_dtype}")
         k = torch.empty(n, self.n_heads, self.head_dim, dtype=out_dtype, device=dev)
         v = torch.empty_like(k)
         _check(_lib.load().spectra_kv_pool_read(self._ref, sp, n, k.data_ptr(), v.data_ptr(), _DT[out_dtype],
@@ -678,7 +688,7 @@ def spectra_attention_paged(pool: KVPool, pages: torch.Tensor, lengths: torch.Te
     that far back and further.  Returns out [n_rows, n_q_heads, head_dim], with
     want_lse also the rows' log sums (float [n_rows, n_q_heads]); update_mass
     adds the weights to the pool's mass.  Rows outside every sequence are not
-    written."""
+    written; out may not overlap q."""
     dev = pool.device
     if stream is not None or _current_device() != dev.index:
         return _elsewhere(dev, stream, spectra_attention_paged, pool, pages, lengths, q, q_start, max_q=max_q,
@@ -696,6 +706,8 @@ def spectra_attention_paged(pool: KVPool, pages: torch.Tensor, lengths: torch.Te
     at_start = 0 if q_start is None else _arg(q_start, "q_start", torch.int32, (n_seq + 1,), dev)
     at_q = _arg(q, "q", torch.bfloat16, shape, dev)
     at_slopes = 0 if slopes is None else _arg(slopes, "slopes", torch.float32, (hq,), dev)
+    if (out_dtype if out is None else out.dtype) not in _DT:
+        raise ValueError("out: float32 or bfloat16 is wanted")
     if out is not None:
         _arg(out, "out", out.dtype, shape, dev)
     elif out_dtype is torch.bfloat16:
@@ -710,7 +722,7 @@ def spectra_attention_paged(pool: KVPool, pages: torch.Tensor, lengths: torch.Te
             need = pool._ws[n_rows, hq] = lib.spectra_attention_paged_workspace_size(pool._ref, n_rows, hq)
         workspace, room = torch.empty(need or 16, dtype=torch.uint8, device=dev), need
     else:
-        room = workspace.numel() * workspace.element_size()
+        room = _room(workspace, dev)
     x = _PAGED_QUERY(at_pages, at_lengths, at_start, n_seq, max_pages, n_rows, max_q, hq, window,
                      d ** -0.5 if scale is None else scale, softcap, at_q, at_slopes, out.data_ptr(),
                      _DT[out.dtype], 1 if update_mass else 0, lse.data_ptr() if want_lse else 0)
@@ -743,7 +755,7 @@ def spectra_kv_evict(pool: KVPool, pages: torch.Tensor, lengths: torch.Tensor, d
         room = lib.spectra_kv_evict_workspace_size(pool._ref, n_seq, max_pages)
         workspace = torch.empty(room or 16, dtype=torch.uint8, device=dev)
     else:
-        room = workspace.numel() * workspace.element_size()
+        room = _room(workspace, dev)
     _check(lib.spectra_kv_evict(pool._ref, at_pages, max_pages, at_lengths, n_seq, at_dst, dst_max, budget, recent,
                                 at_new, workspace.data_ptr(), room, _raw_stream(dev.index)), "spectra_kv_evict")
     return new_lengths

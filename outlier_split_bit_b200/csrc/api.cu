@@ -632,7 +632,7 @@ spectra_status spectra_attention_paged(const spectra_kv_pool *pool, const spectr
     if (!x || x->n_seq < 0 || x->n_rows < 0) return SPECTRA_ERR_INVALID_ARG;
     if (!paged_heads_ok(pool, x->n_q_heads)) return SPECTRA_ERR_SHAPE;
     if (x->n_seq > 65535 || x->max_pages < 1 || x->max_q < 1 || x->window < 0) return SPECTRA_ERR_SHAPE;
-    if ((int64_t)x->max_pages * pool->page_size >= ((int64_t)1 << 31)) return SPECTRA_ERR_SHAPE;
+    if ((int64_t)x->max_pages * pool->page_size > ((int64_t)1 << 30)) return SPECTRA_ERR_SHAPE;
     if (x->out_dtype != SPECTRA_F32 && x->out_dtype != SPECTRA_BF16) return SPECTRA_ERR_INVALID_ARG;
     if (!std::isfinite(x->scale) || !std::isfinite(x->softcap) || x->softcap < 0.f) return SPECTRA_ERR_INVALID_ARG;
     if (x->update_mass && !pool->mass) return SPECTRA_ERR_INVALID_ARG;
@@ -645,6 +645,10 @@ spectra_status spectra_attention_paged(const spectra_kv_pool *pool, const spectr
     if (!aligned4(x->pages) || !aligned4(x->lengths) || !aligned4(x->q_start) || !aligned4(x->slopes) ||
         !aligned4(x->lse) || !aligned16(x->q) || !aligned16(x->out) || !aligned16(workspace))
         return SPECTRA_ERR_ALIGN;
+    const uintptr_t from = (uintptr_t)x->q, to = (uintptr_t)x->out;
+    const uintptr_t elems = (uintptr_t)x->n_rows * x->n_q_heads * pool->head_dim;
+    if (from < to + elems * (x->out_dtype == SPECTRA_F32 ? 4 : 2) && to < from + elems * 2)
+        return SPECTRA_ERR_INVALID_ARG;
     if (workspace_bytes < paged_workspace_bytes(x->n_rows, x->n_q_heads, pool->n_heads, pool->head_dim))
         return SPECTRA_ERR_BUFFER_TOO_SMALL;
     DeviceInfo dev;
@@ -655,7 +659,7 @@ spectra_status spectra_attention_paged(const spectra_kv_pool *pool, const spectr
 
 size_t spectra_kv_evict_workspace_size(const spectra_kv_pool *pool, int32_t n_seq, int32_t max_pages) {
     if (!pool || check_pool_shape(pool->n_heads, pool->head_dim, pool->page_size, pool->n_pages) != SPECTRA_OK ||
-        n_seq < 0 || n_seq > 65535 || max_pages < 1 || (int64_t)max_pages * pool->page_size >= ((int64_t)1 << 31))
+        n_seq < 0 || n_seq > 65535 || max_pages < 1 || (int64_t)max_pages * pool->page_size > ((int64_t)1 << 30))
         return 0;
     return evict_workspace_bytes(n_seq, pool->n_heads, (int64_t)max_pages * pool->page_size);
 }
@@ -670,8 +674,8 @@ spectra_status spectra_kv_evict(const spectra_kv_pool *pool, const int32_t *page
     if (!pool->mass || n_seq < 0) return SPECTRA_ERR_INVALID_ARG;
     if (n_seq > 65535 || max_pages < 1 || dst_max_pages < 1 || budget < 1 || recent < 0 || recent > budget)
         return SPECTRA_ERR_SHAPE;
-    if ((int64_t)max_pages * pool->page_size >= ((int64_t)1 << 31) ||
-        (int64_t)dst_max_pages * pool->page_size >= ((int64_t)1 << 31) ||
+    if ((int64_t)max_pages * pool->page_size > ((int64_t)1 << 30) ||
+        (int64_t)dst_max_pages * pool->page_size > ((int64_t)1 << 30) ||
         (int64_t)dst_max_pages * pool->page_size < budget)
         return SPECTRA_ERR_SHAPE;
     if (n_seq == 0) return SPECTRA_OK;

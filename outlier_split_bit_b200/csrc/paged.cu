@@ -504,7 +504,7 @@ __device__ __forceinline__ void query_operands(const uint16_t *q, int t, uint4 (
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const uint32_t e = max(top >> 7, 16u);  // the largest value's exponent field (2^-111 or less: as 2^-111)
     const float up = __uint_as_float((268u - e) << 23);
-    back = __uint_as_float((e - 14u) << 23);
+    back = e == 255u ? __int_as_float(0x7FC00000) : __uint_as_float((e - 14u) << 23);  // NaN: q is not finite
 #pragma unroll
     for (int gr = 0; gr < G; ++gr) {
         const uint32_t w[4] = {f[gr].x, f[gr].y, f[gr].z, f[gr].w};
@@ -988,11 +988,11 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         if constexpr (kRawV) {
-            float odd = 0.f;  // NaN if a sum is not finite
+            float odd = 0.f;  // NaN if a sum is not finite (though its query is)
 #pragma unroll
             for (int gr = 0; gr < G; ++gr)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) odd = fmaf(o[0][gr][e >> 2][e & 3], 0.f, odd);
+                for (int e = 0; e < 8; ++e) odd = fmaf(mul[0][e & 1] == mul[0][e & 1] ? o[0][gr][e >> 2][e & 3] : 0.f, 0.f, odd);
             if (low == 0 && __any_sync(0xffffffffu, odd != 0.f)) continue;
 #pragma unroll
             for (int gr = 0; gr < G; ++gr)
@@ -1360,7 +1360,7 @@ spectra_status launch_paged_attention(const spectra_kv_pool &pool, const spectra
     a.max_q = x.max_q < x.n_rows ? x.max_q : x.n_rows;
     a.Hq = x.n_q_heads;
     a.grp = x.n_q_heads / pool.n_heads;
-    a.window = x.window;
+    a.window = x.window < (1 << 30) ? x.window : 1 << 30;  // positions number 2^30 at most
     a.scale = x.scale;
     a.cap = x.softcap;
     const Workspace w(a.p.G, 8 * n_tiles(a.p.G, (int64_t)a.max_q * a.grp), x.n_rows, x.n_q_heads);

@@ -281,8 +281,8 @@ __global__ void __launch_bounds__(256) pool_read_kernel(PoolView p, const int32_
 // ---- eviction ----
 // Two launches: select (one CTA per sequence and head) finds the smallest
 // kept key by a radix descent and, per chunk of positions, the number of kept
-// positions before it; move (one CTA per chunk, launched as a programmatic
-// dependent) copies the chunk's kept entries to their places in the fresh
+// positions before it; move (a CTA per chunk or per few, launched as a
+// programmatic dependent) copies the chunk's kept entries to their places in the fresh
 // pages.  Select reads every weight once, through the page table with eight
 // look-ups in flight per thread, and keeps the keys in shared memory (of the
 // first kKeys positions; what lies past them is read again in each pass).
@@ -416,18 +416,15 @@ template <int G>
 __global__ void __launch_bounds__(kMoveChunk) evict_move_kernel(EvictArgs a) {
     __shared__ int part[33];
     __shared__ int64_t s_src[kMoveChunk], s_dst[kMoveChunk];  // the chunk's kept entries
-    const int b = blockIdx.z, h = blockIdx.y, c = blockIdx.x, tid = threadIdx.x;
+    const int b = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
     const EvictPlan e = evict_plan(a, b);
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // select's results; nothing was written before
+    for (int c = blockIdx.x; c * kMoveChunk < e.n; c += gridDim.x) {
     const int t = c * kMoveChunk + tid;
-    if (c * kMoveChunk >= e.n) {
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        return;
-    }
     const int64_t bh = (int64_t)b * a.p.H + h;
     const int32_t ts = t < e.n ? a.p.token_slot(a.pages + (int64_t)b * a.max_pages, t) : -1;
     const int64_t src = ts >= 0 ? a.p.slot(ts, h) : -1;
     const float mass = src >= 0 ? a.p.mass[src] : 0.f;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // select's results; nothing was written before
     const bool old = t < e.old;
     bool keep = t < e.n;
     int base = c * kMoveChunk, rank = tid, total = min(kMoveChunk, e.n - c * kMoveChunk);
@@ -474,6 +471,8 @@ __global__ void __launch_bounds__(kMoveChunk) evict_move_kernel(EvictArgs a) {
             a.p.ks[to] = u;
             a.p.vs[to] = v;
         }
+    }
+    __syncthreads();
     }
 }
 
@@ -553,7 +552,9 @@ spectra_status launch_evict(const spectra_kv_pool &pool, const int32_t *pages, i
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)a.nch, (unsigned)a.p.H, (unsigned)n_seq);
+    // a few waves of CTAs at most, however wide the page tables are
+    const int64_t per_head = cdiv((int64_t)dev.sm_count * 32, (int64_t)bh);
+    cfg.gridDim = dim3((unsigned)(per_head < a.nch ? per_head : a.nch), (unsigned)a.p.H, (unsigned)n_seq);
     cfg.blockDim = dim3(kMoveChunk, 1, 1);
     cfg.stream = s;
     cfg.attrs = &attr;

@@ -70,7 +70,7 @@ def test_read_refusals(L):
 
 def _query(**other):
     f = dict(pages=FAKE, lengths=FAKE, q_start=FAKE, n_seq=3, max_pages=5, n_rows=7, max_q=4, n_q_heads=12, window=0,
-             scale=0.1, softcap=0.0, q=FAKE, slopes=None, out=FAKE, out_dtype=1, update_mass=0, lse=None)
+             scale=0.1, softcap=0.0, q=FAKE, slopes=None, out=64 * FAKE, out_dtype=1, update_mass=0, lse=None)
     f.update(other)
     return _lib.PagedQuery(*f.values())
 
@@ -91,12 +91,15 @@ def test_attention_refusals(L):
     assert call(_pool(mass=None), update_mass=1) == _lib.ERR_INVALID_ARG
     assert call(n_q_heads=11) == call(n_q_heads=0) == call(n_q_heads=2 * 65) == _lib.ERR_SHAPE
     assert call(window=-1) == call(max_q=0) == call(max_pages=0) == call(n_seq=70000) == _lib.ERR_SHAPE
-    assert call(max_pages=1 << 27) == call(q_start=None) == call(n_rows=1 << 29) == _lib.ERR_SHAPE
+    assert call(max_pages=(1 << 26) + 1) == call(q_start=None) == call(n_rows=1 << 29) == _lib.ERR_SHAPE
     for name in ("q", "out"):
         assert call(**{name: FAKE + 8}) == _lib.ERR_ALIGN, name
     for name in ("pages", "lengths", "q_start", "slopes", "lse"):
         assert call(**{name: FAKE + 2}) == _lib.ERR_ALIGN, name
     assert call(ws=FAKE + 8) == _lib.ERR_ALIGN
+    size = 7 * 12 * 128 * 2
+    assert call(out=FAKE) == call(out=FAKE + size - 16) == call(out=FAKE - 2 * size + 16, out_dtype=0) == \
+        _lib.ERR_INVALID_ARG  # over q
     need = L.spectra_attention_paged_workspace_size(ctypes.byref(_pool()), 7, 12)
     assert need > 0 and call(wsb=need - 1) == _lib.ERR_BUFFER_TOO_SMALL
     assert L.spectra_attention_paged(None, ctypes.byref(_query()), FAKE, need, None) == _lib.ERR_INVALID_ARG
@@ -118,7 +121,7 @@ def test_evict_refusals(L):
     assert call(ws=None) == _lib.ERR_INVALID_ARG
     assert call(new=FAKE) == call(new=FAKE + 8) == call(new=FAKE - 8) == _lib.ERR_INVALID_ARG  # overlaps lengths
     assert call(budget=0) == call(recent=-1) == call(recent=51) == call(dmp=3) == call(mp=0) == _lib.ERR_SHAPE
-    assert call(dmp=0) == call(n=70000) == call(mp=1 << 27) == _lib.ERR_SHAPE
+    assert call(dmp=0) == call(n=70000) == call(mp=(1 << 26) + 1) == _lib.ERR_SHAPE
     assert call(pages=FAKE + 2) == call(dst=FAKE + 1) == call(ws=FAKE + 4) == call(new=2 * FAKE + 2) == _lib.ERR_ALIGN
     need = L.spectra_kv_evict_workspace_size(ctypes.byref(_pool()), 3, 9)
     assert need > 0 and call(wsb=need - 1) == _lib.ERR_BUFFER_TOO_SMALL

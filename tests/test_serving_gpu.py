@@ -454,6 +454,59 @@ def test_attention_streams_graphs_and_shared_workspace():
     sp.spectra_device_status()
 
 
+def test_attention_shared_pages():
+    """Two sequences over the same first pages: both see them, both add to their mass."""
+    rng = np.random.default_rng(12)
+    p, pages, free = filled(rng, [64], 2, 64, 16, spare=2)
+    for which in range(2):  # each sequence's own last page
+        x = torch.from_numpy(rng.standard_normal((2, 16, 2, 64))).to(torch.bfloat16)
+        p.append(wl.bits(x[0]), wl.bits(x[1]), np.arange(16) + int(free[which]) * 16)
+    p.mass[p.slot(token_slots(pages[0], 64, 16), 0)] = 0.0
+    p.mass[p.slot(token_slots(pages[0], 64, 16), 1)] = 0.0
+    both = np.stack([np.append(pages[0, :4], free[0]), np.append(pages[0, :4], free[1])]).astype(np.int32)
+    g = device_pool(p)
+    q = torch.from_numpy(rng.standard_normal((2, 4, 64))).to(torch.bfloat16)
+    out = sp.spectra_attention_paged(g, i32(both), i32([75, 80]), q.to(DEV), out_dtype=torch.float32, update_mass=True)
+    want, _, add, to, _, tm = ref.attention(p, both, [75, 80], q.double().numpy(), [0, 1, 2], 0.125)
+    assert (np.abs(out.double().cpu().numpy() - want) <= to + 2.0 ** -23 * np.abs(want)).all()
+    used = add > 0
+    err = np.abs(g.mass.double().cpu().numpy() - p.mass - add)[used]
+    assert (err <= (tm + 2.0 ** -22 * add)[used]).all()
+    assert add[used].sum() > 7.99
+
+
+def test_attention_wide_window_and_overlaps():
+    g, pages, q = _big(2, 500, 2, 4, 64, 16, seed=5)
+    n = i32([500, 3])
+    want = sp.spectra_attention_paged(g, pages, n, q)
+    assert torch.equal(sp.spectra_attention_paged(g, pages, n, q, window=2 ** 31 - 1), want)
+    two = torch.cat([q, q])
+    start = i32([0, 2, 4])  # a sequence of 3 positions with 2 rows, a window wider than anything
+    assert torch.equal(sp.spectra_attention_paged(g, pages, n, two, start, max_q=2, window=2 ** 31 - 1),
+                       sp.spectra_attention_paged(g, pages, n, two, start, max_q=2))
+    with pytest.raises(sp.SpectraError):
+        sp.spectra_attention_paged(g, pages, n, q, out=q)
+    with pytest.raises(ValueError, match="workspace"):
+        sp.spectra_attention_paged(g, pages, n, q, workspace=torch.empty(1 << 26, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="out"):
+        sp.spectra_attention_paged(g, pages, n, q, out_dtype=torch.float16)
+    with pytest.raises(ValueError):
+        g.read(i32([0]), out_dtype=torch.float64)
+    sp.spectra_device_status()
+
+
+def test_attention_reports_a_query_that_is_not_finite():
+    g, pages, q = _big(2, 50, 1, 2, 64, 16, seed=6)
+    good = sp.spectra_attention_paged(g, pages, i32([50, 50]), q)
+    q[0, 1, 5] = float("nan")
+    sp.spectra_device_status()
+    out = sp.spectra_attention_paged(g, pages, i32([50, 50]), q)
+    assert out[0, 1].isnan().all() and torch.equal(out[1], good[1]) and torch.equal(out[0, 0], good[0, 0])
+    with pytest.raises(sp.SpectraError) as e:
+        sp.spectra_device_status()
+    assert e.value.status == 5
+
+
 # ---------------------------------------------------------------- eviction
 
 def check_evict(rng, lengths, H, D, P, budget, recent, ties=False, bad=False):
@@ -525,6 +578,30 @@ def test_evict_long():
             keep = torch.cat([best, t[old:]])
             assert torch.equal(kk[:, h], k[keep, h]) and torch.equal(vv[:, h], v[keep, h])
             assert torch.equal(big.mass.view(-1, 2, 64)[dst[b].long(), h].flatten()[:budget], m[keep])
+
+
+def test_evict_wide_page_tables():
+    """Page tables far wider than the sequences (the unused ids are not looked at)."""
+    g, pages, _ = _big(3, 600, 2, 2, 64, 16)
+    big = sp.KVPool(2, 64, 16, g.n_pages + 6, mass=True)
+    for a, b in zip((big.k_codes, big.k_scales, big.k_zeros, big.v_codes, big.v_scales, big.v_zeros),
+                    (g.k_codes, g.k_scales, g.k_zeros, g.v_codes, g.v_scales, g.v_zeros)):
+        a[:b.numel()].copy_(b)
+    big.mass.exponential_()
+    dst = torch.arange(g.n_pages, big.n_pages, dtype=torch.int32, device=DEV).reshape(3, 2)
+    wide = torch.full((3, 60000), 2 ** 31 - 1, dtype=torch.int32, device=DEV)
+    wide[:, :pages.shape[1]] = pages
+    n = i32([600, 20, 333])
+    got = [sp.spectra_kv_evict(big, t, n, dst, 30, 7) for t in (pages, wide)]
+    assert torch.equal(*got)
+    kv = [big.read(torch.arange(g.n_pages * 16, big.n_pages * 16, dtype=torch.int32, device=DEV))]
+    big.k_codes[g.k_codes.numel():].zero_()
+    sp.spectra_kv_evict(big, wide, n, dst, 30, 7)
+    kv.append(big.read(torch.arange(g.n_pages * 16, big.n_pages * 16, dtype=torch.int32, device=DEV)))
+    keep = torch.ones(96, dtype=torch.bool)
+    keep[[30, 31] + list(range(52, 64)) + [94, 95]] = False  # past each sequence's 30, 20 and 30 entries
+    assert torch.equal(kv[0][0][keep.to(DEV)], kv[1][0][keep.to(DEV)])
+    sp.spectra_device_status()
 
 
 def test_evict_reports_pages_out_of_bounds():
