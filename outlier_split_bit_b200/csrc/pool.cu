@@ -68,8 +68,10 @@ __device__ unsigned int g_pool_error;
 // is more than q's half step, u / 16 at most.  Otherwise the double quotient
 // is taken.
 //
-// Codes, rint(v / S): q = v * (1 / S) in FP32, cut to [-32, 32] (what lies
-// beyond is cut to 0 or 15 in the end), is off by 2^-18 at most.  A true quotient
+// Codes, rint(v / S): q = v * (1 / S) in FP32 is off by 2^-18 at most where |q|
+// is 32 or less; beyond, where it may reach 15 * 2^9 (two different BF16 values
+// near v differ by 2^-8 |v| or more, and S is 1/15 of that, or half of it where S
+// is subnormal), the code is 0 or 15 either way.  A true quotient
 // that is not k + 1/2 lies 2^-12 or more from it: 2v - (2k+1)S is a multiple of
 // the smaller of S's last place (2^-10 of S or more, or S / j for a subnormal
 // S = j 2^-24) and 2v's (2^-8 of S or more, near a tie).  So 2q within 2^-12 of
@@ -78,7 +80,10 @@ __device__ unsigned int g_pool_error;
 // double quotient's result.
 constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: a float sum with it is a whole number
 
-__device__ __forceinline__ uint32_t group_scale(float lo, float hi, bool bad, float *zero_out, unsigned int *flags) {
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t x) { return *reinterpret_cast<const __nv_bfloat162 *>(&x); }
+
+__device__ __forceinline__ uint32_t group_scale(float lo, float hi, float *zero_out, unsigned int *flags) {
+    const bool bad = !(isfinite(lo) && isfinite(hi));
     const float d = hi - lo;
     unsigned short s;
     if (hi - d == lo && d + lo == hi && d < 3e38f) {
@@ -120,29 +125,30 @@ __global__ void __launch_bounds__(256) pool_append_kernel(PoolView p, const uint
 #pragma unroll
     for (int g = 0; g < G; ++g)
         raw[g] = ts >= 0 ? __ldg(reinterpret_cast<const uint4 *>(src + 32 * g)) : make_uint4(0u, 0u, 0u, 0u);
+    // minimum and maximum in BF16 pairs (of the two zeros either may come out,
+    // which makes no difference below); a NaN stays one
     float lo[G], hi[G];
-    uint32_t bad = 0;  // bit g: group g holds a NaN or infinity
 #pragma unroll
     for (int g = 0; g < G; ++g) {
         const uint32_t r4[4] = {raw[g].x, raw[g].y, raw[g].z, raw[g].w};
-        float top = 0.f;
+        __nv_bfloat162 l = as_bf162(r4[0]), u = l;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float a = __uint_as_float(r4[j] << 16) + 0.f, b = __uint_as_float(r4[j] & 0xFFFF0000u) + 0.f;
-            lo[g] = j == 0 ? fminf(a, b) : fminf(lo[g], fminf(a, b));
-            hi[g] = j == 0 ? fmaxf(a, b) : fmaxf(hi[g], fmaxf(a, b));
-            top = fmaf(a, 0.f, fmaf(b, 0.f, top));  // NaN if one of them is not finite
+        for (int j = 1; j < 4; ++j) {
+            l = __hmin2_nan(l, as_bf162(r4[j]));
+            u = __hmax2_nan(u, as_bf162(r4[j]));
         }
-        bad |= top == 0.f ? 0u : 1u << g;
-    }
+        // the two halves, then the four threads: minimum in the lower half, maximum in the upper
+        __nv_bfloat162 both = __halves2bfloat162(__hmin_nan(__low2bfloat16(l), __high2bfloat16(l)),
+                                                 __hmax_nan(__low2bfloat16(u), __high2bfloat16(u)));
 #pragma unroll
-    for (int o = 1; o <= 2; o <<= 1) {
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-            lo[g] = fminf(lo[g], __shfl_xor_sync(0xffffffffu, lo[g], o));
-            hi[g] = fmaxf(hi[g], __shfl_xor_sync(0xffffffffu, hi[g], o));
+        for (int o = 1; o <= 2; o <<= 1) {
+            const uint32_t mine = *reinterpret_cast<const uint32_t *>(&both);
+            const __nv_bfloat162 other = as_bf162(__shfl_xor_sync(0xffffffffu, mine, o));
+            both = __halves2bfloat162(__hmin_nan(__low2bfloat16(both), __low2bfloat16(other)),
+                                      __hmax_nan(__high2bfloat16(both), __high2bfloat16(other)));
         }
-        bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+        lo[g] = __low2float(both);
+        hi[g] = __high2float(both);
     }
     constexpr int kOwn = (G + 3) / 4;  // groups of a thread's own: w, w + 4
     float own_z[kOwn];
@@ -157,7 +163,7 @@ __global__ void __launch_bounds__(256) pool_append_kernel(PoolView p, const uint
                 l = lo[4 * e + j];
                 u = hi[4 * e + j];
             }
-        own_s[e] = group_scale(l, u, (bad >> (4 * e + w)) & 1u, &own_z[e], &flags);
+        own_s[e] = group_scale(l, u, &own_z[e], &flags);
     }
     if (flags && ts >= 0) atomicOr(&g_pool_error, flags);
     uint32_t word[G], sc[G], zw = 0;
@@ -173,7 +179,7 @@ __global__ void __launch_bounds__(256) pool_append_kernel(PoolView p, const uint
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float x = __uint_as_float(j & 1 ? r4[j >> 1] & 0xFFFF0000u : r4[j >> 1] << 16);
-            const float q2 = fminf(fmaxf(x * r2, -64.f), 64.f);
+            const float q2 = x * r2;
             const float near = (q2 + kMagic) - kMagic;
             const float q = (fabsf(q2 - near) < 0x1p-12f ? near : q2) * 0.5f;
             const int c = __float_as_int(q + kMagic) - __float_as_int(kMagic) + z;

@@ -70,7 +70,7 @@ struct SampleArgs {
 };
 
 struct Smem {
-    uint32_t lo[kBins], hi[kBins];   // this CTA's histogram, low and high words
+    uint32_t lo[kBins + 32], hi[kBins + 32];  // this CTA's histogram, low and high words (behind it: what does not count)
     u64 merged[kBins];               // this CTA's share of the bins, over the cluster
     u64 comp[kList], q[kList];       // gathered tokens: (key, ~index), weight
     u64 seg[kMaxSegments];
@@ -134,8 +134,7 @@ struct Weights {
 __device__ __forceinline__ void add_to(Smem &s, int bin, u64 q) {
     const uint32_t l = (uint32_t)q;
     const uint32_t old = atomicAdd(&s.lo[bin], l);
-    const uint32_t h = (uint32_t)(q >> 32) + (old + l < old);
-    if (h) atomicAdd(&s.hi[bin], h);
+    atomicAdd(&s.hi[bin], (uint32_t)(q >> 32) + (old + l < old));
 }
 
 // Over the cluster's histograms (filled, not yet synchronised), from bin 0 up:
@@ -340,8 +339,12 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
     // number of thr's own tokens (top-p after top-k), which lie last.
     auto resolve = [&](int bin, u64 need, bool by_weight, u64 tie_w) {
         const uint32_t from = thr;
+        // a look at the value first, with room for roundings
+        const float width = kReach * temp / kBins, room = 1e-3f * width + 1e-6f * (fabsf(mx) + kReach * temp);
+        const float upper = mx - (float)bin * width + room, lower = mx - (float)(bin + 1) * width - room;
+        const bool look = mx < INFINITY && upper < INFINITY && lower > -INFINITY;
         auto member = [&](float v) { return step_of(v) == bin && (from == 0 || float_key(v) > from); };
-        const int n = gather(member);
+        const int n = gather([&](float v) { return (!look || (v <= upper && v >= lower)) && member(v); });
         if (n <= kList) {
             if (rank == 0) {
                 if (tid == 0) {
@@ -469,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
         clear_bins(s);
         for_each(x, i0, i1, [&](float v, int) {
             const int b = step_of(v);
-            if (b < kBins) atomicAdd(&s.lo[b], 1u);
+            atomicAdd(&s.lo[b < kBins ? b : kBins + lane], 1u);
         });
         int bin;
         u64 above, total, unused;
@@ -493,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
         clear_bins(s);
         for_each(x, i0, i1, [&](float v, int) {
             const int b = step_of(v);
-            if (b < kBins && (thr == 0 || float_key(v) > thr)) add_to(s, b, w.fixed_near(v));
+            add_to(s, b < kBins && (thr == 0 || float_key(v) > thr) ? b : kBins + lane, w.fixed_near(v));
         });
         if (rank == 0 && tid == 0 && tie_w) add_to(s, step_of(key_float(thr)), tie_w * (u64)ties);
         int bin;
