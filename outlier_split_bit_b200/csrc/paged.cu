@@ -13,42 +13,71 @@
 //   mass[h][t] += sum over the group's heads and the tokens of softmax(s)_t.
 //
 // One pass over K and V.  A KV head's queries (tokens x group heads) are the
-// columns of a tile of 8 * NT; a warp takes 16 positions (a unit) at a time
-// and multiplies them on the tensor cores, m16n8k16 with FP32 accumulation:
-//   scores: A = 16 positions x 16 channels of K, B = q.  A code enters as the
-//     exact FP16 integer c - z (a nibble or-ed under 0x6400 is 1024 + c, or
-//     1024 + 16c where it stands, which saves the shift; one half-precision add
-//     or multiply-add takes it to c - z), a query as FP16 after a power of two
-//     that brings its row's largest value to 2^14 (BF16 has fewer bits, so only
-//     values under 2^-28 of the largest lose any).  The product sums are exact
-//     up to FP32 accumulation, and each group's is multiplied by its scale in
-//     FP32;
-//   weighted sum: A = 16 channels x 16 positions of V, dequantised to FP16 (c -
-//     z) * s with one rounding, B = the weights in FP16, scaled so that they lie
-//     under 2^15.  For a BF16 output that is enough: both roundings are 2^-11 at
-//     most, an eighth of the output's own.  For an FP32 output what the two
-//     roundings left goes in as well, as two more products (V's remainder is
-//     exact; of the weights 2^-22 is lost).  A V beyond FP16's range turns the
-//     output non-finite, which is reported.
+// columns of a tile of 8 * NT; a warp takes 16 positions (a unit) at a time, one
+// or two units a step, and multiplies them on the tensor cores, m16n8k16 with
+// FP32 accumulation:
+//   scores: A = 16 positions x 16 channels of K, B = q, as FP16 after a power of
+//     two that brings its row's largest value to 2^14 (BF16 has fewer bits, so
+//     only values under 2^-28 of the largest lose any).  The product sums are
+//     exact up to FP32 accumulation, and each group's is multiplied by its scale
+//     in FP32;
+//   weighted sum: A = 16 channels x 16 positions of V, B = the weights in FP16,
+//     scaled so that they lie under 2^15.
+// The codes enter in one of two forms:
+//   as they stand (8 columns: decode): a nibble masked in place is an FP16
+//     subnormal, one instruction for two codes.  K's zero points take one FP32
+//     multiply-add per group, z times the query's own sum over the group; V's a
+//     product of their own, and V's scale goes into the weight: w * s rounded to
+//     FP16 (to half a subnormal step, 2^-25, at least: 2^-32 of the largest weight,
+//     which is 2^7 or more).  A w * s beyond FP16 (scales over 2) is seen in the
+//     sums, and the item is run again with weights of 1 at most, which no FP16
+//     scale takes out of range;
+//   less the zero point (16 columns and more, and V for an FP32 output): a nibble
+//     or-ed under 0x6400 is 1024 + c, or 1024 + 16c where it stands, and one
+//     half-precision instruction takes it to c - z, exactly.  V is dequantised to
+//     (c - z) * s with one rounding; dearer per code, but done once for all
+//     columns, where the other form's work on weights and zero points is per
+//     column.  A V beyond FP16's range turns the output non-finite, which is
+//     reported.
+// For a BF16 output the FP16 roundings are enough: 2^-11 at most, an eighth of
+// the output's own.  For an FP32 output what the two roundings left goes in as
+// well, as two more products (V's remainder is exact; of the weights 2^-22 is
+// lost), and each unit's sum is added to the accumulator in FP32: the tensor core
+// cuts its sums off (error at 8192 positions 1.4e-6 of the largest output, with
+// the separate addition 2.4e-7).
+//
 // The scores' accumulator layout (positions in rows) is transposed into the
-// weights' operand layout inside the warp (movmatrix on the two halves of the
-// FP32 bits).  Which lane holds which channel or position is free as long as
-// both operands agree, so the pool's words are laid out to be read with one
-// load per position: lane (g, t) = (lane / 4, lane % 4) reads K's word t of
-// every group of positions g', g' + 8 and V's halfword g of every group of
-// positions t, t + 4, t + 8, t + 12.
+// weights' operand layout inside the warp (movmatrix on FP16 pairs).  Which lane
+// holds which channel or position is free as long as both operands agree, so the
+// pool's words are laid out to be read with one load per position: lane (g, t) =
+// (lane / 4, lane % 4) reads K's word t of every group of positions g', g' + 8
+// and V's halfword g of every group of positions t, t + 4, t + 8, t + 12.
 //
 // The running maximum is only a reference: it moves when a weight would pass
 // 2^15, and then to 2^7 for the largest, so most units need no reduction over
 // the lanes and no rescaling.
 //
-// Work split: the tiles (64 positions, one unit per warp) of every (sequence,
-// head, column tile) make one list, cut into equal runs, one per CTA, from
-// the lengths on the device; so ragged batches balance and the host need not
-// know the lengths.  A run's first and last piece may be part of a longer item;
-// such pieces go to the workspace (at most two per CTA) and a second kernel,
-// launched as a programmatic dependent, joins them in order.  Every order is
-// fixed, so results repeat bit for bit.
+// Each warp copies its own units into a ring of three steps in shared memory,
+// asynchronously and without the block's barriers, which only an item's end has.
+//
+// Work split: the tiles (64 positions, or 128 where a step takes two units) of
+// every (sequence, head, column tile) make one list, cut into equal runs, one per
+// CTA, from the lengths on the device; so ragged batches balance and the host
+// need not know the lengths.  A run's first and last piece may be part of a longer
+// item; such pieces go to the workspace (at most two per CTA) and a second
+// kernel, launched as a programmatic dependent, joins them in order.  Every order
+// is fixed, so results repeat bit for bit.
+//
+// Measured (B200; positions of a batch, Hq / H heads, D channels):
+//   16 sequences of 20000 to 65536 positions, 32 / 8, 128, one new token: 862 MB in
+//     186 us, 4.6 TB/s, against 134 us at the rate of a copy.  The ring alone,
+//     without the arithmetic, runs at 6.05 TB/s.  The unit's instructions bound it
+//     (some 185 of the integer and half-precision kind per unit and warp at G = 4),
+//     and the chip is at its power limit, 1.8 GHz;
+//   1 sequence of 8192, 12 / 2, 128: 13.8 us; of 300: 8.5 us, which is the two
+//     launches, the run search, the ring's first fill and the join.
+// Tried and no faster: 4 to 6 CTAs an SM with one unit a step, 4 ring steps, the
+// queries' operands in shared memory for 8 columns, 16 columns a tile where 32 fit.
 #include "internal.cuh"
 #include "pool.cuh"
 #include "select.cuh"
@@ -543,6 +572,7 @@ struct Score {
     __device__ __forceinline__ float cap_of(float y) const { return cap * tanh_abs(y); }
 };
 
+// (No pool has 2^31 units: they would be 4 TB and more.)
 constexpr uint32_t kNoUnit = 0xFFFFFFFFu, kSpecial = 0x80000000u;
 // The unit of the pool that holds positions t0 .. t0 + 15 of head h; kNoUnit
 // for a page outside the pool.  (Units number under 2^31.)
@@ -559,8 +589,8 @@ constexpr int kStages = 3;
 // A warp's way through its units of one item, U at a step: unit j of step i is
 // the positions t0 + i * kTile<U> + 16 j .. + 15.  Copies run kStages - 1 steps
 // ahead, a group each.  The bookkeeping is done 32 units at a time: a lane finds
-// one unit's place in the pool; the top bit marks a unit whose scores need more
-// than their factor (hidden positions, a page outside the pool, a cap, a bias).
+// one unit's place in the pool; the top bit marks a unit with positions that some
+// column does not see, or none does (one past the end, a page outside the pool).
 template <int G, bool V, int U>
 struct UnitRing {
     using S = Stage<G, V>;
@@ -569,19 +599,20 @@ struct UnitRing {
     const int32_t *pages;
     uint32_t first;  // the ring's address
     int h, t0, t_end, pos_lo, pos_hi, window, lane;
-    bool mark_all;
     int steps;
-    uint32_t units = 0, marks = 0, at = 0, done = 0;  // marks: bit i is that of the unit fetched i ago
+    uint32_t units = 0, before = 0;              // the units looked up last, and the 32 before those
+    uint32_t marks = 0, at = 0, done = 0;        // marks: bit i is that of the unit fetched i ago
 
     __device__ __forceinline__ int position(int f) const { return t0 + f / U * kTile<U> + f % U * kUnit; }
     __device__ __forceinline__ void look_up(int f) {
         const int t = position(f + lane);
-        units = kSpecial;  // unit 0 in the place of one that is not there, hidden whole
+        before = units;
+        units = kNoUnit;
         if (t < t_end) {
             const uint32_t unit = unit_of(p, pages[t >> p.lp], t, h);
             if (unit != kNoUnit) {
                 units = unit;
-                if (mark_all || t + kUnit - 1 > pos_lo || (window > 0 && t <= pos_hi - window)) units |= kSpecial;
+                if (t + kUnit - 1 > pos_lo || (window > 0 && t <= pos_hi - window)) units |= kSpecial;
             }
         }
     }
@@ -591,7 +622,8 @@ struct UnitRing {
 #pragma unroll
             for (int j = 0; j < U; ++j) {
                 const uint32_t unit = __shfl_sync(0xffffffffu, units, step * U + j);
-                copier.copy(dst + j * S::kBytes, unit & ~kSpecial, lane);
+                // unit 0 in the place of one that is not there
+                copier.copy(dst + j * S::kBytes, unit == kNoUnit ? 0u : unit & ~kSpecial, lane);
                 marks = __funnelshift_l(unit, marks, 1);
             }
         } else {
@@ -616,9 +648,15 @@ struct UnitRing {
         return {done};
     }
     __device__ __forceinline__ bool marked() const { return marks & (((1u << U) - 1) << ((kStages - 1) * U)); }
-    // Whether the unit at position t is not there.
-    __device__ __forceinline__ bool gone(int t) const {
-        return t >= t_end || (uint32_t)pages[t >> p.lp] >= (uint32_t)p.n_pages;
+    // Unit j of step i (the last that `next` gave): its place in the pool, or kNoUnit.
+    __device__ __forceinline__ uint32_t unit(int i, int j) const {
+        const int f = i * U + j;
+        const uint32_t u = __shfl_sync(0xffffffffu, looked_ahead(i) ? before : units, f);
+        return u == kNoUnit ? u : u & ~kSpecial;
+    }
+    // Whether the units of a later step have been looked up since step i's.
+    __device__ __forceinline__ bool looked_ahead(int i) const {
+        return ((i * U ^ min(i + kStages - 1, steps - 1) * U) & ~31) != 0;
     }
 };
 
@@ -770,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
         // FP16's range (a scale over 2: values of 30 and more).
 #pragma unroll 1
         for (int low = 0;; ++low) {
-        UnitRing<G, true, U> ring{p, copier, pages, ring_at, h, t0, t_end, pos_lo, pos_hi, a.window, lane, shaped};
+        UnitRing<G, true, U> ring{p, copier, pages, ring_at, h, t0, t_end, pos_lo, pos_hi, a.window, lane};
         ring.start();  // the first units are on their way while the queries are prepared
         if (low == 0) {
         if (lane < C) {
@@ -866,25 +904,37 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[j][nt][e] = (kRawK ? x[j][nt][e] * kRaw : x[j][nt][e]) * mul[nt][e & 1];
             }
-            const bool marked = ring.marked();
-            if (marked) {
+            if (shaped) {
 #pragma unroll
-                for (int j = 0; j < U; ++j) {
-                    const int t = t0 + i * kTile<U> + j * kUnit;
-                    const bool gone = ring.gone(t);
+                for (int j = 0; j < U; ++j)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
                             const float2 col = s_col[warp][8 * nt + 2 * t4 + e];
+                            const int gap = __float_as_int(col.x) - (t0 + i * kTile<U> + j * kUnit) - unit_position(g);
 #pragma unroll
                             for (int r = 0; r < 2; ++r) {
-                                const int gap = __float_as_int(col.x) - t - unit_position(g) - 8 * r;
-                                float v = x[j][nt][2 * r + e];
-                                if (score.capped) v = score.cap_of(v);
-                                v = fmaf(-col.y, (float)gap, v);
-                                if (gone || gap < 0 || (a.window > 0 && gap >= a.window)) v = -INFINITY;
-                                x[j][nt][2 * r + e] = v;
+                                const float v = x[j][nt][2 * r + e];
+                                x[j][nt][2 * r + e] = fmaf(-col.y, (float)(gap - 8 * r), score.capped ? score.cap_of(v) : v);
+                            }
+                        }
+            }
+            const bool marked = ring.marked();
+            if (marked) {
+#pragma unroll
+                for (int j = 0; j < U; ++j) {
+                    const int t = t0 + i * kTile<U> + j * kUnit;
+                    const bool gone = ring.unit(i, j) == kNoUnit;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int pos = __float_as_int(s_col[warp][8 * nt + 2 * t4 + e].x);
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                const int gap = pos - t - unit_position(g) - 8 * r;
+                                if (gone || gap < 0 || (a.window > 0 && gap >= a.window)) x[j][nt][2 * r + e] = -INFINITY;
                             }
                         }
                 }
@@ -931,7 +981,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
                 vu.load(at + S::vc + lo.vc, at + S::vs + lo.vs, at + S::vz + lo.vz);
                 if (marked) {
                     const int t = t0 + i * kTile<U> + j * kUnit;
-                    vu.cut_off(ring.gone(t) ? 0 : s.n - t, lane);
+                    vu.cut_off(ring.unit(i, j) == kNoUnit ? 0 : s.n - t, lane);
                 }
                 // the weights as B operands: b, and (EXACT) what its rounding left
                 uint32_t b[NT][2], rest[NT][2];
@@ -1068,7 +1118,8 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
 
 // Joins the pieces of the item that was cut at the end of run blockIdx.x, for
 // column blockIdx.y: piece 0 in that run's second place, the others in the
-// first place of the following runs.
+// first place of the following runs.  Its time is its launch's and two trips to
+// L2, whatever the pieces' number.
 template <int G, int NT, bool EXACT>
 __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedArgs a) {
     constexpr int D = 32 * G, C = 8 * NT, Q = D / 4, kSplit = kThreads / Q;  // Q threads per piece, kSplit pieces at once
@@ -1121,10 +1172,15 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedArgs a)
     }
 }
 
-// The accumulated weights, a second pass over K alone with the rows' lse: a
-// warp per unit, 8 columns at a time.  A position's sum over the columns is
-// formed in one warp, in order; it is added to the mass atomically, for the
-// pages that several sequences share.
+// The accumulated weights, a second pass over K alone with the rows' lse (the
+// weights need the whole row's sum; keeping a row's scores for it would write and
+// read 4 bytes per query head and position, where K is read again for D / 2 + D /
+// 16 per KV head): a warp per unit, 8 columns at a time.  A position's sum over
+// the columns is formed in one warp, in order; it is added to the mass
+// atomically, for the pages that several sequences share.  (Where they do, the
+// order of those additions, and so the last bit, may differ from run to run.)
+// Measured with the attention before it: 48 sequences of 1 to 6000 positions, 32 /
+// 8 heads of 128 channels, 189 MB in 81 us; bound by the same instructions.
 template <int G>
 __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 3) paged_mass_kernel(const PagedArgs a) {
     constexpr int D = 32 * G, U = units_per_step<G, 1>();
@@ -1165,16 +1221,19 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 3) paged_mass_kernel(co
             const int t_end = min((tiles.first + tb - kItemCost<U>) * kTile<U>, min(s.n, pos_hi + 1));
             int t0 = (tiles.first + max(0, ta - kItemCost<U>)) * kTile<U> + warp * (U * kUnit);
             while (t0 + U * kUnit <= vis_lo) t0 += kTile<U>;
-            UnitRing<G, false, U> ring{p, copier, pages, ring_at, h, t0, t_end, pos_lo, pos_hi, a.window, lane, shaped};
+            UnitRing<G, false, U> ring{p, copier, pages, ring_at, h, t0, t_end, pos_lo, pos_hi, a.window, lane};
             __syncwarp();  // every lane has read the ring's last unit of the columns before
             ring.start();
-            float lse2[2];
+            float lse2[2], slope[2];
+            int pos[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 // a column past the last, or one that saw nothing: weight 0
                 const int c = c0 + min(2 * t4 + e, cols - 1);
                 const float v = a.lse[(int64_t)(s.row0 + c / a.grp) * a.Hq + h * a.grp + c % a.grp] * kLog2e;
                 lse2[e] = 2 * t4 + e < cols && v != -INFINITY ? v : INFINITY;
+                pos[e] = s.n - s.m + c / a.grp;
+                slope[e] = a.slopes ? a.slopes[h * a.grp + c % a.grp] * kLog2e : 0.f;
             }
             uint4 qf[G];
             const int cg = c0 + g;
@@ -1217,24 +1276,21 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 3) paged_mass_kernel(co
                     }
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[e] = x[e] * kRaw * mul[e & 1];
-                    bool gone = false;
-                    if (marked) {
-                        gone = ring.gone(t);
+                    if (shaped) {
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int c = c0 + min(2 * t4 + e, cols - 1);
-                            const float slope = a.slopes ? a.slopes[h * a.grp + c % a.grp] * kLog2e : 0.f;
-#pragma unroll
-                            for (int r = 0; r < 2; ++r) {
-                                const int gap = s.n - s.m + c / a.grp - t - unit_position(g) - 8 * r;
-                                float v = x[2 * r + e];
-                                if (score.capped) v = score.cap_of(v);
-                                if (a.slopes) v = fmaf(-slope, (float)gap, v);
-                                if (gap < 0 || (a.window > 0 && gap >= a.window)) v = -INFINITY;
-                                x[2 * r + e] = v;
-                            }
+                        for (int e = 0; e < 4; ++e) {
+                            const int gap = pos[e & 1] - t - unit_position(g) - 4 * (e & 2);
+                            x[e] = fmaf(-slope[e & 1], (float)gap, score.capped ? score.cap_of(x[e]) : x[e]);
                         }
                     }
+                    if (marked) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int gap = pos[e & 1] - t - unit_position(g) - 4 * (e & 2);
+                            if (gap < 0 || (a.window > 0 && gap >= a.window)) x[e] = -INFINITY;
+                        }
+                    }
+                    const uint32_t unit = ring.unit(i, j);
                     float w[2];
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
@@ -1245,8 +1301,7 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 3) paged_mass_kernel(co
                     // lanes t4 = 0 and 1 add the rows g and g + 8 (an entry past the
                     // sequence is left alone: its weight is 0, its mass may be anything)
                     const int u = unit_position(g) + 8 * t4;
-                    if (t4 < 2 && t + u < s.n && !gone) {
-                        const uint32_t unit = unit_of(p, pages[t >> p.lp], t, h);
+                    if (t4 < 2 && t + u < s.n && unit != kNoUnit) {
                         atomicAdd(p.mass + (uint64_t)unit * kUnit + u, t4 ? w[1] : w[0]);
                     }
                 }
