@@ -218,7 +218,9 @@ __global__ void __launch_bounds__(256) pool_append_kernel(PoolView p, const uint
     if (w == 2 && which == 0 && p.mass) p.mass[slot] = 0.f;
 }
 
-// Token slots dequantised, four threads to a vector as above.
+// Token slots dequantised, four threads to a vector as above.  Bound by the
+// writes: 36000 tokens of 8 heads of 128 to BF16 in 31 us, 6.0 TB/s of code
+// records read and vectors written.
 template <int G, bool BF16>
 __global__ void __launch_bounds__(256) pool_read_kernel(PoolView p, const int32_t *__restrict__ slots,
                                                         uint32_t n_vectors, void *__restrict__ k_out,
@@ -286,15 +288,31 @@ __global__ void __launch_bounds__(256) pool_read_kernel(PoolView p, const int32_
 
 // ---- eviction ----
 // Two launches: select (one CTA per sequence and head) finds the smallest
-// kept key by a radix descent and, per chunk of positions, the number of kept
-// positions before it; move (a CTA per chunk or per few, launched as a
-// programmatic dependent) copies the chunk's kept entries to their places in the fresh
-// pages.  Select reads every weight once, through the page table with eight
-// look-ups in flight per thread, and keeps the keys in shared memory (of the
-// first kKeys positions; what lies past them is read again in each pass).
+// kept key and, per chunk of positions, the number of kept positions before it;
+// move (a CTA per chunk or per few, launched as a programmatic dependent) copies
+// the chunk's kept entries to their places in the fresh pages.  Select reads every
+// weight once, through the page table with eight look-ups in flight per thread,
+// and keeps the keys in shared memory (of the first kKeys positions; what lies
+// past them is read again in each pass).
+//
+// The smallest kept key is found by counting in 2048 bins over the keys' range
+// (from the smallest positive one: zeros, of positions that no query has seen,
+// would stretch it over all exponents), then in the bin it lies in; a bin of at
+// most kSelList keys is ranked all pairs.  Few keys share a bin, so the counters'
+// atomics seldom meet.
+//
+// Measured (B200): 1 sequence of 8192 positions, 2 heads of 128, 2048 kept: 15 us,
+// all of it latency (select's chain of look-ups, passes and barriers about 10); 24
+// of 5000, 8 heads, 1500 kept: 50 us for 47 MB that have to move, with the bins
+// taken from the keys' upper 11 bits 53 us (1 of 8192: 16.5; 64 of 300: 29.3
+// against 35.5).  Move reads each position's weight again, which is a page
+// look-up and a load per position, kept or not: that bounds it.
 constexpr int kSelThreads = 1024;
 constexpr int kKeys = 40960;
 constexpr int kLookUps = 8;
+constexpr int kSelList = 256;
+constexpr int kBinBits = 11;               // of kBins
+constexpr uint32_t kZeroKey = 0x80000000u;  // float_key(0)
 constexpr int kMoveChunk = 256;  // positions per chunk (= threads of a move CTA)
 
 struct EvictArgs {
@@ -338,7 +356,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) 
     extern __shared__ uint32_t keys[];
     __shared__ int hist[kBins];
     __shared__ int part[33];
-    __shared__ int s_bin, s_above;
+    __shared__ int s_bin, s_above, s_listed, s_ties;
+    __shared__ uint32_t list[kSelList], s_min, s_max, s_over_zero, s_thr;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int b = blockIdx.y, h = blockIdx.x, tid = threadIdx.x;
     const EvictPlan e = evict_plan(a, b);
@@ -347,6 +366,17 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) 
     const int64_t bh = (int64_t)b * a.p.H + h;
     if (e.need == e.old) return;  // everything stays
     const int cached = min(e.old, kKeys);
+    if (tid == 0) {
+        s_min = s_over_zero = 0xFFFFFFFFu;
+        s_max = 0;
+    }
+    __syncthreads();
+    uint32_t least = 0xFFFFFFFFu, most = 0, over_zero = 0xFFFFFFFFu;
+    auto seen = [&](uint32_t key) {
+        least = min(least, key);
+        most = max(most, key);
+        if (key > kZeroKey) over_zero = min(over_zero, key);
+    };
     for (int t0 = tid; t0 < cached; t0 += kLookUps * kSelThreads) {
         int32_t ts[kLookUps];
         float m[kLookUps];
@@ -359,32 +389,84 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) 
         for (int j = 0; j < kLookUps; ++j) m[j] = ts[j] >= 0 ? a.p.mass[a.p.slot(ts[j], h)] : 0.f;
 #pragma unroll
         for (int j = 0; j < kLookUps; ++j)
-            if (t0 + j * kSelThreads < cached) keys[t0 + j * kSelThreads] = ts[j] >= 0 ? float_key(m[j]) : 0u;
+            if (t0 + j * kSelThreads < cached) {
+                const uint32_t key = ts[j] >= 0 ? float_key(m[j]) : 0u;
+                keys[t0 + j * kSelThreads] = key;
+                seen(key);
+            }
     }
     auto key_at = [&](int t) { return t < cached ? keys[t] : evict_key(a, pages, h, t); };
-    uint32_t prefix = 0;
+    uint32_t thr = 0xFFFFFFFFu;  // no float has this key
     int need = e.need;
     if (need > 0) {
-        for (int d = 0; d < kDigits; ++d) {
+        least = __reduce_min_sync(0xffffffffu, least);
+        most = __reduce_max_sync(0xffffffffu, most);
+        over_zero = __reduce_min_sync(0xffffffffu, over_zero);
+        if ((tid & 31) == 0) {
+            atomicMin(&s_min, least);
+            atomicMax(&s_max, most);
+            atomicMin(&s_over_zero, over_zero);
+        }
+        __syncthreads();
+        // the threshold lies in [lo, hi]; bins of 2^shift keys from base to top,
+        // what lies under base in the first, over top in the last
+        const bool all = cached == e.old;
+        uint32_t lo = all ? s_min : 0, hi = all ? s_max : 0xFFFFFFFFu, top = s_max, base = min(s_over_zero, top);
+        // (the first bins, then 32 bits of a key, 11 at a time: 4 passes at most)
+        for (int pass = 0; lo < hi && pass < 5; ++pass) {
+            const int shift = max(0, 32 - kBinBits - __clz(top - base));
+            const uint32_t last = (top - base) >> shift;
             for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+            if (tid == 0) s_listed = 0;
             __syncthreads();
 #pragma unroll 4
             for (int t = tid; t < e.old; t += kSelThreads) {
                 const uint32_t key = key_at(t);
-                if (digit_in(key, prefix, d)) atomicAdd(&hist[(key >> digit_shift(d)) & digit_mask(d)], 1);
+                if (lo <= key && key <= hi) atomicAdd(&hist[key > base ? min((key - base) >> shift, last) : 0], 1);
             }
             __syncthreads();
             find_bin_from_top(hist, need, part, &s_bin, &s_above);
-            prefix |= (uint32_t)s_bin << digit_shift(d);
+            const uint32_t bin = (uint32_t)s_bin;
+            const int in_bin = hist[bin];
             need -= s_above;
+            if (bin != last) hi = base + ((bin + 1) << shift) - 1;
+            if (bin != 0) lo = base + (bin << shift);
+            base = lo;
+            top = hi;
+            if (in_bin <= kSelList) {
+                for (int t = tid; t < e.old; t += kSelThreads) {
+                    const uint32_t key = key_at(t);
+                    if (lo <= key && key <= hi) {
+                        const int at = atomicAdd(&s_listed, 1);
+                        if (at < kSelList) list[at] = key;  // always, unless the weights change meanwhile
+                    }
+                }
+                __syncthreads();
+                if (tid < in_bin) {
+                    const uint32_t key = list[tid];
+                    int over = 0, equal = 0;
+#pragma unroll 8
+                    for (int i = 0; i < in_bin; ++i) {
+                        over += list[i] > key;
+                        equal += list[i] == key;
+                    }
+                    if (over < need && need <= over + equal) {  // (equal keys write the same)
+                        s_thr = key;
+                        s_ties = need - over;
+                    }
+                }
+                __syncthreads();
+                lo = hi = s_thr;
+                need = s_ties;
+            }
             __syncthreads();
         }
+        thr = lo;
     } else {
-        prefix = 0xFFFFFFFFu;  // no float has this key
         __syncthreads();
     }
     if (tid == 0) {
-        a.thr[bh] = prefix;
+        a.thr[bh] = thr;
         a.ties[bh] = need;
     }
     // chunk totals, a warp per chunk, then their running sums
@@ -397,8 +479,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) 
         for (int i = 0; i < kMoveChunk; i += 32) {
             const int t = c * kMoveChunk + i + lane;
             const uint32_t key = t < e.old ? key_at(t) : 0u;
-            gt += __popc(__ballot_sync(0xffffffffu, t < e.old && key > prefix));
-            eq += __popc(__ballot_sync(0xffffffffu, t < e.old && key == prefix));
+            gt += __popc(__ballot_sync(0xffffffffu, t < e.old && key > thr));
+            eq += __popc(__ballot_sync(0xffffffffu, t < e.old && key == thr));
         }
         if (lane == 0) before[c] = make_int2(gt, eq);
     }
@@ -448,7 +530,9 @@ __global__ void __launch_bounds__(kMoveChunk) evict_move_kernel(EvictArgs a) {
         base = before.x + min(before.y, ties) + max(0, c * kMoveChunk - e.old);
     }
     if (keep) {
-        const int32_t td = a.p.token_slot(a.dst_pages + (int64_t)b * a.dst_max_pages, base + rank);
+        // (a place over `kept`: the weights were changed meanwhile)
+        const bool fits = (uint32_t)(base + rank) < (uint32_t)e.kept;
+        const int32_t td = fits ? a.p.token_slot(a.dst_pages + (int64_t)b * a.dst_max_pages, base + rank) : -1;
         int64_t dst = -1;
         if (src < 0 || td < 0) {
             atomicOr(&g_pool_error, 4u);

@@ -580,6 +580,49 @@ def test_evict_long():
             assert torch.equal(big.mass.view(-1, 2, 64)[dst[b].long(), h].flatten()[:budget], m[keep])
 
 
+@pytest.mark.parametrize("spread", ["equal", "zeros", "all zeros", "sink", "octaves", "two", "signs", "steps", "nan"])
+@pytest.mark.parametrize("n", [700, 45000])
+def test_evict_spreads(spread, n):
+    """Weights that share few values, or spread over the whole range of the type; past
+    the keys that the selection keeps at hand as well."""
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(n)
+    x = torch.rand(n, generator=gen, device=DEV)
+    at = torch.randperm(n, generator=gen, device=DEV)
+    m = {"equal": torch.full_like(x, 0.7), "zeros": torch.where(x < 0.6, 0.0, x), "all zeros": 0 * x,
+         "sink": x.clone(), "octaves": torch.exp2(250 * x - 126), "two": torch.where(x < 0.9, 1.0, 2.0),
+         "signs": x - 0.5, "steps": torch.floor(8 * x) * 2.0 ** -149, "nan": x.clone()}[spread]
+    if spread == "sink":
+        m[at[:2]] = 1e30
+    if spread == "nan":
+        m[at[:n // 3]] = float("nan")
+    H, D, P, budget, recent = 1, 32, 64, n // 3, 17
+    width, kept = -(-n // P), -(-budget // P)
+    g = sp.KVPool(H, D, P, width + kept, mass=True)
+    for c in (g.k_codes, g.v_codes):
+        c.random_(0, 256, generator=gen)
+    for c in (g.k_scales, g.v_scales):
+        c.fill_(0x2E66)  # 0.1
+    for c in (g.k_zeros, g.v_zeros):
+        c.fill_(8)
+    perm = torch.randperm(width + kept, generator=gen, device=DEV).to(torch.int32)
+    pages, dst = perm[None, :width].contiguous(), perm[None, width:].contiguous()
+    t, i = torch.arange(n, device=DEV), torch.arange(budget, device=DEV)
+    src = pages[0, t // P].long() * P + t % P
+    to = dst[0, i // P].long() * P + i % P
+    g.mass[src] = m
+    got = sp.spectra_kv_evict(g, pages, i32([n]), dst, budget, recent)
+    sp.spectra_device_status()
+    assert got.tolist() == [budget]
+    old = n - recent
+    key = torch.where(torch.isnan(m), -float("inf"), m)[:old]  # a NaN goes first
+    best = torch.sort(key, descending=True, stable=True).indices[:budget - recent].sort().values
+    keep = src[torch.cat([best, t[old:]])]
+    for a, b in zip(g.read(to.to(torch.int32)), g.read(keep.to(torch.int32))):
+        assert torch.equal(a, b)
+    assert torch.equal(g.mass[to].view(torch.int32), g.mass[keep].view(torch.int32))
+
+
 def test_evict_wide_page_tables():
     """Page tables far wider than the sequences (the unused ids are not looked at)."""
     g, pages, _ = _big(3, 600, 2, 2, 64, 16)
