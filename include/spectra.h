@@ -712,7 +712,7 @@ SPECTRA_API spectra_status spectra_attention_paged(const spectra_kv_pool *pool,
  */
 /* Workspace bytes; 0 for invalid arguments.  Host only. */
 SPECTRA_API size_t spectra_kv_evict_workspace_size(const spectra_kv_pool *pool, int32_t n_seq,
-                                                   int32_t max_pages);
+                                                   int32_t max_pages, int32_t budget);
 SPECTRA_API spectra_status spectra_kv_evict(const spectra_kv_pool *pool, const int32_t *pages,
                                             int32_t max_pages, const int32_t *lengths, int32_t n_seq,
                                             const int32_t *dst_pages, int32_t dst_max_pages,

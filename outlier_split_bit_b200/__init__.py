@@ -752,7 +752,7 @@ def spectra_kv_evict(pool: KVPool, pages: torch.Tensor, lengths: torch.Tensor, d
         new_lengths = torch.empty_like(lengths)
     at_new = _arg(new_lengths, "new_lengths", torch.int32, (n_seq,), dev)
     if workspace is None:
-        room = lib.spectra_kv_evict_workspace_size(pool._ref, n_seq, max_pages)
+        room = lib.spectra_kv_evict_workspace_size(pool._ref, n_seq, max_pages, budget)
         workspace = torch.empty(room or 16, dtype=torch.uint8, device=dev)
     else:
         room = _room(workspace, dev)

@@ -117,7 +117,7 @@ SIGNATURES = {
     "spectra_kv_pool_read": (ctypes.c_int, [PP, P, i32, P, P, ctypes.c_int, P]),
     "spectra_attention_paged_workspace_size": (sz, [PP, i32, i32]),
     "spectra_attention_paged": (ctypes.c_int, [PP, P, P, sz, P]),  # the query: a PagedQuery's bytes
-    "spectra_kv_evict_workspace_size": (sz, [PP, i32, i32]),
+    "spectra_kv_evict_workspace_size": (sz, [PP, i32, i32, i32]),
     "spectra_kv_evict": (ctypes.c_int, [PP, P, i32, P, i32, P, i32, i32, i32, P, P, sz, P]),
     "spectra_sample": (ctypes.c_int, [P, i32, i32, i64, P, P, P, P, P, P, P, P]),
     "spectra_trdc_write": (ctypes.c_int, [ctypes.c_char_p, i32, P, LP, P, ctypes.c_int, P, sz, P]),

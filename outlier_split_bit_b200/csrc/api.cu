@@ -657,11 +657,13 @@ spectra_status spectra_attention_paged(const spectra_kv_pool *pool, const spectr
     return launch_paged_attention(*pool, *x, workspace, (cudaStream_t)stream, dev);
 }
 
-size_t spectra_kv_evict_workspace_size(const spectra_kv_pool *pool, int32_t n_seq, int32_t max_pages) {
+size_t spectra_kv_evict_workspace_size(const spectra_kv_pool *pool, int32_t n_seq, int32_t max_pages,
+                                       int32_t budget) {
     if (!pool || check_pool_shape(pool->n_heads, pool->head_dim, pool->page_size, pool->n_pages) != SPECTRA_OK ||
-        n_seq < 0 || n_seq > 65535 || max_pages < 1 || (int64_t)max_pages * pool->page_size > ((int64_t)1 << 30))
+        n_seq < 0 || n_seq > 65535 || max_pages < 1 || budget < 1 ||
+        (int64_t)max_pages * pool->page_size > ((int64_t)1 << 30))
         return 0;
-    return evict_workspace_bytes(n_seq, pool->n_heads, (int64_t)max_pages * pool->page_size);
+    return evict_workspace_bytes(n_seq, pool->n_heads, (int64_t)max_pages * pool->page_size, budget);
 }
 
 spectra_status spectra_kv_evict(const spectra_kv_pool *pool, const int32_t *pages, int32_t max_pages,
@@ -685,7 +687,7 @@ spectra_status spectra_kv_evict(const spectra_kv_pool *pool, const int32_t *page
     if (!aligned4(pages) || !aligned4(lengths) || !aligned4(dst_pages) || !aligned4(new_lengths) ||
         !aligned16(workspace))
         return SPECTRA_ERR_ALIGN;
-    if (workspace_bytes < evict_workspace_bytes(n_seq, pool->n_heads, (int64_t)max_pages * pool->page_size))
+    if (workspace_bytes < evict_workspace_bytes(n_seq, pool->n_heads, (int64_t)max_pages * pool->page_size, budget))
         return SPECTRA_ERR_BUFFER_TOO_SMALL;
     DeviceInfo dev;
     st = current_device(&dev);

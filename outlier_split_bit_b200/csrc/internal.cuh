@@ -154,7 +154,7 @@ spectra_status launch_pool_append(const spectra_kv_pool &pool, const uint16_t *k
                                   cudaStream_t s);
 spectra_status launch_pool_read(const spectra_kv_pool &pool, const int32_t *slots, int n, void *k_out,
                                 void *v_out, bool bf16, cudaStream_t s);
-size_t evict_workspace_bytes(int n_seq, int n_heads, int64_t positions);
+size_t evict_workspace_bytes(int n_seq, int n_heads, int64_t positions, int budget);
 spectra_status launch_evict(const spectra_kv_pool &pool, const int32_t *pages, int max_pages,
                             const int32_t *lengths, int n_seq, const int32_t *dst_pages,
                             int dst_max_pages, int budget, int recent, int32_t *new_lengths, void *ws,

@@ -307,13 +307,13 @@ __global__ void __launch_bounds__(256) pool_read_kernel(PoolView p, const int32_
 // taken from the keys' upper 11 bits 53 us (1 of 8192: 16.5; 64 of 300: 29.3
 // against 35.5).  Move reads each position's weight again, which is a page
 // look-up and a load per position, kept or not: that bounds it.
-constexpr int kSelThreads = 1024;
 constexpr int kKeys = 40960;
 constexpr int kLookUps = 8;
 constexpr int kSelList = 256;
 constexpr int kBinBits = 11;               // of kBins
 constexpr uint32_t kZeroKey = 0x80000000u;  // float_key(0)
-constexpr int kMoveChunk = 256;  // positions per chunk (= threads of a move CTA)
+constexpr int kMoveThreads = 256;
+constexpr int kMoveChunk = 128;            // kept entries of a move CTA
 
 struct EvictArgs {
     PoolView p;
@@ -321,10 +321,8 @@ struct EvictArgs {
     const int32_t *dst_pages;
     const int32_t *lengths;
     int32_t *new_lengths;
-    int max_pages, dst_max_pages, budget, recent, nch;  // nch: chunks of the longest sequence
-    uint32_t *thr;   // [seq][head]: smallest kept key
-    int *ties;       // [seq][head]: kept positions with that key, the first ones
-    int2 *before;    // [seq][head][nch]: (keys above thr, keys equal to it) before the chunk
+    int max_pages, dst_max_pages, budget, recent, room;
+    int32_t *list;   // [seq][head][room]: the kept ones of the `old` positions, in order
 };
 
 // n entries, of which the last `recent` always stay and `need` of the `old`
@@ -352,11 +350,13 @@ __device__ __forceinline__ uint32_t evict_key(const EvictArgs &a, const int32_t 
     return ts < 0 ? 0u : float_key(a.p.mass[a.p.slot(ts, h)]);
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) {
+template <int T>
+__global__ void __launch_bounds__(T) evict_select_kernel(EvictArgs a) {
     extern __shared__ uint32_t keys[];
     __shared__ int hist[kBins];
     __shared__ int part[33];
     __shared__ int s_bin, s_above, s_listed, s_ties;
+    __shared__ int2 s_counts[T / 32];
     __shared__ uint32_t list[kSelList], s_min, s_max, s_over_zero, s_thr;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int b = blockIdx.y, h = blockIdx.x, tid = threadIdx.x;
@@ -377,27 +377,27 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) 
         most = max(most, key);
         if (key > kZeroKey) over_zero = min(over_zero, key);
     };
-    for (int t0 = tid; t0 < cached; t0 += kLookUps * kSelThreads) {
+    for (int t0 = tid; t0 < cached; t0 += kLookUps * T) {
         int32_t ts[kLookUps];
         float m[kLookUps];
 #pragma unroll
         for (int j = 0; j < kLookUps; ++j) {
-            const int t = t0 + j * kSelThreads;
+            const int t = t0 + j * T;
             ts[j] = t < cached ? a.p.token_slot(pages, t) : -1;
         }
 #pragma unroll
         for (int j = 0; j < kLookUps; ++j) m[j] = ts[j] >= 0 ? a.p.mass[a.p.slot(ts[j], h)] : 0.f;
 #pragma unroll
         for (int j = 0; j < kLookUps; ++j)
-            if (t0 + j * kSelThreads < cached) {
+            if (t0 + j * T < cached) {
                 const uint32_t key = ts[j] >= 0 ? float_key(m[j]) : 0u;
-                keys[t0 + j * kSelThreads] = key;
+                keys[t0 + j * T] = key;
                 seen(key);
             }
     }
     auto key_at = [&](int t) { return t < cached ? keys[t] : evict_key(a, pages, h, t); };
     uint32_t thr = 0xFFFFFFFFu;  // no float has this key
-    int need = e.need;
+    int need = e.need;  // (of the threshold's own, in the end: the first ones stay)
     if (need > 0) {
         least = __reduce_min_sync(0xffffffffu, least);
         most = __reduce_max_sync(0xffffffffu, most);
@@ -416,11 +416,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) 
         for (int pass = 0; lo < hi && pass < 5; ++pass) {
             const int shift = max(0, 32 - kBinBits - __clz(top - base));
             const uint32_t last = (top - base) >> shift;
-            for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+            for (int i = tid; i < kBins; i += T) hist[i] = 0;
             if (tid == 0) s_listed = 0;
             __syncthreads();
 #pragma unroll 4
-            for (int t = tid; t < e.old; t += kSelThreads) {
+            for (int t = tid; t < e.old; t += T) {
                 const uint32_t key = key_at(t);
                 if (lo <= key && key <= hi) atomicAdd(&hist[key > base ? min((key - base) >> shift, last) : 0], 1);
             }
@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) 
             base = lo;
             top = hi;
             if (in_bin <= kSelList) {
-                for (int t = tid; t < e.old; t += kSelThreads) {
+                for (int t = tid; t < e.old; t += T) {
                     const uint32_t key = key_at(t);
                     if (lo <= key && key <= hi) {
                         const int at = atomicAdd(&s_listed, 1);
@@ -463,94 +463,76 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictArgs a) 
         }
         thr = lo;
     } else {
-        __syncthreads();
+        return;  // the recent ones alone
     }
-    if (tid == 0) {
-        a.thr[bh] = thr;
-        a.ties[bh] = need;
-    }
-    // chunk totals, a warp per chunk, then their running sums
-    int2 *before = a.before + bh * a.nch;
+    // the list: a warp takes a part of the positions, counts its keys over the
+    // threshold and at it, and after the warps before it writes its own
+    int32_t *list_out = a.list + bh * a.room;
     const int warp = tid >> 5, lane = tid & 31;
-    const int nch = (e.n + kMoveChunk - 1) / kMoveChunk;
-    for (int c = warp; c < nch; c += kSelThreads / 32) {
-        int gt = 0, eq = 0;
-#pragma unroll
-        for (int i = 0; i < kMoveChunk; i += 32) {
-            const int t = c * kMoveChunk + i + lane;
-            const uint32_t key = t < e.old ? key_at(t) : 0u;
-            gt += __popc(__ballot_sync(0xffffffffu, t < e.old && key > thr));
-            eq += __popc(__ballot_sync(0xffffffffu, t < e.old && key == thr));
-        }
-        if (lane == 0) before[c] = make_int2(gt, eq);
+    const int per = (e.old + T - 1) / T * 32;
+    const int t0 = warp * per, t1 = min(e.old, t0 + per);
+    int over = 0, equal = 0;
+#pragma unroll 4
+    for (int t = t0; t < t1; t += 32) {
+        const uint32_t key = t + lane < t1 ? key_at(t + lane) : 0u;
+        over += __popc(__ballot_sync(0xffffffffu, t + lane < t1 && key > thr));
+        equal += __popc(__ballot_sync(0xffffffffu, t + lane < t1 && key == thr));
     }
+    if (lane == 0) s_counts[warp] = make_int2(over, equal);
     __syncthreads();
-    int carry_gt = 0, carry_eq = 0;
-    for (int c0 = 0; c0 < nch; c0 += kSelThreads) {
-        const int c = c0 + tid;
-        const int2 v = c < nch ? before[c] : make_int2(0, 0);
-        int tg, te;
-        const int g = block_exclusive(v.x, part, &tg);
-        __syncthreads();
-        const int q = block_exclusive(v.y, part, &te);
-        __syncthreads();
-        if (c < nch) before[c] = make_int2(carry_gt + g, carry_eq + q);
-        carry_gt += tg;
-        carry_eq += te;
+    const int2 all_counts = s_counts[lane];
+    over = __shfl_sync(0xffffffffu, warp_exclusive(all_counts.x, lane), warp);
+    equal = __shfl_sync(0xffffffffu, warp_exclusive(all_counts.y, lane), warp);
+    const uint32_t below = (1u << lane) - 1;
+#pragma unroll 4
+    for (int t = t0; t < t1; t += 32) {
+        const bool in = t + lane < t1;
+        const uint32_t key = in ? key_at(t + lane) : 0u;
+        const uint32_t gt = __ballot_sync(0xffffffffu, in && key > thr), eq = __ballot_sync(0xffffffffu, in && key == thr);
+        const int ties = equal + __popc(eq & below);
+        const bool keep = in && (key > thr || (key == thr && ties < need));
+        // (a place over the list's end: the weights were changed meanwhile)
+        const int place = over + __popc(gt & below) + min(ties, need);
+        if (keep && place < e.need) list_out[place] = t + lane;
+        over += __popc(gt);
+        equal += __popc(eq);
     }
 }
 
 template <int G>
-__global__ void __launch_bounds__(kMoveChunk) evict_move_kernel(EvictArgs a) {
-    __shared__ int part[33];
-    __shared__ int64_t s_src[kMoveChunk], s_dst[kMoveChunk];  // the chunk's kept entries
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictArgs a) {
+    __shared__ int64_t s_src[kMoveChunk], s_dst[kMoveChunk];
     const int b = blockIdx.z, h = blockIdx.y, tid = threadIdx.x;
     const EvictPlan e = evict_plan(a, b);
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // select's results; nothing was written before
-    for (int c = blockIdx.x; c * kMoveChunk < e.n; c += gridDim.x) {
-    const int t = c * kMoveChunk + tid;
-    const int64_t bh = (int64_t)b * a.p.H + h;
-    const int32_t ts = t < e.n ? a.p.token_slot(a.pages + (int64_t)b * a.max_pages, t) : -1;
-    const int64_t src = ts >= 0 ? a.p.slot(ts, h) : -1;
-    const float mass = src >= 0 ? a.p.mass[src] : 0.f;
-    const bool old = t < e.old;
-    bool keep = t < e.n;
-    int base = c * kMoveChunk, rank = tid, total = min(kMoveChunk, e.n - c * kMoveChunk);
-    if (e.need != e.old) {
-        const uint32_t thr = a.thr[bh];
-        const int ties = a.ties[bh];
-        const int2 before = a.before[bh * a.nch + c];
-        const uint32_t key = old && src >= 0 ? float_key(mass) : 0u;
-        const int eq = before.y + block_exclusive((int)(old && key == thr), part, &total);
-        __syncthreads();
-        keep = t < e.n && (!old || key > thr || (key == thr && eq < ties));
-        rank = block_exclusive((int)keep, part, &total);
-        // kept before the chunk: keys above the threshold, the first ties, and
-        // (in the last chunks) entries past `old`
-        base = before.x + min(before.y, ties) + max(0, c * kMoveChunk - e.old);
-    }
-    if (keep) {
-        // (a place over `kept`: the weights were changed meanwhile)
-        const bool fits = (uint32_t)(base + rank) < (uint32_t)e.kept;
-        const int32_t td = fits ? a.p.token_slot(a.dst_pages + (int64_t)b * a.dst_max_pages, base + rank) : -1;
-        int64_t dst = -1;
-        if (src < 0 || td < 0) {
+    const int32_t *src_pages = a.pages + (int64_t)b * a.max_pages, *dst_pages = a.dst_pages + (int64_t)b * a.dst_max_pages;
+    const int32_t *list = a.list + ((int64_t)b * a.p.H + h) * a.room;
+    for (int r0 = blockIdx.x * kMoveChunk; r0 < e.kept; r0 += gridDim.x * kMoveChunk) {
+    const int rank = r0 + tid, total = min(kMoveChunk, e.kept - r0);
+    const int32_t td = tid < total ? a.p.token_slot(dst_pages, rank) : -1;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // select's lists; nothing was written before
+    if (tid < total) {
+        int t = rank;  // everything stays
+        if (e.need != e.old) t = rank < e.need ? list[rank] : e.old + rank - e.need;
+        const int32_t ts = (uint32_t)t < (uint32_t)e.n ? a.p.token_slot(src_pages, t) : -1;
+        int64_t src = -1, dst = -1;
+        if (ts < 0 || td < 0) {
             atomicOr(&g_pool_error, 4u);
         } else {
+            src = a.p.slot(ts, h);
             dst = a.p.slot(td, h);
             a.p.kz[dst] = a.p.kz[src];
             a.p.vz[dst] = a.p.vz[src];
-            a.p.mass[dst] = mass;
+            a.p.mass[dst] = a.p.mass[src];
         }
-        s_src[rank] = src;
-        s_dst[rank] = dst;
+        s_src[tid] = src;
+        s_dst[tid] = dst;
     }
     __syncthreads();
     // code records, G 16-byte pieces of K and of V, and scales: neighbouring
     // threads on neighbouring pieces of an entry
     uint4 *kc = reinterpret_cast<uint4 *>(a.p.kc), *vc = reinterpret_cast<uint4 *>(a.p.vc);
 #pragma unroll 2
-    for (int i = tid; i < total * G; i += kMoveChunk) {
+    for (int i = tid; i < total * G; i += kMoveThreads) {
         const int s = i / G, g = i - s * G;
         const int64_t from = s_src[s] * G + g, to = s_dst[s] * G + g;
         if (to >= 0) {
@@ -565,8 +547,6 @@ __global__ void __launch_bounds__(kMoveChunk) evict_move_kernel(EvictArgs a) {
     __syncthreads();
     }
 }
-
-int64_t evict_chunks(int64_t positions) { return cdiv(positions, kMoveChunk); }
 
 }  // namespace
 
@@ -608,9 +588,8 @@ spectra_status launch_pool_read(const spectra_kv_pool &pool, const int32_t *slot
     return cudaGetLastError() == cudaSuccess ? SPECTRA_OK : SPECTRA_ERR_CUDA;
 }
 
-size_t evict_workspace_bytes(int n_seq, int n_heads, int64_t positions) {
-    const size_t bh = (size_t)n_seq * n_heads;
-    return bh * 8 + bh * (size_t)evict_chunks(positions) * sizeof(int2) + 8;
+size_t evict_workspace_bytes(int n_seq, int n_heads, int64_t positions, int budget) {
+    return (size_t)n_seq * n_heads * (size_t)(positions < budget ? positions : budget) * 4 + 16;
 }
 
 spectra_status launch_evict(const spectra_kv_pool &pool, const int32_t *pages, int max_pages,
@@ -627,25 +606,34 @@ spectra_status launch_evict(const spectra_kv_pool &pool, const int32_t *pages, i
     a.dst_max_pages = dst_max_pages;
     a.budget = budget;
     a.recent = recent;
-    a.nch = (int)evict_chunks((int64_t)max_pages << a.p.lp);
-    const size_t bh = (size_t)n_seq * a.p.H;
-    a.before = static_cast<int2 *>(ws);
-    a.thr = reinterpret_cast<uint32_t *>(a.before + bh * a.nch);
-    a.ties = reinterpret_cast<int *>(a.thr + bh);
     const int64_t longest = (int64_t)max_pages << a.p.lp;
+    a.room = (int)(longest < budget ? longest : budget);
+    a.list = static_cast<int32_t *>(ws);
     const size_t smem = (size_t)(longest < kKeys ? longest : kKeys) * 4;
-    static std::atomic<uint64_t> ready{0};
-    if (allow_smem((const void *)evict_select_kernel, kKeys * 4, dev, &ready) != cudaSuccess) return SPECTRA_ERR_CUDA;
-    evict_select_kernel<<<dim3((unsigned)a.p.H, (unsigned)n_seq), kSelThreads, smem, s>>>(a);
+    // Threads: one row's chain of passes is shorter with more; with more rows than
+    // SMs, smaller CTAs share an SM (24 sequences of 5000, 8 heads: 43 us with 1024,
+    // 41 with 512; 1 of 8192: 14.9 and 17.7).
+    const dim3 grid((unsigned)a.p.H, (unsigned)n_seq);
+    if ((int64_t)n_seq * a.p.H <= dev.sm_count) {
+        static std::atomic<uint64_t> ready{0};
+        if (allow_smem((const void *)evict_select_kernel<1024>, kKeys * 4, dev, &ready) != cudaSuccess)
+            return SPECTRA_ERR_CUDA;
+        evict_select_kernel<1024><<<grid, 1024, smem, s>>>(a);
+    } else {
+        static std::atomic<uint64_t> ready{0};
+        if (allow_smem((const void *)evict_select_kernel<512>, kKeys * 4, dev, &ready) != cudaSuccess)
+            return SPECTRA_ERR_CUDA;
+        evict_select_kernel<512><<<grid, 512, smem, s>>>(a);
+    }
     if (cudaGetLastError() != cudaSuccess) return SPECTRA_ERR_CUDA;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    // a few waves of CTAs at most, however wide the page tables are
-    const int64_t per_head = cdiv((int64_t)dev.sm_count * 32, (int64_t)bh);
-    cfg.gridDim = dim3((unsigned)(per_head < a.nch ? per_head : a.nch), (unsigned)a.p.H, (unsigned)n_seq);
-    cfg.blockDim = dim3(kMoveChunk, 1, 1);
+    // a few waves of CTAs at most, however large the budget is
+    const int64_t chunks = cdiv(a.room, kMoveChunk), per_head = cdiv((int64_t)dev.sm_count * 32, (int64_t)n_seq * a.p.H);
+    cfg.gridDim = dim3((unsigned)(per_head < chunks ? per_head : chunks), (unsigned)a.p.H, (unsigned)n_seq);
+    cfg.blockDim = dim3(kMoveThreads, 1, 1);
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;

@@ -123,9 +123,10 @@ def test_evict_refusals(L):
     assert call(budget=0) == call(recent=-1) == call(recent=51) == call(dmp=3) == call(mp=0) == _lib.ERR_SHAPE
     assert call(dmp=0) == call(n=70000) == call(mp=(1 << 26) + 1) == _lib.ERR_SHAPE
     assert call(pages=FAKE + 2) == call(dst=FAKE + 1) == call(ws=FAKE + 4) == call(new=2 * FAKE + 2) == _lib.ERR_ALIGN
-    need = L.spectra_kv_evict_workspace_size(ctypes.byref(_pool()), 3, 9)
+    need = L.spectra_kv_evict_workspace_size(ctypes.byref(_pool()), 3, 9, 50)
     assert need > 0 and call(wsb=need - 1) == _lib.ERR_BUFFER_TOO_SMALL
-    assert L.spectra_kv_evict_workspace_size(ctypes.byref(_pool()), 3, 0) == 0
+    assert L.spectra_kv_evict_workspace_size(ctypes.byref(_pool()), 3, 0, 50) == 0
+    assert L.spectra_kv_evict_workspace_size(ctypes.byref(_pool()), 3, 9, 0) == 0
 
 
 def test_sample_refusals(L):
