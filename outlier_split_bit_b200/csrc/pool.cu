@@ -78,6 +78,10 @@ __device__ unsigned int g_pool_error;
 // a whole number means that 2v / S is that number, or near an even one, where
 // it makes no difference; q is set to it, and rounding half to even gives the
 // double quotient's result.
+//
+// Measured (B200): 8192 tokens of 8 heads of 128, K and V, 33.5 MB read and 10.5
+// written, 13 us, 3.4 TB/s, bound by the codec's instructions (minima and maxima in
+// FP32 instead of BF16 pairs: 16 us); one token of 2 heads 2.3 us, its launch.
 constexpr float kMagic = 12582912.f;  // 1.5 * 2^23: a float sum with it is a whole number
 
 __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t x) { return *reinterpret_cast<const __nv_bfloat162 *>(&x); }
@@ -219,8 +223,8 @@ __global__ void __launch_bounds__(256) pool_append_kernel(PoolView p, const uint
 }
 
 // Token slots dequantised, four threads to a vector as above.  Bound by the
-// writes: 36000 tokens of 8 heads of 128 to BF16 in 31 us, 6.0 TB/s of code
-// records read and vectors written.
+// writes: 36000 tokens of 8 heads of 128 to BF16 in 31 us, 44 MB of records read
+// and 147 written.
 template <int G, bool BF16>
 __global__ void __launch_bounds__(256) pool_read_kernel(PoolView p, const int32_t *__restrict__ slots,
                                                         uint32_t n_vectors, void *__restrict__ k_out,
@@ -287,27 +291,27 @@ __global__ void __launch_bounds__(256) pool_read_kernel(PoolView p, const int32_
 }
 
 // ---- eviction ----
-// Two launches: select (one CTA per sequence and head) finds the smallest
-// kept key and, per chunk of positions, the number of kept positions before it;
-// move (a CTA per chunk or per few, launched as a programmatic dependent) copies
-// the chunk's kept entries to their places in the fresh pages.  Select reads every
-// weight once, through the page table with eight look-ups in flight per thread,
-// and keeps the keys in shared memory (of the first kKeys positions; what lies
-// past them is read again in each pass).
+// Two launches: select (one CTA per sequence and head) finds the smallest kept
+// key and lists the kept positions; move (launched as a programmatic dependent)
+// copies their entries to the fresh pages, an entry's pieces by neighbouring
+// threads.  Select reads every weight once, through the page table with eight
+// look-ups in flight per thread, and keeps the keys in shared memory (of the first
+// kKeys positions; what lies past them is read again in each pass).
 //
 // The smallest kept key is found by counting in 2048 bins over the keys' range
 // (from the smallest positive one: zeros, of positions that no query has seen,
 // would stretch it over all exponents), then in the bin it lies in; a bin of at
 // most kSelList keys is ranked all pairs.  Few keys share a bin, so the counters'
-// atomics seldom meet.
+// atomics seldom meet (with the key's upper 11 bits as the bin, and three passes: 53
+// us where this takes 50).
 //
 // Measured (B200): 1 sequence of 8192 positions, 2 heads of 128, 2048 kept: 15 us,
-// all of it latency (select's chain of look-ups, passes and barriers about 10); 24
-// of 5000, 8 heads, 1500 kept: 50 us for 47 MB that have to move, with the bins
-// taken from the keys' upper 11 bits 53 us (1 of 8192: 16.5; 64 of 300: 29.3
-// against 35.5).  Move reads each position's weight again, which is a page
-// look-up and a load per position, kept or not: that bounds it.
-constexpr int kKeys = 40960;
+// latency (select's chain of look-ups, passes and barriers is 10 of them).  24 of
+// 5000, 8 heads, 1500 kept: 38 us; move takes 22 of them for 90 MB read (45 of
+// entries: an entry's scales, zero points and weight fill 36 of the 160 bytes in
+// their sectors) and 45 MB written, 6.1 TB/s, select the rest.  Without the list,
+// move looking at every position's weight again: 50 us.
+constexpr int kKeys = 55296;  // 216 KB of an SM's 227
 constexpr int kLookUps = 8;
 constexpr int kSelList = 256;
 constexpr int kBinBits = 11;               // of kBins
@@ -611,10 +615,10 @@ spectra_status launch_evict(const spectra_kv_pool &pool, const int32_t *pages, i
     a.list = static_cast<int32_t *>(ws);
     const size_t smem = (size_t)(longest < kKeys ? longest : kKeys) * 4;
     // Threads: one row's chain of passes is shorter with more; with more rows than
-    // SMs, smaller CTAs share an SM (24 sequences of 5000, 8 heads: 43 us with 1024,
-    // 41 with 512; 1 of 8192: 14.9 and 17.7).
+    // SMs, smaller CTAs share an SM where their keys leave room (24 sequences of 5000,
+    // 8 heads: 43 us with 1024, 38 with 512; 1 of 8192: 14.9 and 17.7).
     const dim3 grid((unsigned)a.p.H, (unsigned)n_seq);
-    if ((int64_t)n_seq * a.p.H <= dev.sm_count) {
+    if ((int64_t)n_seq * a.p.H <= dev.sm_count || smem > 100 * 1024) {
         static std::atomic<uint64_t> ready{0};
         if (allow_smem((const void *)evict_select_kernel<1024>, kKeys * 4, dev, &ready) != cudaSuccess)
             return SPECTRA_ERR_CUDA;

@@ -13,7 +13,8 @@
 // top-p, finds the threshold's step; the few tokens in it are gathered and
 // ranked against one another.  A step that holds too many of them (equal
 // logits, say) is divided by the digits of the order-preserving key instead.
-// A top-k of up to 512 gathers all that it keeps and ends in one CTA.
+// Where what a row keeps fits a list of 512 (a small top-k, a min-p that leaves few)
+// it is gathered whole and the row ends in one CTA of the cluster.
 //
 // Weights are 64-bit fixed point, w * 2^44 rounded from a double: integer sums
 // do not depend on their order, so the histograms use atomics and the row
@@ -24,6 +25,13 @@
 // wave; a CTA takes a contiguous part of the row, reads it from memory once
 // (the maximum) and from L2 after that, and exchanges maxima, histograms and
 // sums with its cluster through distributed shared memory.
+//
+// Measured (B200): 1 row of 131072 logits, top-k 50 then top-p: 16 us, a chain of
+// passes, cluster barriers and remote reads (histogram and its search 6, the list's
+// end 3), where the row's bytes would take 0.1.  64 rows of 131071, top-p and
+// min-p: 57 us against 5 for the bytes: every weight in reach is an exponential in
+// FP64 (some 12 FP64 instructions) and two shared atomics, of which the one and
+// the other take about half.  By counts alone (top-k 50): 25 us.
 #include <cooperative_groups.h>
 
 #include "internal.cuh"

@@ -581,7 +581,7 @@ def test_evict_long():
 
 
 @pytest.mark.parametrize("spread", ["equal", "zeros", "all zeros", "sink", "octaves", "two", "signs", "steps", "nan"])
-@pytest.mark.parametrize("n", [700, 45000])
+@pytest.mark.parametrize("n", [700, 60000])
 def test_evict_spreads(spread, n):
     """Weights that share few values, or spread over the whole range of the type; past
     the keys that the selection keeps at hand as well."""
