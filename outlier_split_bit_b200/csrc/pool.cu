@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(T) evict_select_kernel(EvictArgs a) {
     }
     if (lane == 0) s_counts[warp] = make_int2(over, equal);
     __syncthreads();
-    const int2 all_counts = s_counts[lane];
+    const int2 all_counts = lane < T / 32 ? s_counts[lane] : make_int2(0, 0);
     over = __shfl_sync(0xffffffffu, warp_exclusive(all_counts.x, lane), warp);
     equal = __shfl_sync(0xffffffffu, warp_exclusive(all_counts.y, lane), warp);
     const uint32_t below = (1u << lane) - 1;

@@ -552,6 +552,14 @@ def test_evict_shapes(H, D, P):
     check_evict(np.random.default_rng(D), [90, 150], H, D, P, 70, 5)
 
 
+@pytest.mark.parametrize("kind", ["plain", "ties", "bad"])
+def test_evict_many(kind):
+    """More rows than the GPU has processors, some without an entry."""
+    rng = np.random.default_rng(41)
+    lengths = [0, 900, 1, 300] + [int(x) for x in rng.integers(1, 700, 37)]
+    check_evict(rng, lengths, 4, 32, 16, 120, 9, kind == "ties", kind == "bad")
+
+
 def test_evict_long():
     """A long sequence on the GPU alone: the entries that stay, by a stable sort."""
     g, pages, _ = _big(2, 30000, 2, 2, 64, 64)
