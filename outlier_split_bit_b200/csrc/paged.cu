@@ -74,7 +74,7 @@
 //     without the arithmetic, runs at 6.05 TB/s.  The unit's instructions bound it
 //     (some 185 of the integer and half-precision kind per unit and warp at G = 4),
 //     and the chip is at its power limit, 1.8 GHz;
-//   1 sequence of 8192, 12 / 2, 128: 13.8 us; of 300: 8.5 us, which is the two
+//   1 sequence of 8192, 12 / 2, 128: 10.1 us; of 300: 8.7 us, which is the two
 //     launches, the run search, the ring's first fill and the join.
 // Tried and no faster: 4 to 6 CTAs an SM with one unit a step, 4 ring steps, the
 // queries' operands in shared memory for 8 columns, 16 columns a tile where 32 fit.
@@ -1116,47 +1116,122 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
     if (tid == 0) a.ws_item[blockIdx.x] = cut;
 }
 
-// Joins the pieces of the item that was cut at the end of run blockIdx.x, for
-// column blockIdx.y: piece 0 in that run's second place, the others in the
-// first place of the following runs.  Its time is its launch's and two trips to
-// L2, whatever the pieces' number.
-template <int G, int NT, bool EXACT>
-__global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedArgs a) {
-    constexpr int D = 32 * G, C = 8 * NT, Q = D / 4, kSplit = kThreads / Q;  // Q threads per piece, kSplit pieces at once
-    __shared__ float4 s_v[kThreads];
+// Joins the pieces of the item that was cut at the end of run blockIdx.x: piece 0
+// in that run's second place, the others in the first place of the following runs.
+// Of few pieces (a batch: most items lie in one run or two) each thread joins four
+// channels of a column, with all its loads in flight; of many (a long sequence) a
+// CTA takes a column, its threads the pieces side by side, and the first loads of
+// the sums do not wait for the weights.  LONG: for few items in many runs, the
+// second form alone (a smaller kernel starts sooner: 1 sequence of 300 positions
+// 8.6 us instead of 9.9 with both).  Bound by its launch and the trips to L2.
+constexpr int kJoinThreads = 128, kFewPieces = 4;
+template <int G, int NT, bool EXACT, bool LONG>
+__global__ void __launch_bounds__(kJoinThreads, LONG ? 7 : 8) paged_join_kernel(const PagedArgs a) {
+    constexpr int D = 32 * G, C = 8 * NT, Q = D / 4, kSplit = kJoinThreads / Q;  // Q threads per piece, kSplit pieces at once
+    constexpr int kAhead = 8, kW = kJoinThreads / 32;
+    __shared__ float4 s_v[kJoinThreads];
+    __shared__ float s_f[kMaxCtas], s_m[kW], s_l[kW];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 cut = a.ws_item[blockIdx.x];
-    const int c0 = cut.z & 0xFFFFFF, cols = cut.z >> 24, c = blockIdx.y;
-    if (cut.x < 0 || c >= cols) return;
+    const int c0 = cut.z & 0xFFFFFF, cols = cut.z >> 24;
+    if (cut.x < 0) return;
     const int np = cut.x - (int)blockIdx.x + 1;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto finish = [&](int c, int d, const float4 &v, float m, float l) {
+        const int h = cut.w;
+        const int64_t row = (int64_t)(cut.y + (c0 + c) / a.grp) * a.Hq + h * a.grp + (c0 + c) % a.grp;
+        store_out<EXACT>(a, row * D + d, v, l);
+        if (d == 0 && a.lse) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    };
+    if (!LONG && np <= kFewPieces) {
+        for (int i = blockIdx.y * kJoinThreads + tid; i < cols * Q; i += gridDim.y * kJoinThreads) {
+            const int c = i / Q, d = 4 * (i - c * Q);
+            float2 x[kFewPieces];
+            float4 u[kFewPieces];
+            float m = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int k = 0; k < kFewPieces; ++k) {
+                const int64_t at = (2 * ((int64_t)blockIdx.x + k) + (k == 0)) * C + c;
+                x[k] = k < np ? a.ws_ml[at] : make_float2(-INFINITY, 0.f);
+                u[k] = k < np ? *reinterpret_cast<const float4 *>(a.ws_acc + at * D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+            for (int k = 0; k < kFewPieces; ++k) m = fmaxf(m, x[k].x);
+            const float mm = m == -INFINITY ? 0.f : m;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kFewPieces; ++k) {
+                const float f = ex2(x[k].x - mm);
+                l = fmaf(f, x[k].y, l);
+                v.x = fmaf(f, u[k].x, v.x);
+                v.y = fmaf(f, u[k].y, v.y);
+                v.z = fmaf(f, u[k].z, v.z);
+                v.w = fmaf(f, u[k].w, v.w);
+            }
+            finish(c, d, v, m, l);
+        }
+        return;
+    }
+    // (a turn's shared values are last read before the next turn's second barrier)
+    for (int c = blockIdx.y; c < cols; c += gridDim.y) {
     auto at = [&](int i) -> int64_t { return (2 * ((int64_t)blockIdx.x + i) + (i == 0)) * C + c; };
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int part = tid / Q, d = 4 * (tid - part * Q);
+    const bool summing = part < kSplit;
+    // the first pieces' sums are on their way while the weights are found
+    float4 ahead[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+        const int i = part + j * kSplit;
+        if (summing && i < np) ahead[j] = *reinterpret_cast<const float4 *>(a.ws_acc + at(i) * D + d);
+    }
+    constexpr int kOwn = (kMaxCtas + kJoinThreads - 1) / kJoinThreads;
+    float2 own[kOwn];
     float m = -INFINITY;
-    for (int i = lane; i < np; i += 32) m = fmaxf(m, a.ws_ml[at(i)].x);
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+        const int i = tid + j * kJoinThreads;
+        own[j] = i < np ? a.ws_ml[at(i)] : make_float2(-INFINITY, 0.f);
+        m = fmaxf(m, own[j].x);
+    }
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) s_m[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kW; ++w) m = fmaxf(m, s_m[w]);
     const float mm = m == -INFINITY ? 0.f : m;
     float l = 0.f;
-    for (int i = lane; i < np; i += 32) {
-        const float2 x = a.ws_ml[at(i)];
-        l = fmaf(ex2(x.x - mm), x.y, l);
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j) {
+        const int i = tid + j * kJoinThreads;
+        const float f = ex2(own[j].x - mm);
+        if (i < np) s_f[i] = f;
+        l = fmaf(f, own[j].y, l);
     }
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    const int part = tid / Q, d = 4 * (tid - part * Q);
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (part < kSplit) {
+    auto add = [&](int i, const float4 &u) {
+        const float f = s_f[i];
+        v.x = fmaf(f, u.x, v.x);
+        v.y = fmaf(f, u.y, v.y);
+        v.z = fmaf(f, u.z, v.z);
+        v.w = fmaf(f, u.w, v.w);
+    };
+    if (summing) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+            if (part + j * kSplit < np) add(part + j * kSplit, ahead[j]);
 #pragma unroll 8
-        for (int i = part; i < np; i += kSplit) {
-            const float f = ex2(a.ws_ml[at(i)].x - mm);
-            const float4 u = *reinterpret_cast<const float4 *>(a.ws_acc + at(i) * D + d);
-            v.x = fmaf(f, u.x, v.x);
-            v.y = fmaf(f, u.y, v.y);
-            v.z = fmaf(f, u.z, v.z);
-            v.w = fmaf(f, u.w, v.w);
-        }
+        for (int i = part + kAhead * kSplit; i < np; i += kSplit)
+            add(i, *reinterpret_cast<const float4 *>(a.ws_acc + at(i) * D + d));
     }
     s_v[tid] = v;
     __syncthreads();
     if (tid < Q) {
+        l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kW; ++w) l += s_l[w];
 #pragma unroll
         for (int k = 1; k < kSplit; ++k) {
             const float4 u = s_v[k * Q + tid];
@@ -1165,10 +1240,9 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedArgs a)
             v.z += u.z;
             v.w += u.w;
         }
-        const int h = cut.w;
-        const int64_t row = (int64_t)(cut.y + (c0 + c) / a.grp) * a.Hq + h * a.grp + (c0 + c) % a.grp;
-        store_out<EXACT>(a, row * D + d, v, l);
-        if (d == 0 && a.lse) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        finish(c, d, v, m, l);
+    }
+    if (LONG) break;  // a CTA for every column
     }
 }
 
@@ -1180,7 +1254,7 @@ __global__ void __launch_bounds__(kThreads) paged_join_kernel(const PagedArgs a)
 // atomically, for the pages that several sequences share.  (Where they do, the
 // order of those additions, and so the last bit, may differ from run to run.)
 // Measured with the attention before it: 48 sequences of 1 to 6000 positions, 32 /
-// 8 heads of 128 channels, 189 MB in 81 us; bound by the same instructions.
+// 8 heads of 128 channels, 189 MB in 82 us; bound by the same instructions.
 template <int G>
 __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 3) paged_mass_kernel(const PagedArgs a) {
     constexpr int D = 32 * G, U = units_per_step<G, 1>();
@@ -1336,13 +1410,14 @@ struct Workspace {
 };
 
 template <class... A>
-cudaError_t launch(void (*kernel)(A...), dim3 grid, size_t smem, bool dependent, cudaStream_t s, const PagedArgs &a) {
+cudaError_t launch(void (*kernel)(A...), dim3 grid, int threads, size_t smem, bool dependent, cudaStream_t s,
+                   const PagedArgs &a) {
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = &attr;
@@ -1367,13 +1442,23 @@ cudaError_t run_attention(const PagedArgs &a, const DeviceInfo &dev, bool mass, 
         return (unsigned)(items * each < most ? items * each : most);
     };
     const unsigned grid = runs(heads * n_ct, min_ctas<G, NT>(), units_per_step<G, NT>());
-    e = launch(paged_attention_kernel<G, NT, EXACT>, dim3(grid), smem, false, s, a);
+    e = launch(paged_attention_kernel<G, NT, EXACT>, dim3(grid), kThreads, smem, false, s, a);
     if (e != cudaSuccess) return e;
-    e = launch(paged_join_kernel<G, NT, EXACT>, dim3(grid, (unsigned)(cols < C ? cols : C)), 0, true, s, a);
+    // the join's CTAs for a run's cut item: one a column where few items make many
+    // runs (an item in four at least, on the average), else fewer (12 sequences of 16
+    // tokens, 32 columns a tile: 78 us with 10 CTAs, 83 with 32)
+    const int64_t item_cols = cols < C ? cols : C;
+    if (heads * n_ct * 4 <= grid) {
+        e = launch(paged_join_kernel<G, NT, EXACT, true>, dim3(grid, (unsigned)item_cols), kJoinThreads, 0, true, s, a);
+    } else {
+        const unsigned y = (unsigned)(item_cols < 2 * NT + 2 ? item_cols : 2 * NT + 2);
+        e = launch(paged_join_kernel<G, NT, EXACT, false>, dim3(grid, y), kJoinThreads, 0, true, s, a);
+    }
     if (e != cudaSuccess || !mass) return e;
     constexpr int mass_smem = kWarps * kStages * units_per_step<G, 1>() * Stage<G, false>::kBytes;
     static_assert(mass_smem <= 46 * 1024, "fits without asking for more");
-    return launch(paged_mass_kernel<G>, dim3(runs(heads, G <= 4 ? 4 : 3, units_per_step<G, 1>())), mass_smem, true, s, a);
+    return launch(paged_mass_kernel<G>, dim3(runs(heads, G <= 4 ? 4 : 3, units_per_step<G, 1>())), kThreads, mass_smem, true, s,
+                  a);
 }
 
 template <int G, bool EXACT>

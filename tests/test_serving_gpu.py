@@ -352,6 +352,20 @@ def test_long_and_many(n_seq, length, H, Hq, D, P):
     assert ((lse - wl_).abs() <= 2.0 ** -14).all()
 
 
+@pytest.mark.parametrize("H,Hq,D,P", [(2, 16, 128, 64), (1, 3, 64, 16), (3, 48, 96, 32)])
+def test_one_long_among_many(H, Hq, D, P):
+    """A sequence that fills most runs between ones of a few positions."""
+    n_seq, long = 130, 12000
+    g, pages, q = _big(n_seq, long, H, Hq, D, P)
+    lengths = [1 + 7 * b % 90 for b in range(n_seq)]
+    lengths[70] = long
+    out, lse = sp.spectra_attention_paged(g, pages, i32(lengths), q, out_dtype=torch.float32, want_lse=True)
+    want, wl_ = _plain_rows(g, pages, q, lengths, D ** -0.5)
+    # as above
+    assert ((out - want).norm(dim=-1) <= 2.0 ** -14 * want.norm(dim=-1)).all()
+    assert ((lse - wl_).abs() <= 2.0 ** -14).all()
+
+
 def test_offsets_past_32_bits():
     """Entries whose code words lie more than 2^31 words into the pool."""
     H, D, P = 8, 128, 1024
