@@ -70,7 +70,7 @@
 //
 // Measured (B200; positions of a batch, Hq / H heads, D channels):
 //   16 sequences of 20000 to 65536 positions, 32 / 8, 128, one new token: 862 MB in
-//     186 us, 4.6 TB/s, against 134 us at the rate of a copy.  The ring alone,
+//     188 us, 4.6 TB/s, against 134 us at the rate of a copy.  The ring alone,
 //     without the arithmetic, runs at 6.05 TB/s.  The unit's instructions bound it
 //     (some 185 of the integer and half-precision kind per unit and warp at G = 4),
 //     and the chip is at its power limit, 1.8 GHz;
