@@ -34,6 +34,8 @@
 // the other take about half.  By counts alone (top-k 50): 25 us.
 #include <cooperative_groups.h>
 
+#include <utility>
+
 #include "internal.cuh"
 #include "select.cuh"
 
@@ -476,6 +478,14 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
             if (run <= target && target < run + own) choose((int)(0xFFFFFFFFu - (uint32_t)mine), left);
         }
     };
+    // The row's end in rank 0's list: the other CTAs have read its counter, which
+    // lies in rank 0's memory, when they arrive at the barrier, and rank 0 leaves
+    // only after that.  It arrives before its own work, so nobody waits for that.
+    auto end_row = [&](int n, int most, u64 need) {
+        auto read = cl.barrier_arrive();
+        if (rank == 0) finish(n, most, need);
+        cl.barrier_wait(std::move(read));
+    };
     if (k > 0 && k < a.vocab) {
         clear_bins(s);
         for_each(x, i0, i1, [&](float v, int) {
@@ -492,8 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
                 if (r < ranks) members += cl.map_shared_rank(&s, r)->lo[bin];
             if (above + members <= kList) {
                 const int n = gather([&](float v) { return step_of(v) <= bin; });
-                if (rank == 0) finish(n, k, 0);  // (nobody reads another CTA's memory any more)
-                return;
+                return end_row(n, k, 0);
             }
             resolve(bin, (u64)k - above, false, 0);
         }
@@ -515,19 +524,13 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
             // pass it weigh more than that): what passes it and lies over the
             // threshold's step or in it holds all that stays, and all that is better
             const int n = gather([&](float v) { return v > least_v && step_of(v) <= bin; });
-            if (n <= kList) {
-                if (rank == 0) finish(n, kList, need);
-                return;
-            }
+            if (n <= kList) return end_row(n, kList, need);
             cl.sync();  // (the count was read; the list starts anew)
         }
         resolve(bin, need - above, true, tie_w);
     } else if (least > 0.0 && thr == 0) {
         const int n = gather([&](float v) { return v > least_v; });
-        if (n <= kList) {
-            if (rank == 0) finish(n, kList, 0);
-            return;
-        }
+        if (n <= kList) return end_row(n, kList, 0);
     }
 
     // the kept weight of each segment in index order, thr's ties counted apart

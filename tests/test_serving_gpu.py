@@ -755,6 +755,29 @@ def test_sample_ties_and_masks():
     assert check_sample(x, [0.985] * 8, temperature=[0.0] * 8).tolist()[:3] == [17, 5, 0]
 
 
+@pytest.mark.parametrize("kw", [dict(top_k=50), dict(top_k=300, top_p=0.8), dict(top_p=0.9, min_p=0.2), dict(min_p=0.2)],
+                         ids=["top-k", "top-k-p", "top-p-min-p", "min-p"])
+def test_sample_rows_that_end_in_one_cta(kw):
+    """Rows whose kept tokens fit one list, spread over clusters of 1, 2, 4 and 8 CTAs: the
+    CTA with the list outlives the others' reads of it, and the choice is the same."""
+    rng = np.random.default_rng(50)
+    rows, vocab = 100, 33001
+    x = (2 * rng.standard_normal((rows, vocab))).astype(np.float32)
+    u = rng.random(rows).astype(np.float32)
+    full = {k: [v] * rows for k, v in kw.items()}
+    check_sample(x[:4], u[:4], **{k: v[:4] for k, v in full.items()})
+    dx, du = torch.from_numpy(x).to(DEV), torch.from_numpy(u).to(DEV)
+    dk = {k: torch.tensor(v, dtype=torch.int32 if k == "top_k" else torch.float32, device=DEV) for k, v in full.items()}
+    want = sp.spectra_sample(dx, du, **dk)
+    for batch in (50, 20, 10, 1):
+        for _ in range(5):
+            got = [sp.spectra_sample(dx[i:i + batch], du[i:i + batch], **{k: v[i:i + batch] for k, v in dk.items()})
+                   for i in range(0, rows, batch)]
+            for g, w in zip(zip(*got), want):
+                assert torch.equal(torch.cat(g), w), batch
+    sp.spectra_device_status()
+
+
 def test_sample_u_at_its_ends():
     x = np.log(np.array([[1.0, 2.0, 0.0, 5.0, 0.0]] * 3, np.float64) + 1e-300).astype(np.float32)
     x[:, [2, 4]] = -np.inf
