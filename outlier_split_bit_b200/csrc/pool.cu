@@ -550,6 +550,9 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictArgs a) {
     }
     __syncthreads();
     }
+    // a CTA without entries waits too: this grid's end stands for select's, whose
+    // lengths the next kernel of the stream may read
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 }  // namespace

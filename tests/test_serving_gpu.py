@@ -669,6 +669,35 @@ def test_evict_wide_page_tables():
     sp.spectra_device_status()
 
 
+def test_evict_of_empty_sequences_is_ordered():
+    """Nothing to move: what follows in the stream, or in the graph, still sees the new lengths."""
+    n_seq = 200
+    g = sp.KVPool(4, 64, 16, n_seq * 3, mass=True)
+    pages = torch.arange(2 * n_seq, dtype=torch.int32, device=DEV).reshape(n_seq, 2)
+    dst = torch.arange(2 * n_seq, 3 * n_seq, dtype=torch.int32, device=DEV).reshape(n_seq, 1)
+    n, m = i32([0] * n_seq), i32([0] * n_seq)
+    seen = torch.empty_like(m)
+
+    def call():
+        m.fill_(99)
+        sp.spectra_kv_evict(g, pages, n, dst, 16, 3, new_lengths=m)
+        seen.copy_(m)
+
+    for _ in range(20):
+        call()
+        assert not seen.any()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr, stream=s):
+        call()
+    for _ in range(20):
+        seen.fill_(7)
+        gr.replay()
+        assert not seen.any()
+    sp.spectra_device_status()
+
+
 def test_evict_reports_pages_out_of_bounds():
     rng = np.random.default_rng(6)
     p, pages, free = filled(rng, [60], 1, 64, 16, spare=4)
