@@ -662,7 +662,10 @@ typedef struct {
  * FP32 accumulation, K's with the exact codes.  For a BF16 output V's values
  * and the weights (or the weights and their products with V's scales) are
  * rounded to FP16 on the way, 2^-11 each, an eighth of the output's own
- * rounding; an FP32 output has no such rounding.  A non-finite output (from a
+ * rounding, and what lies under FP16's normal range there is off by 2^-32 of
+ * the largest weight (2^-29 of the largest weight times the largest of V's
+ * scales); an FP32 output has no such rounding, but loses 2^-22 of a weight or
+ * 2^-32 of the largest one.  A non-finite output (from a
  * non-finite q, or from V's entries beyond 65504 in magnitude, which FP16 does
  * not hold) is reported by spectra_device_status as RANGE.  Out of bounds
  * values are reported by spectra_device_status as INVALID_ARG and

@@ -28,10 +28,14 @@
 //     subnormal, one instruction for two codes.  K's zero points take one FP32
 //     multiply-add per group, z times the query's own sum over the group; V's a
 //     product of their own, and V's scale goes into the weight: w * s rounded to
-//     FP16 (to half a subnormal step, 2^-25, at least: 2^-32 of the largest weight,
-//     which is 2^7 or more).  A w * s beyond FP16 (scales over 2) is seen in the
-//     sums, and the item is run again with weights of 1 at most, which no FP16
-//     scale takes out of range;
+//     FP16.  For that the scales are multiplied with a power of two that brings the
+//     largest of the warp's first step to 2^-3 .. 2 (none where it lies there), and
+//     the sums with its inverse: a product under FP16's normal range is then off by
+//     2^-25 where the largest weight times the largest scale is 2^4 or more, 2^-29 of
+//     it.  (Without the power, values of 1e-5 lost 0.2 % of the largest output, and
+//     many light weights beside a heavy one far more.)  Where scales grow so far
+//     that a product passes FP16's range, which is seen in the sums, the item is
+//     run again with the power that the largest of all its scales wants;
 //   less the zero point (16 columns and more, and V for an FP32 output): a nibble
 //     or-ed under 0x6400 is 1024 + c, or 1024 + 16c where it stands, and one
 //     half-precision instruction takes it to c - z, exactly.  V is dequantised to
@@ -39,12 +43,13 @@
 //     columns, where the other form's work on weights and zero points is per
 //     column.  A V beyond FP16's range turns the output non-finite, which is
 //     reported.
-// For a BF16 output the FP16 roundings are enough: 2^-11 at most, an eighth of
-// the output's own.  For an FP32 output what the two roundings left goes in as
+// For a BF16 output the FP16 roundings are enough: 2^-11 each, an eighth of the
+// output's own, and for a weight under FP16's normal range 2^-25, which is 2^-32
+// of the largest.  For an FP32 output what the two roundings left goes in as
 // well, as two more products (V's remainder is exact; of the weights 2^-22 is
-// lost), and each unit's sum is added to the accumulator in FP32: the tensor core
-// cuts its sums off (error at 8192 positions 1.4e-6 of the largest output, with
-// the separate addition 2.4e-7).
+// lost, or 2^-32 of the largest), and each unit's sum is added to the accumulator
+// in FP32: the tensor core cuts its sums off (error at 8192 positions 1.4e-6 of
+// the largest output, with the separate addition 2.4e-7).
 //
 // The scores' accumulator layout (positions in rows) is transposed into the
 // weights' operand layout inside the warp (movmatrix on FP16 pairs).  Which lane
@@ -54,7 +59,7 @@
 // and V's halfword g of every group of positions t, t + 4, t + 8, t + 12.
 //
 // The running maximum is only a reference: it moves when a weight would pass
-// 2^15, and then to 2^7 for the largest, so most units need no reduction over
+// 2^15 (2^14 where V's scale is multiplied in), and then to 2^7 for the largest, so most units need no reduction over
 // the lanes and no rescaling.
 //
 // Each warp copies its own units into a ring of three steps in shared memory,
@@ -78,6 +83,8 @@
 //     launches, the run search, the ring's first fill and the join.
 // Tried and no faster: 4 to 6 CTAs an SM with one unit a step, 4 ring steps, the
 // queries' operands in shared memory for 8 columns, 16 columns a tile where 32 fit.
+#include <type_traits>
+
 #include "internal.cuh"
 #include "pool.cuh"
 #include "select.cuh"
@@ -97,11 +104,9 @@ constexpr int kTile = kUnit * kWarps * U;
 constexpr int kMaxCtas = 148 * 4;        // runs, at most: a wave
 constexpr int kMinPositions = 128;       // of a run, at least (fewer pieces to join)
 // The reference lies kRefBelow under the maximum (base 2) when it is set, and
-// moves when a score is kRefRoom over it.  The second values are for weights
-// that are multiplied with V's scales: a weight of 1 at most times any FP16
-// number is one again.
-constexpr float kRefBelow = 7.f, kRefBelowLow = -8.f;
-constexpr float kRefRoom = 15.f, kRefRoomLow = 0.f;
+// moves when a score is kRefRoom over it (kRefRoomRaw for weights that are
+// multiplied with V's scales, brought under 2).
+constexpr float kRefBelow = 7.f, kRefRoom = 15.f, kRefRoomRaw = 14.f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -218,6 +223,12 @@ __device__ __forceinline__ void raw_codes(uint32_t w, uint32_t (&x)[4]) {
     x[3] = w8 & 0x00F000F0u;
 }
 constexpr float kRaw = 16777216.f;  // 2^24
+
+// The bits of 2^p in FP16, -24 <= p <= 15 (16: infinity), and its exponent of x > 0.
+__device__ __forceinline__ uint32_t half_pow2(int p) { return p >= -14 ? (uint32_t)(p + 15) << 10 : 1u << (24 + p); }
+__device__ __forceinline__ int half_exponent(uint32_t x) { return x >= 0x400u ? (int)(x >> 10) - 15 : 7 - __clz(x); }
+// 2^p in FP32, -126 <= p <= 127.
+__device__ __forceinline__ float pow2(int p) { return __uint_as_float((uint32_t)(p + 127) << 23); }
 
 // A group's zero points of two rows (or one, twice), as the FP16 pairs that
 // take 1024 + c and (1024 + 16c) / 16 to c - z.  zp: the rows' zero halfwords
@@ -475,6 +486,21 @@ struct VUnit {
             az[2 * r + 1] = masked_or<0x00F000F0u>(gr & 1 ? zp : zp << 4, 0x80008000u);
         }
     }
+    // The scales times 2^pow, -17 <= pow <= 22.
+    __device__ __forceinline__ void scale_by(int pow) {
+        const uint32_t by = half_pow2(min(pow, 15)) * 0x10001u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < W; ++k) s[i][k] = as_bits(__hmul2(as_half2(s[i][k]), as_half2(by)));
+        if (pow > 15) {
+            const uint32_t more = half_pow2(pow - 15) * 0x10001u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int k = 0; k < W; ++k) s[i][k] = as_bits(__hmul2(as_half2(s[i][k]), as_half2(more)));
+        }
+    }
     // The scales of group gr at two of the lane's four positions.
     __device__ __forceinline__ __half2 scale_pair(int gr, int r) const {
         return as_half2(__byte_perm(s[2 * r][gr / 2], s[2 * r + 1][gr / 2], gr & 1 ? 0x7632u : 0x5410u));
@@ -586,6 +612,25 @@ __device__ __forceinline__ uint32_t unit_of(const PoolView &p, int32_t page, int
 
 constexpr int kStages = 3;
 
+// The bits of the largest scale of V over a warp's units t0, t0 + kTile<1> ... (U of
+// them at a time) before t_end, of a length of n positions.  Seldom called, and
+// kept out of the kernel's registers.
+template <int G, int U>
+__device__ __forceinline__ uint32_t largest_scale(const PoolView &p, const int32_t *pages, int h, int t0, int t_end, int n) {
+    uint32_t most = 0;
+    for (int f = threadIdx.x & 31;; f += 32) {
+        const int t = t0 + f / U * kTile<U> + f % U * kUnit;
+        if (t >= t_end) break;
+        const uint32_t unit = unit_of(p, pages[t >> p.lp], t, h);
+        if (unit == kNoUnit) continue;
+        const uint16_t *at = p.vs + (uint64_t)unit * kUnit * G;
+        const int count = min(kUnit, n - t) * G;
+#pragma unroll 1
+        for (int k = 0; k < count; ++k) most = max(most, (uint32_t)at[k]);
+    }
+    return __reduce_max_sync(0xffffffffu, most);
+}
+
 // A warp's way through its units of one item, U at a step: unit j of step i is
 // the positions t0 + i * kTile<U> + 16 j .. + 15.  Copies run kStages - 1 steps
 // ahead, a group each.  The bookkeeping is done 32 units at a time: a lane finds
@@ -653,6 +698,32 @@ struct UnitRing {
         const int f = i * U + j;
         const uint32_t u = __shfl_sync(0xffffffffu, looked_ahead(i) ? before : units, f);
         return u == kNoUnit ? u : u & ~kSpecial;
+    }
+    // The bits of the largest scale of V of step 0's entries, whose stage is waited
+    // for (vs: LaneOffsets), of a length of n positions.
+    __device__ __forceinline__ uint32_t first_scales(int n, uint32_t vs) const {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        __syncwarp();
+        if (__all_sync(0xffffffffu, lane >= U || !(units & kSpecial))) {  // whole units: 8 scales a lane
+            const int piece = min(lane, U * 2 * G - 1), j = piece / (2 * G);
+            const uint4 w = (Shared{first} + j * S::kBytes + S::vs + 16 * (piece - j * 2 * G)).get16();
+            const uint32_t b = as_bits(__hmax2(__hmax2(as_half2(w.x), as_half2(w.y)), __hmax2(as_half2(w.z), as_half2(w.w))));
+            return __reduce_max_sync(0xffffffffu, max(b & 0xFFFFu, b >> 16));
+        }
+        uint32_t most = 0;
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int left = unit(0, j) == kNoUnit ? 0 : n - position(j);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t w[(G + 1) / 2];
+                load_halfwords<G>(w, Shared{first} + j * S::kBytes + S::vs + vs + i * 4 * 2 * G);
+                if ((lane & 3) + 4 * i < left)
+#pragma unroll
+                    for (int k = 0; k < (G + 1) / 2; ++k) most = max(most, max(w[k] & 0xFFFFu, w[k] >> 16));
+            }
+        }
+        return __reduce_max_sync(0xffffffffu, most);
     }
     // Whether the units of a later step have been looked up since step i's.
     __device__ __forceinline__ bool looked_ahead(int i) const {
@@ -804,13 +875,14 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
         uint4 qf[G];
         float mul[NT][2], qz[kRawK ? G : 1][2];
         float ref[NT][2], limit[NT][2], sum[NT][2], o[NT][G][2][4];
-        // Once; again, with lower weights, where a weight times V's scale passed
-        // FP16's range (a scale over 2: values of 30 and more).
+        // V's scales go into the products times 2^v_pow, which brings the first step's
+        // largest to 2^-3 .. 2; where scales grow so far that a product passes FP16's
+        // range, the item is run again, with the largest of all.
 #pragma unroll 1
-        for (int low = 0;; ++low) {
+        for (bool again = false;; again = true) {
         UnitRing<G, true, U> ring{p, copier, pages, ring_at, h, t0, t_end, pos_lo, pos_hi, a.window, lane};
         ring.start();  // the first units are on their way while the queries are prepared
-        if (low == 0) {
+        if (!again) {
         if (lane < C) {
             const int c = c0 + min(lane, cols - 1);
             s_col[warp][lane] = make_float2(__int_as_float(s.n - s.m + c / a.grp),
@@ -860,6 +932,16 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
                 for (int i = 0; i < 8; ++i) o[nt][gr][i >> 2][i & 3] = 0.f;
         }
 
+        int v_pow = 0;
+        if constexpr (kRawV) {
+            uint32_t most = again || ring.steps == 0 ? 0u : ring.first_scales(s.n, lo.vs);
+            if (most == 0) most = largest_scale<G, U>(p, pages, h, t0, t_end, s.n);
+            if (most > 0) {
+                const int e = half_exponent(most);
+                v_pow = e >= -3 && e <= 0 ? 0 : -2 - e;
+            }
+        }
+        auto units = [&](auto scaled) {
         for (int i = 0; i < ring.steps; ++i) {
             const Shared here = ring.next(i);
             float x[U][NT][4];
@@ -959,10 +1041,10 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
                         for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
                         // a column that saw nothing yet keeps its zeros
                         const bool first = limit[nt][e] == -INFINITY;
-                        const float under = m - (low ? kRefBelowLow : kRefBelow);
+                        const float under = m - kRefBelow;
                         const float to = m == -INFINITY ? ref[nt][e] : (first ? under : fmaxf(under, ref[nt][e]));
                         const float f = first ? 1.f : ex2(ref[nt][e] - to);
-                        if (m > -INFINITY) limit[nt][e] = to + (low ? kRefRoomLow : kRefRoom);
+                        if (m > -INFINITY) limit[nt][e] = to + (kRawV ? kRefRoomRaw : kRefRoom);
                         ref[nt][e] = to;
                         sum[nt][e] *= f;
 #pragma unroll
@@ -983,8 +1065,10 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
                     const int t = t0 + i * kTile<U> + j * kUnit;
                     vu.cut_off(ring.unit(i, j) == kNoUnit ? 0 : s.n - t, lane);
                 }
+                if constexpr (decltype(scaled)::value) vu.scale_by(v_pow);
                 // the weights as B operands: b, and (EXACT) what its rounding left
-                uint32_t b[NT][2], rest[NT][2];
+                uint32_t b[NT][2];
+                [[maybe_unused]] uint32_t rest[NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -1036,6 +1120,9 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
                 }
             }
         }
+        };
+        if (kRawV && v_pow != 0) units(std::integral_constant<bool, kRawV>());
+        else units(std::false_type());
         asm volatile("cp.async.wait_group 0;" ::: "memory");
         if constexpr (kRawV) {
             float odd = 0.f;  // NaN if a sum is not finite (though its query is)
@@ -1043,11 +1130,12 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
             for (int gr = 0; gr < G; ++gr)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) odd = fmaf(mul[0][e & 1] == mul[0][e & 1] ? o[0][gr][e >> 2][e & 3] : 0.f, 0.f, odd);
-            if (low == 0 && __any_sync(0xffffffffu, odd != 0.f)) continue;
+            if (!again && __any_sync(0xffffffffu, odd != 0.f)) continue;
+            const float f = kRaw * pow2(-v_pow);
 #pragma unroll
             for (int gr = 0; gr < G; ++gr)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[0][gr][e >> 2][e & 3] *= e & 2 ? kRaw * 0.0625f : kRaw;  // rows g + 8: odd codes
+                for (int e = 0; e < 8; ++e) o[0][gr][e >> 2][e & 3] *= e & 2 ? f * 0.0625f : f;  // rows g + 8: odd codes
         }
         break;
         }

@@ -270,6 +270,105 @@ def test_magnitudes(value_scale, q_scale, Hq, out_dtype):
                     value_scale=value_scale, q_scale=q_scale)
 
 
+def _check_bf16_values(heads_per_kv, score, v, D=64, P=64, n_seq=460):
+    """One new token over entries whose scores are score[t] (whole numbers of 1/16, 0 to 15) and
+    whose values are v [n, D] >= 0, as a BF16 output, against FP64 from the pool's read-back;
+    of so many sequences (over the same pages) that a CTA has all of one's positions.
+
+    Tolerance, with p the weights: the output's half step; two FP16 roundings of a weight
+    and of what it is multiplied with, 2^-11 of p |v| each; 2^-22, and the scores' and sums'
+    FP32 roundings, under 2^-11 all together ((32 + 4 + 4) 2^-23 of scores under 16, twice;
+    a lane adds n / 64 < 512 weights, 2^-24 each, and as many products' sums, twice, which the
+    tensor core may cut off, 2^-23); a weight under FP16's normal range, 2^-32 of the largest
+    one at most.  For 8 columns or fewer a weight meets V's scale in FP16, after a power of
+    two that brings the largest scale to 2^-3 at least where the largest weight is 2^7 at
+    least: a product under the normal range is off by 2^-25, 2^-29 of largest weight times
+    largest scale, times |c - z| <= 15; and a scale by 2^-25 after a power below 1 (scales of
+    2 and more), 2^-22 of the largest."""
+    n = len(score)
+    assert n <= 2 ** 15 and float(score.max()) < 16 and float(v.min()) >= 0
+    width = -(-n // P)
+    g = sp.KVPool(1, D, P, width + 1)
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(n)
+    pages = torch.randperm(width + 1, generator=gen, device=DEV)[:width].to(torch.int32)[None]
+    t = torch.arange(n, device=DEV)
+    slots = (pages[0, t // P] * P + t % P).to(torch.int32)
+    k = torch.zeros((n, 1, D), device=DEV)  # channels of 0 and 15 make the group's codes whole numbers
+    k[:, 0, 1] = 15.0
+    k[:, 0, 2] = torch.floor(score)
+    k[:, 0, 33] = 15.0
+    k[:, 0, 34] = torch.floor(16 * (score - torch.floor(score)))
+    g.append(k.bfloat16(), v[:, None].bfloat16(), slots)
+    q = torch.zeros((n_seq, heads_per_kv, D), device=DEV)
+    q[:, :, 2] = 1.0
+    q[:, :, 34] = 1 / 16
+    sp.spectra_device_status()
+    out = sp.spectra_attention_paged(g, pages.repeat(n_seq, 1), i32([n] * n_seq), q.bfloat16(), scale=1.0).double()
+    sp.spectra_device_status()
+    x = g.read(slots, out_dtype=torch.float32)[1][:, 0].double()
+    p = torch.softmax(score.double(), 0)
+    want = p @ x
+    tol = 2.0 ** -8 * want.abs() + (2.0 ** -10 + 2.0 ** -11) * 1.01 * (p @ x.abs()) + 2.0 ** -32 * x.abs().sum(0)
+    if heads_per_kv <= 8:
+        s = g.v_scales.view(torch.float16).double().view(-1, D // 32)[slots.long()].max()
+        tol += 15 * s * (n * 2.0 ** -29 + (2.0 ** -22 if s >= 2 else 0.0))
+    err = (out - want).abs().amax((0, 1))
+    assert (err <= tol).all(), f"worst ratio {float((err / tol).max()):.3g}"
+    return want, tol
+
+
+@pytest.mark.parametrize("heads", [4, 12])
+@pytest.mark.parametrize("size", [1e-6, 3e-5, 1e-3, 0.03, 1.0, 50.0, 3e3])
+@pytest.mark.parametrize("nats,ramp", [(0, 0), (8, 0), (11, 0), (8, 5)])
+@pytest.mark.parametrize("late", [False, True], ids=["early", "late"])
+def test_light_weights_keep_their_bits(heads, size, nats, ramp, late):
+    """A few heavy entries of no value, early or late, and thousands of light ones with all
+    of it, even or rising: the output is the light ones', whatever the values' size."""
+    n = 30000
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(nats)
+    score = torch.floor(32 * torch.rand(n, generator=gen, device=DEV)) / 16
+    score += torch.floor(16 * ramp * torch.arange(n, device=DEV) / n) / 16
+    heavy = torch.arange(8, device=DEV) * 16 + (n - 300 if late else 5)
+    score[heavy] = nats + 2 + ramp
+    v = size * (0.3 + torch.rand((n, 64), generator=gen, device=DEV))
+    v[heavy] = 0.0
+    want, tol = _check_bf16_values(heads, score, v)
+    assert (tol <= 2.0 ** -6 * want.abs()).all()  # it would show a wrong output
+
+
+@pytest.mark.parametrize("heads", [4, 12])
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+@pytest.mark.parametrize("kind", ["growing", "shrinking", "groups", "late", "spikes", "none"])
+def test_values_of_changing_size(heads, D, kind):
+    """Values that grow or shrink by 2^30 along the sequence, differ between groups, begin
+    late, jump now and then, or are all zero."""
+    n = 20000
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(77)
+    r = lambda *shape: torch.rand(shape, generator=gen, device=DEV)  # noqa: E731
+    score = torch.floor(128 * r(n)) / 16
+    v = 0.3 + r(n, D)
+    t = torch.arange(n, device=DEV)[:, None]
+    if kind in ("growing", "shrinking"):
+        e = 30 * t / n
+        v *= torch.exp2(-18 + (e if kind == "growing" else 30 - e))
+    elif kind == "groups":
+        v[:, 32:] *= 2.0 ** -10
+    elif kind == "late":
+        v *= torch.where(t < 777, 0.0, 1e-4)
+    elif kind == "spikes":
+        v *= torch.where(r(n)[:, None] < 0.001, 3e4, 0.1)
+    else:
+        v.zero_()
+    want, tol = _check_bf16_values(heads, score, v, D=D)
+    if kind == "none":
+        assert not want.any()
+    elif kind not in ("groups", "spikes"):  # (there the largest scale is far over the output: 15 * 2600 * n * 2^-29 = 1.5 of 17)
+        assert (tol <= 2.0 ** -6 * want.abs()).all()
+
+
 def test_queries_of_every_magnitude():
     """Rows from subnormal to huge, zeros, and elements 2^40 apart in one row."""
     rng = np.random.default_rng(19)
