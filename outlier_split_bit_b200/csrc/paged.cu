@@ -583,19 +583,52 @@ __device__ __forceinline__ void query_operands(const uint16_t *q, int t, uint4 (
     }
 }
 
-// tanh to an absolute 2^-21 or so.
-__device__ __forceinline__ float tanh_abs(float y) { return 1.f - __fdividef(2.f, ex2(2.f * kLog2e * y) + 1.f); }
+// tanh to a relative 1.5 * 2^-22: a score is the cap times it, so an absolute error
+// would grow with the cap.  Under kTanhNear y + y^3 p(y^2), p of degree 4 fitted to
+// the least relative error (4.1e-9; 1.3 * 2^-24 with its roundings); over it 1 - 2 /
+// (exp(2y) + 1), where the exponential's 2^-22 and the reciprocal's 2^-23 count by
+// 0.35 and 0.45 of 0.55 or more.  Scores are mostly well under their cap, so a warp's step takes the second
+// form only where one of its values wants it.
+constexpr float kTanhNear = 0.625f;
+__device__ __forceinline__ float tanh_near(float y) {
+    const float u = y * y;
+    float p = fmaf(u, -0.00571703365f, 0.0206505762f);
+    p = fmaf(p, u, -0.0537434943f);
+    p = fmaf(p, u, 0.133314912f);
+    p = fmaf(p, u, -0.333332839f);
+    return fmaf(p, u * y, y);
+}
+__device__ __forceinline__ float tanh_any(float y) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(2.f * kLog2e * fabsf(y)) + 1.f));
+    return fabsf(y) < kTanhNear ? tanh_near(y) : copysignf(fmaf(-2.f, r, 1.f), y);
+}
 
 // What turns a product sum (its factor taken in) into a score in base 2.
 struct Score {
     float mul, cap;  // without a cap: s = mul * dot; with: cap * tanh(mul * dot)
     bool capped;
     __device__ __forceinline__ explicit Score(const PagedArgs &a) {
-        capped = a.cap > 0.f;
+        // (a cap over 2^100 changes no score under 2^88, and its product with log2 e
+        // might not be finite)
+        capped = a.cap > 0.f && a.cap < 0x1p100f;
         mul = capped ? a.scale / a.cap : a.scale * kLog2e;
         cap = a.cap * kLog2e;
     }
-    __device__ __forceinline__ float cap_of(float y) const { return cap * tanh_abs(y); }
+    // Caps a step's values, N of this lane's.
+    template <int N>
+    __device__ __forceinline__ void cap_all(float (&y)[N]) const {
+        bool near = true;
+#pragma unroll
+        for (int i = 0; i < N; ++i) near = near && fabsf(y[i]) < kTanhNear;
+        if (__all_sync(0xffffffffu, near)) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) y[i] = cap * tanh_near(y[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) y[i] = cap * tanh_any(y[i]);
+        }
+    }
 };
 
 // (No pool has 2^31 units: they would be 4 TB and more.)
@@ -987,6 +1020,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
                     for (int e = 0; e < 4; ++e) x[j][nt][e] = (kRawK ? x[j][nt][e] * kRaw : x[j][nt][e]) * mul[nt][e & 1];
             }
             if (shaped) {
+                if (score.capped) score.cap_all(reinterpret_cast<float(&)[U * NT * 4]>(x));
 #pragma unroll
                 for (int j = 0; j < U; ++j)
 #pragma unroll
@@ -997,8 +1031,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
                             const int gap = __float_as_int(col.x) - (t0 + i * kTile<U> + j * kUnit) - unit_position(g);
 #pragma unroll
                             for (int r = 0; r < 2; ++r) {
-                                const float v = x[j][nt][2 * r + e];
-                                x[j][nt][2 * r + e] = fmaf(-col.y, (float)(gap - 8 * r), score.capped ? score.cap_of(v) : v);
+                                x[j][nt][2 * r + e] = fmaf(-col.y, (float)(gap - 8 * r), x[j][nt][2 * r + e]);
                             }
                         }
             }
@@ -1439,10 +1472,11 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 3) paged_mass_kernel(co
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[e] = x[e] * kRaw * mul[e & 1];
                     if (shaped) {
+                        if (score.capped) score.cap_all(x);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int gap = pos[e & 1] - t - unit_position(g) - 4 * (e & 2);
-                            x[e] = fmaf(-slope[e & 1], (float)gap, score.capped ? score.cap_of(x[e]) : x[e]);
+                            x[e] = fmaf(-slope[e & 1], (float)gap, x[e]);
                         }
                     }
                     if (marked) {

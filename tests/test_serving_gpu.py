@@ -369,6 +369,38 @@ def test_values_of_changing_size(heads, D, kind):
         assert (tol <= 2.0 ** -6 * want.abs()).all()
 
 
+@pytest.mark.parametrize("heads", [4, 12])
+@pytest.mark.parametrize("cap", [1.0, 20.0, 50.0, 1e3, 1e6, 1e37, 3e38])
+def test_cap_is_relative(heads, cap):
+    """Sequences of one position, so that lse is the score: cap * tanh(x / cap), whatever the cap.
+
+    Tolerance, relative: scale / cap, its product with x, tanh (1.5 * 2^-22), cap * log2 e
+    and the product with it, 2^-24 each or as told, the reference 7 under the score and back
+    with the logarithm, and ln 2: 10 * 2^-24 and 1.5 * 2^-22, 2^-20; and where the score is
+    small beside the 7, 2^-24 of 8, twice: 2^-20 absolute."""
+    n = 16 * 40
+    x = torch.arange(1, n + 1, device=DEV) * (15.0 / n)
+    x = torch.where(torch.arange(n, device=DEV) % 2 == 0, x, -x)
+    x[::5] *= 2.0 ** -6
+    g = sp.KVPool(1, 64, 16, n)
+    k = torch.zeros((n, 1, 64), device=DEV)
+    k[:, 0, 7] = 15.0  # whole numbers as codes: 0 and 15
+    slots = torch.arange(n, dtype=torch.int32, device=DEV) * 16
+    g.append(k.bfloat16(), k.bfloat16(), slots)
+    q = torch.zeros((n, heads, 64), device=DEV)
+    q[:, :, 7] = (x / 15)[:, None]
+    q = q.bfloat16()
+    x = 15 * q[:, :, 7].double()
+    sp.spectra_device_status()
+    _, lse = sp.spectra_attention_paged(g, torch.arange(n, dtype=torch.int32, device=DEV)[:, None].contiguous(),
+                                        i32([1] * n), q, scale=1.0, softcap=cap, want_lse=True, out_dtype=torch.float32)
+    sp.spectra_device_status()
+    cap = float(np.float32(cap))
+    want = cap * torch.tanh(x / cap)
+    err, tol = (lse.double() - want).abs(), 2.0 ** -20 * want.abs() + 2.0 ** -20
+    assert (err <= tol).all(), f"worst ratio {float((err / tol).max()):.3g}"
+
+
 def test_queries_of_every_magnitude():
     """Rows from subnormal to huge, zeros, and elements 2^40 apart in one row."""
     rng = np.random.default_rng(19)
