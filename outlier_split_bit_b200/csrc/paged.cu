@@ -119,6 +119,7 @@ struct PagedArgs {
     const float *slopes;
     void *out;
     float *lse;
+    float2 *ws_row;  // [rows][query heads]: store_lse's, for the accumulated weights (null without them)
     float *ws_acc;   // [2 * runs][columns][D]
     float2 *ws_ml;   // [2 * runs][columns]: reference, sum
     int4 *ws_item;   // [runs]: an item cut at the run's end: (last run, first row, columns, head); last run -1: none
@@ -833,6 +834,15 @@ __device__ __forceinline__ void store_out(const PagedArgs &a, int64_t at, float4
     if (!(isfinite(v.x) && isfinite(v.y) && isfinite(v.z) && isfinite(v.w))) atomicOr(&g_paged_error, 2u);
 }
 
+// A row's lse from its reference and sum (base 2).  The accumulated weights take the
+// two apart, reference and inverse sum, so that a score and the reference, both of
+// them large perhaps, are subtracted before anything is rounded to their size.
+// A row that saw nothing: infinity and 0, which make every weight 0.
+__device__ __forceinline__ void store_lse(const PagedArgs &a, int64_t row, float m, float l) {
+    if (a.lse) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    if (a.ws_row) a.ws_row[row] = l > 0.f ? make_float2(m, 1.f / l) : make_float2(INFINITY, 0.f);
+}
+
 // Units of a step: two where the accumulators leave the registers for it (the
 // loop's own work is done once for both, and their instructions interleave).
 template <int G, int NT>
@@ -1217,7 +1227,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
                 if (whole) {
                     const int64_t row = (int64_t)(s.row0 + (c0 + c) / a.grp) * a.Hq + h * a.grp + (c0 + c) % a.grp;
                     store_out<EXACT>(a, row * D + d, v, l);
-                    if (d == 0 && a.lse) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+                    if (d == 0) store_lse(a, row, m, l);
                 } else {
                     *reinterpret_cast<float4 *>(a.ws_acc + (slot * C + c) * D + d) = v;
                     if (d == 0) a.ws_ml[slot * C + c] = make_float2(m, l);
@@ -1262,7 +1272,7 @@ __global__ void __launch_bounds__(kJoinThreads, LONG ? 7 : 8) paged_join_kernel(
         const int h = cut.w;
         const int64_t row = (int64_t)(cut.y + (c0 + c) / a.grp) * a.Hq + h * a.grp + (c0 + c) % a.grp;
         store_out<EXACT>(a, row * D + d, v, l);
-        if (d == 0 && a.lse) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        if (d == 0) store_lse(a, row, m, l);
     };
     if (!LONG && np <= kFewPieces) {
         for (int i = blockIdx.y * kJoinThreads + tid; i < cols * Q; i += gridDim.y * kJoinThreads) {
@@ -1367,7 +1377,7 @@ __global__ void __launch_bounds__(kJoinThreads, LONG ? 7 : 8) paged_join_kernel(
     }
 }
 
-// The accumulated weights, a second pass over K alone with the rows' lse (the
+// The accumulated weights, a second pass over K alone with the rows' sums (the
 // weights need the whole row's sum; keeping a row's scores for it would write and
 // read 4 bytes per query head and position, where K is read again for D / 2 + D /
 // 16 per KV head): a warp per unit, 8 columns at a time.  A position's sum over
@@ -1394,7 +1404,7 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 3) paged_mass_kernel(co
         return s.m == 0 || s.n == 0 ? 0 : (int64_t)p.H * tiles_of<U>(a, s).count;
     };
     Run run = find_run(per_seq, a.n_seq, blockIdx.x, gridDim.x, kMinPositions / kTile<U>, s_part, s_found);
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the rows' lse
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the rows' sums
     int b = run.b;
     while (run.cur < run.end) {
         const Sequence s = sequence_of(a, b);
@@ -1419,14 +1429,15 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 3) paged_mass_kernel(co
             UnitRing<G, false, U> ring{p, copier, pages, ring_at, h, t0, t_end, pos_lo, pos_hi, a.window, lane};
             __syncwarp();  // every lane has read the ring's last unit of the columns before
             ring.start();
-            float lse2[2], slope[2];
+            float ref[2], inv[2], slope[2];
             int pos[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 // a column past the last, or one that saw nothing: weight 0
                 const int c = c0 + min(2 * t4 + e, cols - 1);
-                const float v = a.lse[(int64_t)(s.row0 + c / a.grp) * a.Hq + h * a.grp + c % a.grp] * kLog2e;
-                lse2[e] = 2 * t4 + e < cols && v != -INFINITY ? v : INFINITY;
+                const float2 v = a.ws_row[(int64_t)(s.row0 + c / a.grp) * a.Hq + h * a.grp + c % a.grp];
+                ref[e] = 2 * t4 + e < cols ? v.x : INFINITY;
+                inv[e] = 2 * t4 + e < cols ? v.y : 0.f;
                 pos[e] = s.n - s.m + c / a.grp;
                 slope[e] = a.slopes ? a.slopes[h * a.grp + c % a.grp] * kLog2e : 0.f;
             }
@@ -1490,7 +1501,7 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 3) paged_mass_kernel(co
                     float w[2];
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        w[r] = ex2(x[2 * r] - lse2[0]) + ex2(x[2 * r + 1] - lse2[1]);
+                        w[r] = fmaf(ex2(x[2 * r] - ref[0]), inv[0], ex2(x[2 * r + 1] - ref[1]) * inv[1]);
                         w[r] += __shfl_xor_sync(0xffffffffu, w[r], 1);
                         w[r] += __shfl_xor_sync(0xffffffffu, w[r], 2);
                     }
@@ -1521,13 +1532,13 @@ int n_tiles(int G, int64_t cols) {
 size_t ceil16(size_t n) { return (n + 15) / 16 * 16; }
 
 struct Workspace {
-    size_t acc, ml, item, lse, total;
+    size_t acc, ml, item, row, total;
     Workspace(int G, int C, int64_t n_rows, int Hq) {
         acc = 0;
         ml = acc + (size_t)2 * kMaxCtas * C * 32 * G * sizeof(float);
         item = ml + (size_t)2 * kMaxCtas * C * sizeof(float2);
-        lse = item + kMaxCtas * sizeof(int4);
-        total = lse + ceil16((size_t)n_rows * Hq * sizeof(float));
+        row = item + kMaxCtas * sizeof(int4);
+        total = row + ceil16((size_t)n_rows * Hq * sizeof(float2));
     }
 };
 
@@ -1630,7 +1641,8 @@ spectra_status launch_paged_attention(const spectra_kv_pool &pool, const spectra
     a.ws_acc = reinterpret_cast<float *>(base + w.acc);
     a.ws_ml = reinterpret_cast<float2 *>(base + w.ml);
     a.ws_item = reinterpret_cast<int4 *>(base + w.item);
-    a.lse = x.lse ? x.lse : (x.update_mass ? reinterpret_cast<float *>(base + w.lse) : nullptr);
+    a.lse = x.lse;
+    a.ws_row = x.update_mass ? reinterpret_cast<float2 *>(base + w.row) : nullptr;
     cudaError_t e = cudaErrorInvalidValue;
     const bool mass = x.update_mass != 0, exact = x.out_dtype == SPECTRA_F32;
     switch (a.p.G) {

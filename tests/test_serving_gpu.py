@@ -401,6 +401,32 @@ def test_cap_is_relative(heads, cap):
     assert (err <= tol).all(), f"worst ratio {float((err / tol).max()):.3g}"
 
 
+@pytest.mark.parametrize("heads", [4, 12])
+def test_mass_of_one_position_is_one(heads):
+    """Sequences of one position with scores up to 1500: each head's weight there is 1.
+
+    Tolerance: both passes find the same score (one product, exact but for the factor);
+    its distance to the row's reference is exact, so the sum and the weight are the same
+    exponential, 2^-22 each should they differ, with the inverse's rounding and the
+    products', under 2^-20 all together, whatever the scores."""
+    n = 800
+    x = torch.arange(1, n + 1, device=DEV) * (2000.0 / n)
+    x = torch.where(torch.arange(n, device=DEV) % 2 == 0, x, -x)
+    g = sp.KVPool(1, 64, 16, n, mass=True)
+    k = torch.zeros((n, 1, 64), device=DEV)
+    k[:, 0, 7] = 15.0  # whole numbers as codes: 0 and 15
+    slots = torch.arange(n, dtype=torch.int32, device=DEV) * 16
+    g.append(k.bfloat16(), k.bfloat16(), slots)
+    q = torch.zeros((n, heads, 64), device=DEV)
+    q[:, :, 7] = (x / 15)[:, None]
+    q = q.bfloat16()
+    sp.spectra_attention_paged(g, torch.arange(n, dtype=torch.int32, device=DEV)[:, None].contiguous(), i32([1] * n), q,
+                               scale=0.7371, update_mass=True)
+    sp.spectra_device_status()
+    err = (g.mass.view(n, 16)[:, 0].double() / heads - 1).abs()
+    assert (err <= 2.0 ** -20).all(), float(err.max())
+
+
 def test_queries_of_every_magnitude():
     """Rows from subnormal to huge, zeros, and elements 2^40 apart in one row."""
     rng = np.random.default_rng(19)
