@@ -653,7 +653,8 @@ typedef struct {
  *   p = softmax(s), out[d] = sum_t p_t * v_hat[t][d], lse = log sum_t exp(s_t),
  *   mass[t of head h] += sum over the rows and the group's query heads of p_t.
  * A row that sees nothing (an empty sequence, or pos < 0) gets zeros and lse
- * = -infinity.  Rows of q outside every sequence are neither read nor
+ * = -infinity.  A query that is not finite has a NaN output and lse and adds
+ * nothing to the mass; other heads and rows are not touched by it.  Rows of q outside every sequence are neither read nor
  * written.  Positions and distances count cached entries: after an eviction
  * they count the entries that are left.
  *   workspace  device, 16-byte aligned, >= the stated size; its contents need

@@ -837,9 +837,10 @@ __device__ __forceinline__ void store_out(const PagedArgs &a, int64_t at, float4
 // A row's lse from its reference and sum (base 2).  The accumulated weights take the
 // two apart, reference and inverse sum, so that a score and the reference, both of
 // them large perhaps, are subtracted before anything is rounded to their size.
-// A row that saw nothing: infinity and 0, which make every weight 0.
+// A row that saw nothing, or whose query is not finite (l is NaN then, and so is its
+// lse): infinity and 0, which make every weight 0.
 __device__ __forceinline__ void store_lse(const PagedArgs &a, int64_t row, float m, float l) {
-    if (a.lse) a.lse[row] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    if (a.lse) a.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     if (a.ws_row) a.ws_row[row] = l > 0.f ? make_float2(m, 1.f / l) : make_float2(INFINITY, 0.f);
 }
 
@@ -1442,10 +1443,10 @@ __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 3) paged_mass_kernel(co
                 slope[e] = a.slopes ? a.slopes[h * a.grp + c % a.grp] * kLog2e : 0.f;
             }
             uint4 qf[G];
-            const int cg = c0 + g;
+            // (a query whose weights are 0 all the same reads as zeros: its products may be NaN)
+            const int64_t at_q = (int64_t)(s.row0 + (c0 + g) / a.grp) * a.Hq + h * a.grp + (c0 + g) % a.grp;
             float back, mul[2], zero[G], qz[G][2];
-            query_operands<G, true>(g < cols ? a.q + ((int64_t)(s.row0 + cg / a.grp) * a.Hq + h * a.grp + cg % a.grp) * D
-                                       : nullptr, t4, qf, back, zero);
+            query_operands<G, true>(g < cols && a.ws_row[at_q].y != 0.f ? a.q + at_q * D : nullptr, t4, qf, back, zero);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 mul[e] = score.mul * __shfl_sync(0xffffffffu, back, 4 * (2 * t4 + e));

@@ -678,6 +678,47 @@ def test_attention_reports_a_query_that_is_not_finite():
     assert e.value.status == 5
 
 
+@pytest.mark.parametrize("heads", [3, 9])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_query_that_is_not_finite_adds_no_mass(heads, bad):
+    """The entries' mass is the other heads' and rows' alone, and that row's lse is NaN."""
+    n_seq, length, H = 2, 3000, 2
+    g, pages, _ = _big(n_seq, length, H, H * heads, 64, 16, seed=6)
+    g = sp.KVPool.from_buffers(H, 64, 16, g.n_pages, g.k_codes, g.k_scales, g.k_zeros, g.v_codes, g.v_scales, g.v_zeros,
+                               torch.zeros(g.n_pages * H * 16, device=DEV))
+    q = torch.randn((2 * n_seq, H * heads, 64), device=DEV).bfloat16()
+    start, n = i32([0, 2, 4]), i32([length, length - 5])
+    good, lse = sp.spectra_attention_paged(g, pages, n, q, start, max_q=2, want_lse=True, update_mass=True)
+    sp.spectra_device_status()
+    sick = q.clone()
+    sick[1, 2, 7] = bad  # row 1 of sequence 0, a head of KV head 0
+    g.mass.zero_()
+    out, lse2 = sp.spectra_attention_paged(g, pages, n, sick, start, max_q=2, want_lse=True, update_mass=True)
+    with pytest.raises(sp.SpectraError) as e:
+        sp.spectra_device_status()
+    assert e.value.status == 5
+    same = torch.ones((2 * n_seq, H * heads), dtype=torch.bool, device=DEV)
+    same[1, 2] = False
+    assert torch.equal(out[same], good[same]) and torch.equal(lse2[same], lse[same])
+    assert out[1, 2].isnan().all() and lse2[1, 2].isnan()
+    # the FP64 weights of all the others
+    t = torch.arange(length, device=DEV)
+    want = torch.zeros_like(g.mass, dtype=torch.float64).view(-1, H, 16)
+    for b, m in enumerate([length, length - 5]):
+        k = g.read((pages[b, t[:m] // 16] * 16 + t[:m] % 16).to(torch.int32), out_dtype=torch.float32)[0].double()
+        for r in range(2):
+            for i in range(H * heads):
+                if same[2 * b + r, i]:
+                    s = k[:, i // heads] @ q[2 * b + r, i].double() / 8
+                    s[m - 1 + r:] = -float("inf")
+                    add = torch.zeros(length, dtype=torch.float64, device=DEV)
+                    add[:m] = torch.softmax(s, 0)
+                    want[pages[b].long(), i // heads] += torch.nn.functional.pad(add, (0, pages.shape[1] * 16 - length)).view(-1, 16)
+    # FP32 scores of 64 products, under 40 (2^-23 * 68 each of a sum of magnitudes under 60), twice; sums and weights 2^-18
+    err = (g.mass.double() - want.flatten()).abs()
+    assert (err <= want.flatten() * (2 * 68 * 60 * 2.0 ** -23 + 2.0 ** -18) + 1e-37).all()
+
+
 # ---------------------------------------------------------------- eviction
 
 def check_evict(rng, lengths, H, D, P, budget, recent, ties=False, bad=False):
