@@ -670,7 +670,8 @@ typedef struct {
  * non-finite q, or from V's entries beyond 65504 in magnitude, which FP16 does
  * not hold) is reported by spectra_device_status as RANGE.  Out of bounds
  * values are reported by spectra_device_status as INVALID_ARG and
- * touch nothing: a page id outside the pool hides its positions, a length
+ * touch nothing: a page id outside the pool hides its positions (one that no
+ * row sees, behind a window, is not looked at), a length
  * outside [0, max_pages*page_size] counts as 0, and a sequence whose rows lie
  * outside [0, n_rows) or number more than max_q has its rows left as they
  * were.  Sequences may share pages.  Deterministic (but for the mass of an

@@ -646,15 +646,16 @@ __device__ __forceinline__ uint32_t unit_of(const PoolView &p, int32_t page, int
 
 constexpr int kStages = 3;
 
-// The bits of the largest scale of V over a warp's units t0, t0 + kTile<1> ... (U of
-// them at a time) before t_end, of a length of n positions.  Seldom called, and
-// kept out of the kernel's registers.
+// The bits of the largest scale of V over a warp's units (U at a time, from t0)
+// with positions from `lo` on and before t_end, of a length of n positions.
 template <int G, int U>
-__device__ __forceinline__ uint32_t largest_scale(const PoolView &p, const int32_t *pages, int h, int t0, int t_end, int n) {
+__device__ __forceinline__ uint32_t largest_scale(const PoolView &p, const int32_t *pages, int h, int t0, int lo,
+                                                  int t_end, int n) {
     uint32_t most = 0;
     for (int f = threadIdx.x & 31;; f += 32) {
         const int t = t0 + f / U * kTile<U> + f % U * kUnit;
         if (t >= t_end) break;
+        if (t + kUnit <= lo) continue;
         const uint32_t unit = unit_of(p, pages[t >> p.lp], t, h);
         if (unit == kNoUnit) continue;
         const uint16_t *at = p.vs + (uint64_t)unit * kUnit * G;
@@ -687,7 +688,8 @@ struct UnitRing {
         const int t = position(f + lane);
         before = units;
         units = kNoUnit;
-        if (t < t_end) {
+        // (a unit wholly behind the window may lie on a page that was freed)
+        if (t < t_end && !(window > 0 && t + kUnit - 1 <= pos_lo - window)) {
             const uint32_t unit = unit_of(p, pages[t >> p.lp], t, h);
             if (unit != kNoUnit) {
                 units = unit;
@@ -979,7 +981,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
         int v_pow = 0;
         if constexpr (kRawV) {
             uint32_t most = again || ring.steps == 0 ? 0u : ring.first_scales(s.n, lo.vs);
-            if (most == 0) most = largest_scale<G, U>(p, pages, h, t0, t_end, s.n);
+            if (most == 0) most = largest_scale<G, U>(p, pages, h, t0, vis_lo, t_end, s.n);
             if (most > 0) {
                 const int e = half_exponent(most);
                 v_pow = e >= -3 && e <= 0 ? 0 : -2 - e;

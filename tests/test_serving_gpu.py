@@ -591,6 +591,33 @@ def test_attention_refuses_values_out_of_bounds():
             assert status() == 1 and (out == 7.0).any()
 
 
+@pytest.mark.parametrize("D,Hq,m,out_dtype", [(64, 4, 1, torch.bfloat16), (128, 12, 1, torch.float32), (256, 2, 1, torch.bfloat16),
+                                              (96, 3, 5, torch.bfloat16), (64, 2, 20, torch.float32)])
+@pytest.mark.parametrize("window", [1, 17, 40])
+def test_pages_behind_the_window_may_be_gone(D, Hq, m, out_dtype, window):
+    """A page that no row sees is not looked at: outputs and mass are the same bits, and nothing is reported."""
+    lengths = list(range(m, 150, 7))
+    g, pages, _ = _big(len(lengths), 160, 1, Hq, D, 16, seed=9)
+    g = sp.KVPool.from_buffers(1, D, 16, g.n_pages, g.k_codes, g.k_scales, g.k_zeros, g.v_codes, g.v_scales, g.v_zeros,
+                               torch.zeros(g.n_pages * 16, device=DEV))
+    g.v_scales[: g.v_scales.numel() // 3].zero_()  # some first steps without a scale
+    q = torch.randn((m * len(lengths), Hq, D), device=DEV).bfloat16()
+    start = i32(m * np.arange(len(lengths) + 1))
+    call = lambda table: sp.spectra_attention_paged(g, table, i32(lengths), q, start, max_q=m, window=window,  # noqa: E731
+                                                    out_dtype=out_dtype, want_lse=True, update_mass=True)
+    sp.spectra_device_status()
+    want = [*call(pages), g.mass.clone()]
+    g.mass.zero_()
+    freed = pages.clone()
+    for b, n in enumerate(lengths):
+        freed[b, : max(0, n - m - window + 1) // 16] = -1  # the first row's first position is n - m - window + 1
+        freed[b, -(-n // 16):] = 2 ** 31 - 1
+    assert (freed == -1).any()
+    got = [*call(freed), g.mass]
+    sp.spectra_device_status()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_attention_streams_graphs_and_shared_workspace():
     """Two captured graphs that share a workspace, replayed in turn with lengths
     and pages changed in place; and calls on two streams at once."""
