@@ -731,8 +731,8 @@ SPECTRA_API spectra_status spectra_kv_evict(const spectra_kv_pool *pool, const i
  *   temperature  device float [rows], or NULL for 1; <= 0 (or NaN): the first
  *                of the largest logits
  *   top_k        device int32 [rows], or NULL; <= 0: off
- *   top_p        device float [rows], or NULL; >= 1: off
- *   min_p        device float [rows], or NULL; <= 0: off
+ *   top_p        device float [rows], or NULL; >= 1: off (and a NaN)
+ *   min_p        device float [rows], or NULL; <= 0: off (and a NaN)
  *   ids          device int32 [rows]
  *   logprob      device float [rows], or NULL: log of the chosen token's share
  *                of what is left after the filters

@@ -417,7 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
 
     const int k = a.top_k ? a.top_k[row] : 0;
     const float p = a.top_p ? a.top_p[row] : 1.f;
-    const double least = a.min_p ? fmin((double)a.min_p[row], 1.0) : 0.0;
+    const float min_p = a.min_p ? a.min_p[row] : 0.f;
+    const double least = min_p > 0.f ? fmin((double)min_p, 1.0) : 0.0;  // (a NaN: off)
     float u = a.u[row];
     u = u == u ? fminf(fmaxf(u, 0.f), 0.99999994f) : 0.f;
     auto choose = [&](int i, u64 total) {

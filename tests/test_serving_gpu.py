@@ -1032,6 +1032,22 @@ def test_sample_rows_that_end_in_one_cta(kw):
     sp.spectra_device_status()
 
 
+@pytest.mark.parametrize("vocab", [1000, 40000])
+def test_sample_nan_settings_are_off(vocab):
+    """A NaN in top_p or min_p filters nothing, as a value past its range does."""
+    rng = np.random.default_rng(vocab)
+    x = torch.from_numpy((2 * rng.standard_normal((6, vocab))).astype(np.float32)).to(DEV)
+    u = torch.from_numpy(rng.random(6).astype(np.float32)).to(DEV)
+    nan = torch.full((6,), float("nan"), device=DEV)
+    want = sp.spectra_sample(x, u)
+    for got in (sp.spectra_sample(x, u, min_p=nan), sp.spectra_sample(x, u, top_p=nan),
+                sp.spectra_sample(x, u, top_p=nan, min_p=nan, top_k=torch.zeros(6, dtype=torch.int32, device=DEV)),
+                sp.spectra_sample(x, u, min_p=-nan.nan_to_num(1.0))):
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.equal(sp.spectra_sample(x, u, min_p=nan, top_p=torch.full_like(u, 0.5))[0],
+                       sp.spectra_sample(x, u, top_p=torch.full_like(u, 0.5))[0])
+
+
 def test_sample_u_at_its_ends():
     x = np.log(np.array([[1.0, 2.0, 0.0, 5.0, 0.0]] * 3, np.float64) + 1e-300).astype(np.float32)
     x[:, [2, 4]] = -np.inf
