@@ -312,11 +312,13 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
     w.inv_t = 1.0 / (double)temp;
     w.table = s.table;
     w.c = &a.exp;
-    const float inv_step = (float)kBins / (kReach * temp);
+    // half the distance to the maximum in steps: of logits of 1e38 and both signs the
+    // distance itself may not be finite (at a temperature of that size)
+    const float half_mx = 0.5f * mx, inv_step = 2.f * kBins / (kReach * temp);
     // the step of a value below the maximum, kBins or more beyond the reach
     // (subtraction, product and truncation keep the order of the values)
     auto step_of = [&](float v) -> int {
-        return v == mx ? 0 : (int)fminf((mx - v) * inv_step, (float)kBins);  // (fminf drops a NaN)
+        return v == mx ? 0 : (int)fminf(fmaf(v, -0.5f, half_mx) * inv_step, (float)kBins);  // (fminf drops a NaN)
     };
 
     uint32_t thr = 0;  // the smallest kept key,

@@ -1032,6 +1032,22 @@ def test_sample_rows_that_end_in_one_cta(kw):
     sp.spectra_device_status()
 
 
+@pytest.mark.parametrize("vocab", [7, 3000, 40000])
+@pytest.mark.parametrize("temperature", [1e30, 1.05e37, 2e37, 1e38, 3e38])
+def test_sample_logits_of_every_finite_size(vocab, temperature):
+    """Logits up to the type's ends, whose differences the type does not hold."""
+    rng = np.random.default_rng(vocab)
+    x = (rng.uniform(-3.4e38, 3.4e38, (4, vocab))).astype(np.float32)
+    x[0, ::5] = -np.inf
+    x[1] *= np.float32(1e-3)
+    t = [temperature] * 4
+    u = rng.random(4).astype(np.float32)
+    check_sample(x, u, temperature=t)
+    check_sample(x, u, temperature=t, top_p=[0.5, 0.9, 0.3, 0.99])
+    check_sample(x, u, temperature=t, top_k=[3, 100, 1, 2000])
+    check_sample(x, u, temperature=t, top_k=[5, 600, 40, 0], top_p=[0.9, 0.6, 0.8, 0.7], min_p=[0.0, 0.1, 0.02, 0.3])
+
+
 @pytest.mark.parametrize("vocab", [1000, 40000])
 def test_sample_nan_settings_are_off(vocab):
     """A NaN in top_p or min_p filters nothing, as a value past its range does."""
