@@ -1090,7 +1090,8 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
                         const float under = m - kRefBelow;
                         const float to = m == -INFINITY ? ref[nt][e] : (first ? under : fmaxf(under, ref[nt][e]));
                         const float f = first ? 1.f : ex2(ref[nt][e] - to);
-                        if (m > -INFINITY) limit[nt][e] = to + (kRawV ? kRefRoomRaw : kRefRoom);
+                        // (rounded down: up, at scores past 2^24, a weight would leave FP16's range)
+                        if (m > -INFINITY) limit[nt][e] = __fadd_rd(to, kRawV ? kRefRoomRaw : kRefRoom);
                         ref[nt][e] = to;
                         sum[nt][e] *= f;
 #pragma unroll

@@ -427,6 +427,36 @@ def test_mass_of_one_position_is_one(heads):
     assert (err <= 2.0 ** -20).all(), float(err.max())
 
 
+@pytest.mark.parametrize("heads,out_dtype", [(4, torch.bfloat16), (4, torch.float32), (12, torch.bfloat16), (12, torch.float32)])
+@pytest.mark.parametrize("e", range(22, 32))
+def test_scores_a_few_steps_of_the_type_apart(heads, out_dtype, e):
+    """Scores of 2^e to 2^(e+1), rising along the sequence by a few steps of FP32 at that size:
+    outputs are averages of the values (all 1, scale 1 and a code of 1 or 15), and the weights
+    of each row and head sum to 1."""
+    n, D = 2560, 64
+    g = sp.KVPool(1, D, 16, n // 16, mass=True)
+    k = torch.zeros((n, 1, D), device=DEV)
+    k[:, 0, 1] = 15.0
+    k[:, 0, 2] = torch.floor(torch.arange(n, device=DEV) * (16.0 / n))
+    v = torch.ones((n, 1, D), device=DEV)
+    v[:, :, ::2] = 15.0
+    v[:, :, :2] = 0.0  # (a group's scale is 1)
+    slots = torch.arange(n, dtype=torch.int32, device=DEV)
+    g.append(k.bfloat16(), v.bfloat16(), slots)
+    n_seq = 460  # as many as leave a sequence in one run
+    q = torch.zeros((n_seq, heads, D), device=DEV)
+    q[:, :, 1] = (2.0 ** e * (1 + torch.arange(n_seq, device=DEV) / n_seq) / 15)[:, None]
+    q[:, :, 2] = 2.0 ** (e - 24)
+    pages = torch.arange(n // 16, dtype=torch.int32, device=DEV).repeat(n_seq, 1)
+    sp.spectra_device_status()
+    out = sp.spectra_attention_paged(g, pages, i32([n] * n_seq), q.bfloat16(), scale=1.0, out_dtype=out_dtype, update_mass=True)
+    sp.spectra_device_status()
+    want = g.read(slots[:1], out_dtype=torch.float32)[1].double()[0]
+    # FP16 roundings and the output's own; the sums of n terms
+    assert ((out.double() - want).abs() <= (2.0 ** -8 + 2.0 ** -9 if out_dtype is torch.bfloat16 else 2.0 ** -15) * want).all()
+    assert abs(float(g.mass.double().sum()) - n_seq * heads) <= n_seq * heads * 2.0 ** -15
+
+
 def test_queries_of_every_magnitude():
     """Rows from subnormal to huge, zeros, and elements 2^40 apart in one row."""
     rng = np.random.default_rng(19)
