@@ -646,7 +646,7 @@ __device__ __forceinline__ uint32_t unit_of(const PoolView &p, int32_t page, int
 
 constexpr int kStages = 3;
 
-// The bits of the largest scale of V over a warp's units (U at a time, from t0)
+// The bits of the largest scale of V (whatever its sign: a pool's own are positive) over a warp's units (U at a time, from t0)
 // with positions from `lo` on and before t_end, of a length of n positions.
 template <int G, int U>
 __device__ __forceinline__ uint32_t largest_scale(const PoolView &p, const int32_t *pages, int h, int t0, int lo,
@@ -661,7 +661,7 @@ __device__ __forceinline__ uint32_t largest_scale(const PoolView &p, const int32
         const uint16_t *at = p.vs + (uint64_t)unit * kUnit * G;
         const int count = min(kUnit, n - t) * G;
 #pragma unroll 1
-        for (int k = 0; k < count; ++k) most = max(most, (uint32_t)at[k]);
+        for (int k = 0; k < count; ++k) most = max(most, at[k] & 0x7FFFu);
     }
     return __reduce_max_sync(0xffffffffu, most);
 }
@@ -735,15 +735,16 @@ struct UnitRing {
         const uint32_t u = __shfl_sync(0xffffffffu, looked_ahead(i) ? before : units, f);
         return u == kNoUnit ? u : u & ~kSpecial;
     }
-    // The bits of the largest scale of V of step 0's entries, whose stage is waited
+    // The bits of the largest scale of V, without its sign, of step 0's entries, whose stage is waited
     // for (vs: LaneOffsets), of a length of n positions.
     __device__ __forceinline__ uint32_t first_scales(int n, uint32_t vs) const {
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
         __syncwarp();
+        auto size = [](uint32_t x) { return __habs2(as_half2(x)); };
         if (__all_sync(0xffffffffu, lane >= U || !(units & kSpecial))) {  // whole units: 8 scales a lane
             const int piece = min(lane, U * 2 * G - 1), j = piece / (2 * G);
             const uint4 w = (Shared{first} + j * S::kBytes + S::vs + 16 * (piece - j * 2 * G)).get16();
-            const uint32_t b = as_bits(__hmax2(__hmax2(as_half2(w.x), as_half2(w.y)), __hmax2(as_half2(w.z), as_half2(w.w))));
+            const uint32_t b = as_bits(__hmax2(__hmax2(size(w.x), size(w.y)), __hmax2(size(w.z), size(w.w))));
             return __reduce_max_sync(0xffffffffu, max(b & 0xFFFFu, b >> 16));
         }
         uint32_t most = 0;
@@ -756,7 +757,7 @@ struct UnitRing {
                 load_halfwords<G>(w, Shared{first} + j * S::kBytes + S::vs + vs + i * 4 * 2 * G);
                 if ((lane & 3) + 4 * i < left)
 #pragma unroll
-                    for (int k = 0; k < (G + 1) / 2; ++k) most = max(most, max(w[k] & 0xFFFFu, w[k] >> 16));
+                    for (int k = 0; k < (G + 1) / 2; ++k) most = max(most, max(w[k] & 0x7FFFu, w[k] >> 16 & 0x7FFFu));
             }
         }
         return __reduce_max_sync(0xffffffffu, most);

@@ -457,6 +457,19 @@ def test_scores_a_few_steps_of_the_type_apart(heads, out_dtype, e):
     assert abs(float(g.mass.double().sum()) - n_seq * heads) <= n_seq * heads * 2.0 ** -15
 
 
+@pytest.mark.parametrize("size", [1.0, 1e-4, 1e3])
+@pytest.mark.parametrize("D", [64, 96, 256])
+def test_scales_of_either_sign(D, size):
+    """A caller's own pool may hold negative scales: the same output with the other sign."""
+    g, pages, q = _big(40, 700, 1, 4, D, 16, seed=8)
+    n = i32([700 - 17 * b for b in range(40)])
+    g.v_scales.copy_((g.v_scales.view(torch.float16) * size).view(torch.int16))
+    want = sp.spectra_attention_paged(g, pages, n, q)
+    g.v_scales.copy_((-g.v_scales.view(torch.float16)).view(torch.int16))
+    assert torch.equal(sp.spectra_attention_paged(g, pages, n, q), -want) and want.any()
+    sp.spectra_device_status()
+
+
 def test_queries_of_every_magnitude():
     """Rows from subnormal to huge, zeros, and elements 2^40 apart in one row."""
     rng = np.random.default_rng(19)
