@@ -666,14 +666,14 @@ typedef struct {
  * rounding, and what lies under FP16's normal range there is off by 2^-32 of
  * the largest weight (2^-29 of the largest weight times the largest of V's
  * scales); an FP32 output has no such rounding, but loses 2^-22 of a weight or
- * 2^-32 of the largest one.  A non-finite output (from a
- * non-finite q, or from V's entries beyond 65504 in magnitude, which FP16 does
- * not hold) is reported by spectra_device_status as RANGE.  Out of bounds
- * values are reported by spectra_device_status as INVALID_ARG and
- * touch nothing: a page id outside the pool hides its positions (one that no
- * row sees, behind a window, is not looked at), a length
- * outside [0, max_pages*page_size] counts as 0, and a sequence whose rows lie
- * outside [0, n_rows) or number more than max_q has its rows left as they
+ * 2^-32 of the largest one, and 2^-38 of a value under 2^-14.  A non-finite
+ * output (from a non-finite q, or from V's entries beyond 65504 in magnitude,
+ * which FP16 does not hold) is reported by spectra_device_status as RANGE.  Out
+ * of bounds values are reported by spectra_device_status as INVALID_ARG and touch
+ * nothing: a page id outside the pool hides its positions (one that no row
+ * sees, behind a window, is not looked at), a length outside [0,
+ * max_pages*page_size] counts as 0, and a sequence whose rows lie outside
+ * [0, n_rows) or number more than max_q has its rows left as they
  * were.  Sequences may share pages.  Deterministic (but for the mass of an
  * entry that several sequences of a call share, whose sums are added in any
  * order), asynchronous, allocates nothing, graph-capturable

@@ -35,7 +35,13 @@
 //     it.  (Without the power, values of 1e-5 lost 0.2 % of the largest output, and
 //     many light weights beside a heavy one far more.)  Where scales grow so far
 //     that a product passes FP16's range, which is seen in the sums, the item is
-//     run again with the power that the largest of all its scales wants;
+//     run again with the power that the largest of all its scales wants.
+//     The tensor core lines an instruction's products up at their exponents, of which
+//     a subnormal's counts as 2^-14 (by its results), and cuts off 24 bits under the
+//     largest: 2^-14 of a code's step times the largest query value (K), or times the
+//     unit's largest weight (V).  For K that shows where a query value is a thousand times the
+//     others (one of 3000 beside ones of 1: outputs off by 4.6e-5, in FP32
+//     arithmetic 1.5e-5; of 300 both 1e-6), for V it is under a BF16 output's step;
 //   less the zero point (16 columns and more, and V for an FP32 output): a nibble
 //     or-ed under 0x6400 is 1024 + c, or 1024 + 16c where it stands, and one
 //     half-precision instruction takes it to c - z, exactly.  V is dequantised to
@@ -47,7 +53,7 @@
 // output's own, and for a weight under FP16's normal range 2^-25, which is 2^-32
 // of the largest.  For an FP32 output what the two roundings left goes in as
 // well, as two more products (V's remainder is exact; of the weights 2^-22 is
-// lost, or 2^-32 of the largest), and each unit's sum is added to the accumulator
+// lost, or 2^-32 of the largest; of values under 2^-14 2^-38, as above), and each unit's sum is added to the accumulator
 // in FP32: the tensor core cuts its sums off (error at 8192 positions 1.4e-6 of
 // the largest output, with the separate addition 2.4e-7).
 //
@@ -73,16 +79,21 @@
 // kernel, launched as a programmatic dependent, joins them in order.  Every order
 // is fixed, so results repeat bit for bit.
 //
-// Measured (B200; positions of a batch, Hq / H heads, D channels):
+// Measured (B200, in a graph; positions of a batch, Hq / H heads, D channels):
 //   16 sequences of 20000 to 65536 positions, 32 / 8, 128, one new token: 862 MB in
-//     188 us, 4.6 TB/s, against 134 us at the rate of a copy.  The ring alone,
-//     without the arithmetic, runs at 6.05 TB/s.  The unit's instructions bound it
-//     (some 185 of the integer and half-precision kind per unit and warp at G = 4),
-//     and the chip is at its power limit, 1.8 GHz;
-//   1 sequence of 8192, 12 / 2, 128: 10.1 us; of 300: 8.7 us, which is the two
+//     191 us, 4.5 TB/s, against 134 us at the rate of a copy (over a second and
+//     more of such calls 195 to 205 us: the clock falls to the power limit).  The ring
+//     alone, without the arithmetic, runs at 6.05 TB/s.  No pipe is full (189 MB of
+//     such sequences: integer 48 %, matrix 27 %, half of the issue slots): a warp waits
+//     on its own chain from code to operand, product and weight, at 1.8 GHz; how
+//     the time over the copy divides between the chain and the clock is open;
+//   1 sequence of 8192, 12 / 2, 128: 10.4 us; of 300: 9.2 us, which is the two
 //     launches, the run search, the ring's first fill and the join.
 // Tried and no faster: 4 to 6 CTAs an SM with one unit a step, 4 ring steps, the
 // queries' operands in shared memory for 8 columns, 16 columns a tile where 32 fit.
+// The power of V's scales: found at each step 217 us instead of 202 in a loop of the
+// first case, multiplied in always (also by 1) 184 instead of 178 on a like pool; so
+// it is found once per item and the loop exists twice, with it and without.
 #include <type_traits>
 
 #include "internal.cuh"
@@ -154,7 +165,10 @@ __device__ __forceinline__ Sequence sequence_of(const PagedArgs &a, int b) {
 // visible position, and before them as many as make 256 positions, which stand
 // for the time an item takes whatever its length.  (Without them the runs of
 // short items came last: 48 sequences of 1 to 6000 positions took 68 us; with
-// 128, 256, 384 and 768 positions 60, 51, 51 and 55 us.)
+// 128, 256, 384 and 768 positions 60, 51, 51 and 55 us.)  Every column tile lists the
+// whole sequence's tiles, those after its own last row's position too, which cost
+// nothing when their run comes to them: of a whole prompt half the list is empty,
+// and the runs over the last column tiles set the time.
 template <int U>
 constexpr int kItemCost = 256 / kTile<U>;
 struct Tiles {
@@ -291,8 +305,8 @@ struct Shared {
 
 // N 32-bit words, or N halfwords in (N + 1) / 2 words, with the widest loads
 // that their alignment (the size's own) allows.
-template <int N, class P>
-__device__ __forceinline__ void load_words(uint32_t (&r)[N], P p) {
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&r)[N], Shared p) {
     if constexpr (N % 4 == 0) {
 #pragma unroll
         for (int i = 0; i < N; i += 4) {
@@ -310,8 +324,8 @@ __device__ __forceinline__ void load_words(uint32_t (&r)[N], P p) {
         for (int i = 0; i < N; ++i) r[i] = (p + 4 * i).get4();
     }
 }
-template <int N, class P>
-__device__ __forceinline__ void load_halfwords(uint32_t (&r)[(N + 1) / 2], P p) {
+template <int N>
+__device__ __forceinline__ void load_halfwords(uint32_t (&r)[(N + 1) / 2], Shared p) {
     if constexpr (N % 2 == 0) {
         load_words<N / 2>(r, p);
     } else {
@@ -411,9 +425,8 @@ struct KUnit {
     uint32_t w[2][G];
     uint32_t s[2][(G + 1) / 2];
     uint32_t z[2];
-    // From the lane's places in a stage, or in the pool.
-    template <class P>
-    __device__ __forceinline__ void load(P kc, P ks, P kz) {
+    // From the lane's places in a stage.
+    __device__ __forceinline__ void load(Shared kc, Shared ks, Shared kz) {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {  // unit_position(g + 8) = unit_position(g) + 8
             load_words<G>(w[r], kc + r * 8 * 16 * G);
@@ -853,6 +866,10 @@ template <int G, int NT>
 constexpr int units_per_step() {
     return G * NT <= 4 ? 2 : 1;
 }
+// (Three CTAs an SM where two would have registers to spare: under the bound FP32
+// decode keeps 312 bytes a thread in local memory at D = 256 and 108 at 224, BF16
+// decode 160 and 68, the other forms 60 or less, but 116 at D = 32 with 32 columns; the
+// join of few pieces 8 to 104.)
 template <int G, int NT>
 constexpr int min_ctas() {
     return G * NT <= 8 ? 3 : 2;
@@ -1259,7 +1276,7 @@ __global__ void __launch_bounds__(kThreads, min_ctas<G, NT>()) paged_attention_k
 // CTA takes a column, its threads the pieces side by side, and the first loads of
 // the sums do not wait for the weights.  LONG: for few items in many runs, the
 // second form alone (a smaller kernel starts sooner: 1 sequence of 300 positions
-// 8.6 us instead of 9.9 with both).  Bound by its launch and the trips to L2.
+// takes 1.3 us less than with both).  Bound by its launch and the trips to L2.
 constexpr int kJoinThreads = 128, kFewPieces = 4;
 template <int G, int NT, bool EXACT, bool LONG>
 __global__ void __launch_bounds__(kJoinThreads, LONG ? 7 : 8) paged_join_kernel(const PagedArgs a) {
@@ -1382,15 +1399,19 @@ __global__ void __launch_bounds__(kJoinThreads, LONG ? 7 : 8) paged_join_kernel(
     }
 }
 
-// The accumulated weights, a second pass over K alone with the rows' sums (the
-// weights need the whole row's sum; keeping a row's scores for it would write and
-// read 4 bytes per query head and position, where K is read again for D / 2 + D /
-// 16 per KV head): a warp per unit, 8 columns at a time.  A position's sum over
-// the columns is formed in one warp, in order; it is added to the mass
+// The accumulated weights, a second pass over K alone with the rows' sums (a
+// weight needs the whole row's): a warp per unit, 8 columns at a time.  A position's
+// sum over the columns is formed in one warp, in order; it is added to the mass
 // atomically, for the pages that several sequences share.  (Where they do, the
 // order of those additions, and so the last bit, may differ from run to run.)
+// Keeping the first pass's scores instead would move fewer bytes up to 8 query heads
+// per KV head (8 bytes a head and position, written and read, against K's D / 2 + D /
+// 16 + 4 = 76 at D = 128), and would spare the products; it is not built.  With more
+// columns the pass walks K once per 8 of them.
 // Measured with the attention before it: 48 sequences of 1 to 6000 positions, 32 /
-// 8 heads of 128 channels, 189 MB in 82 us; bound by the same instructions.
+// 8 heads of 128 channels, 189 MB in 85 us, 33 of them this pass; 12 of 40 to 7001 with 16
+// tokens (8 walks) 162 us, 83 more than without; a prompt of 2048 tokens (1024 walks)
+// 2.2 ms, 1.8 of them this pass.
 template <int G>
 __global__ void __launch_bounds__(kThreads, G <= 4 ? 4 : 3) paged_mass_kernel(const PagedArgs a) {
     constexpr int D = 32 * G, U = units_per_step<G, 1>();

@@ -223,8 +223,8 @@ __global__ void __launch_bounds__(256) pool_append_kernel(PoolView p, const uint
 }
 
 // Token slots dequantised, four threads to a vector as above.  Bound by the
-// writes: 36000 tokens of 8 heads of 128 to BF16 in 31 us, 44 MB of records read
-// and 147 written.
+// writes: 36000 tokens of 8 heads of 128 to BF16 in 32 us, 44 MB of records read
+// and 147 written; to FP32 in 77 us, 295 written.
 template <int G, bool BF16>
 __global__ void __launch_bounds__(256) pool_read_kernel(PoolView p, const int32_t *__restrict__ slots,
                                                         uint32_t n_vectors, void *__restrict__ k_out,

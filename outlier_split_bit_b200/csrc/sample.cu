@@ -31,7 +31,8 @@
 // end 3), where the row's bytes would take 0.1.  64 rows of 131071, top-p and
 // min-p: 57 us against 5 for the bytes: every weight in reach is an exponential in
 // FP64 (some 12 FP64 instructions) and two shared atomics, of which the one and
-// the other take about half.  By counts alone (top-k 50): 25 us.
+// the other take about half.  By counts alone (top-k 50): 25 us.  Without filters 37 us
+// (1 row 16), greedy 10 (1 row 5.5).
 #include <cooperative_groups.h>
 
 #include <utility>
