@@ -672,9 +672,17 @@ __device__ __forceinline__ uint32_t largest_scale(const PoolView &p, const int32
         const uint32_t unit = unit_of(p, pages[t >> p.lp], t, h);
         if (unit == kNoUnit) continue;
         const uint16_t *at = p.vs + (uint64_t)unit * kUnit * G;
-        const int count = min(kUnit, n - t) * G;
-#pragma unroll 1
-        for (int k = 0; k < count; ++k) most = max(most, at[k] & 0x7FFFu);
+        const int count = min(kUnit, n - t) * G;  // (of what lies behind them nothing counts)
+#pragma unroll 4
+        for (int k = 0; k < 2 * G; ++k) {
+            const uint4 w4 = reinterpret_cast<const uint4 *>(at)[k];
+            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (8 * k + 2 * e < count) most = max(most, w[e] & 0x7FFFu);
+                if (8 * k + 2 * e + 1 < count) most = max(most, w[e] >> 16 & 0x7FFFu);
+            }
+        }
     }
     return __reduce_max_sync(0xffffffffu, most);
 }
@@ -868,7 +876,7 @@ constexpr int units_per_step() {
 }
 // (Three CTAs an SM where two would have registers to spare: under the bound FP32
 // decode keeps 312 bytes a thread in local memory at D = 256 and 108 at 224, BF16
-// decode 160 and 68, the other forms 60 or less, but 116 at D = 32 with 32 columns; the
+// decode 156 and 64, the other forms 60 or less, but 116 at D = 32 with 32 columns; the
 // join of few pieces 8 to 104.)
 template <int G, int NT>
 constexpr int min_ctas() {
