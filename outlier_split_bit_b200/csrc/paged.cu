@@ -659,8 +659,9 @@ __device__ __forceinline__ uint32_t unit_of(const PoolView &p, int32_t page, int
 
 constexpr int kStages = 3;
 
-// The bits of the largest scale of V (whatever its sign: a pool's own are positive) over a warp's units (U at a time, from t0)
-// with positions from `lo` on and before t_end, of a length of n positions.
+// The bits of the largest scale of V, without its sign (a pool's own are positive),
+// over a warp's units (U at a time, from t0) with positions from `lo` on and before
+// t_end, of a length of n positions.
 template <int G, int U>
 __device__ __forceinline__ uint32_t largest_scale(const PoolView &p, const int32_t *pages, int h, int t0, int lo,
                                                   int t_end, int n) {
